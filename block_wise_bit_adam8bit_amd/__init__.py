@@ -17,12 +17,13 @@ from .functional import (  # noqa: F401
     qopt_quantize_blockwise, qopt_dequantize_blockwise, qopt_adam8bit_step,
     qopt_adam8bit_launch_count, qopt_adam8bit_traffic_probe, qopt_quantize_blockwise_multi,
     qopt_dequantize_blockwise_multi, make_tensor_array, qopt_pattern_probe,
-    qopt_pattern_probe_names,
+    qopt_pattern_probe_names, AdamWPlan, qopt_adamw8bit_plan, qopt_adamw32bit_plan,
+    qopt_adamw8bit_step, qopt_adamw32bit_step,
 )
 from .checkpoint import (  # noqa: F401
     compress_moments, decompress_moments, compress_moments_multi, decompress_moments_multi,
 )
-from .optim import Adam8bit  # noqa: F401
+from .optim import Adam8bit, AdamW  # noqa: F401
 from .embedding import (  # noqa: F401
     StableEmbedding, StableEmbeddingFunction, qopt_embedding_xavier_init,
     qopt_stable_embedding_forward, qopt_stable_embedding_backward,

@@ -71,12 +71,33 @@ class qopt_codec_tensor(ctypes.Structure):
     ]
 
 
+class qopt_tensor32(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+    ]
+
+
 class qopt_adam_hparams(ctypes.Structure):
     _fields_ = [
         ("lr", ctypes.c_float),
         ("beta1", ctypes.c_float),
         ("beta2", ctypes.c_float),
         ("eps", ctypes.c_float),
+        ("step", ctypes.c_int64),
+    ]
+
+
+class qopt_adamw_hparams(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_float),
+        ("beta1", ctypes.c_float),
+        ("beta2", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
         ("step", ctypes.c_int64),
     ]
 
@@ -98,6 +119,14 @@ _SIGNATURES = {
                                           ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.POINTER(qopt_adam_hparams),
                                           ctypes.c_void_p]),
+    "qopt_adamw8bit_step": (ctypes.c_int, [ctypes.POINTER(qopt_tensor), ctypes.c_int32,
+                                           ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.POINTER(qopt_adamw_hparams),
+                                           ctypes.c_void_p, ctypes.c_void_p]),
+    "qopt_adamw32bit_step": (ctypes.c_int, [ctypes.POINTER(qopt_tensor32), ctypes.c_int32,
+                                            ctypes.c_int, ctypes.c_int,
+                                            ctypes.POINTER(qopt_adamw_hparams), ctypes.c_void_p,
+                                            ctypes.c_void_p]),
     "qopt_adam8bit_launch_count": (ctypes.c_int, [ctypes.POINTER(qopt_tensor), ctypes.c_int32,
                                                   ctypes.c_int, ctypes.c_int,
                                                   ctypes.POINTER(ctypes.c_int64)]),

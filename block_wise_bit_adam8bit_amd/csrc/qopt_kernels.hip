@@ -252,6 +252,7 @@ __device__ __forceinline__ uint32_t piece_of(const uint32_t* block_start, uint32
 // One codec launch's work: up to kMaxTensors pieces, each a run of whole blocks of
 // one tensor (the same plan as the step's, see plan_chunks).
 struct CodecChunk {
+  static constexpr int kMax = kMaxTensors;
   float* vals[kMaxTensors];               // quantize: input; dequantize: output
   uint8_t* codes[kMaxTensors];
   float* absmax[kMaxTensors];
@@ -472,6 +473,25 @@ struct AdamScalars {
   float short_a, short_b, t_limit;
 };
 
+// An AdamW step's scalars: those of the Adam step, the decoupled weight decay's factor
+// decay = fl32(1 - lr wd), applied to the parameter before the update, and the factor of
+// the gradients, read from device memory when the kernel starts (1 without one).
+struct AdamWScalars : AdamScalars {
+  float decay;
+  float gscale;
+  const float* grad_scale;
+};
+
+// The scalars as the kernel uses them, and the two places where AdamW differs.
+__device__ __forceinline__ void load_grad_scale(AdamScalars&) {}
+__device__ __forceinline__ void load_grad_scale(AdamWScalars& k) {
+  k.gscale = k.grad_scale ? *k.grad_scale : 1.0f;
+}
+__device__ __forceinline__ float scaled_grad(const AdamScalars&, float g) { return g; }
+__device__ __forceinline__ float scaled_grad(const AdamWScalars& k, float g) { return g * k.gscale; }
+__device__ __forceinline__ float decayed(const AdamScalars&, float p) { return p; }
+__device__ __forceinline__ float decayed(const AdamWScalars& k, float p) { return p * k.decay; }
+
 // How bf16 parameters use the screened short path (fp32 parameters never do):
 // not at all, or screened, or screened with slices holding a subnormal second
 // moment sent to the correctly rounded sequence as well.
@@ -536,6 +556,7 @@ template <uint32_t kRun> struct StepWalk {
 // tensor.  Large tensors may be split over several launches so that every launch
 // of a step covers the same number of blocks.
 struct StepChunk {
+  static constexpr int kMax = kMaxTensors;
   void* param[kMaxTensors];             // tensor base pointers
   const void* grad[kMaxTensors];
   uint8_t* m_codes[kMaxTensors];
@@ -582,8 +603,11 @@ template <> __device__ __forceinline__ void store1<uint16_t>(uint16_t* p, int i,
 }
 
 // One element of the update; returns the new parameter, leaves m and v.
-__device__ __forceinline__ float adam_element(const AdamScalars& k, float p, float g, float m_prev,
+template <typename K>
+__device__ __forceinline__ float adam_element(const K& k, float p, float g, float m_prev,
                                               float v_prev, float& m, float& v) {
+  p = decayed(k, p);
+  g = scaled_grad(k, g);
   m = (k.b1 * m_prev) + (k.omb1 * g);
   v = (k.b2 * v_prev) + (k.omb2 * (g * g));
   const float denom = (sqrtf(v) * k.inv_sqrt_bc2) + k.eps;
@@ -756,8 +780,8 @@ __device__ __forceinline__ void unstash_v(const float* vstash, int s, int lane, 
 // Update of a full block from prefetched vector inputs; stores p, keeps m and v
 // (v in the LDS stash where StepShape says so).  Where the step rolls (step_rolls),
 // slice s of block nr is loaded into `in` as soon as slice s of this block is used up.
-template <typename PT, typename GT, int kMode>
-__device__ __forceinline__ void update_vec(const AdamScalars& k, const qopt_codebook& cbm,
+template <typename PT, typename GT, int kMode, typename K>
+__device__ __forceinline__ void update_vec(const K& k, const qopt_codebook& cbm,
                                            const qopt_codebook& cbv, BlockIn<PT, GT>& in,
                                            const BlockRef& r, const BlockRef& nr, int lane,
                                            float m[kSlices][4], float v[kSlices][4], float* vstash,
@@ -769,6 +793,11 @@ __device__ __forceinline__ void update_vec(const AdamScalars& k, const qopt_code
     float p4[4], g4[4];
     unpack4(in.p[s], p4);
     unpack4(in.g[s], g4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p4[j] = decayed(k, p4[j]);
+      g4[j] = scaled_grad(k, g4[j]);
+    }
     constexpr bool kScreened = std::is_same<PT, uint16_t>::value && kMode != kNoScreen;
     // the moments of the slice's 4 elements; where the correctly rounded sequence
     // runs, its square roots skip sqrtf's rescaling of tiny inputs unless some lane of
@@ -862,8 +891,8 @@ __device__ __forceinline__ void update_vec(const AdamScalars& k, const qopt_code
 
 // Update of a short block, or of a tensor without vector alignment: element-wise
 // accesses guarded by the block length; elements past it hold m = v = 0.
-template <typename PT, typename GT>
-__device__ __forceinline__ void update_scalar(const AdamScalars& k, const qopt_codebook& cbm,
+template <typename PT, typename GT, typename K>
+__device__ __forceinline__ void update_scalar(const K& k, const qopt_codebook& cbm,
                                               const qopt_codebook& cbv, const BlockRef& r,
                                               int lane, float m[kSlices][4], float v[kSlices][4],
                                               float* vstash, float& mmax, float& vmax) {
@@ -967,12 +996,14 @@ __device__ __forceinline__ void requantize(const Encoder& em, const Encoder& ev,
 // block, the vector inputs of its next block are already in flight: loaded into the
 // registers the update no longer needs, slice by slice during the update where the
 // step rolls (step_rolls), else all at once after it.
-template <typename PT, typename GT, int kMode>
+// K: AdamScalars, or AdamWScalars for the step with weight decay and scaled gradients.
+template <typename PT, typename GT, int kMode, typename K>
 __global__ void __launch_bounds__(kThreads, (step_waves<PT, kMode>()))
-adam8bit_kernel(StepChunk c, AdamScalars k, const qopt_codebook* cbm_g, const qopt_codebook* cbv_g) {
+adam8bit_kernel(StepChunk c, K k, const qopt_codebook* cbm_g, const qopt_codebook* cbv_g) {
   constexpr bool kVInLds = StepShape<PT>::kVInLds;
   __shared__ __align__(16) qopt_codebook cb[2];
   __shared__ __align__(16) float vstash_all[kVInLds ? kWaves * QOPT_BLOCK : 4];
+  load_grad_scale(k);
   stage_codebook(&cb[0], cbm_g);
   stage_codebook(&cb[1], cbv_g);
   __syncthreads();
@@ -1096,6 +1127,88 @@ __global__ void __launch_bounds__(kThreads) step_traffic_kernel(StepChunk c) {
   }
 }
 
+// ------------------------------------------------- AdamW with 32-bit moments
+
+// One launch's work, as StepChunk: fp32 moments instead of codes and block maxima.
+struct Step32Chunk {
+  static constexpr int kMax = 64;         // pieces per launch (kernarg budget, piece_of's depth)
+  void* param[kMax];
+  const void* grad[kMax];
+  float* m[kMax];
+  float* v[kMax];
+  int64_t n[kMax];
+  uint32_t block_lo[kMax];
+  uint32_t block_start[kMax + 1];
+  uint32_t npieces;
+  uint64_t vector_ok;
+};
+
+// One AdamW update with fp32 moments: per element the arithmetic of adam8bit_kernel's
+// exact path, the moments read and written as they are.  Pure streaming: a wave takes
+// one run of 2048 consecutive elements at a time and has all of its loads in flight
+// before it uses the first.
+template <typename PT, typename GT>
+__global__ void __launch_bounds__(kThreads) adamw32_kernel(Step32Chunk c, AdamWScalars k) {
+  typedef typename Vec4T<PT>::type PV;
+  typedef typename Vec4T<GT>::type GV;
+  load_grad_scale(k);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x % kWave;
+  const uint32_t total = c.block_start[c.npieces];
+  for (uint32_t blk = blockIdx.x * kWaves + wave; blk < total; blk += gridDim.x * kWaves) {
+    const uint32_t t = piece_of(c.block_start, c.npieces, blk);
+    const int64_t base = static_cast<int64_t>(c.block_lo[t] + (blk - c.block_start[t])) * QOPT_BLOCK;
+    const int64_t rem = c.n[t] - base;
+    PT* pb = static_cast<PT*>(c.param[t]) + base;
+    const GT* gb = static_cast<const GT*>(c.grad[t]) + base;
+    float* mb = c.m[t] + base;
+    float* vb = c.v[t] + base;
+    if (rem >= QOPT_BLOCK && ((c.vector_ok >> t) & 1u)) {
+      PV* p = reinterpret_cast<PV*>(pb) + lane;
+      const GV* g = reinterpret_cast<const GV*>(gb) + lane;
+      f32x4* m = reinterpret_cast<f32x4*>(mb) + lane;
+      f32x4* v = reinterpret_cast<f32x4*>(vb) + lane;
+      PV P[kSlices];
+      GV G[kSlices];
+      f32x4 M[kSlices], V[kSlices];
+#pragma unroll
+      for (int s = 0; s < kSlices; ++s) {
+        P[s] = ld_wide(p + s * kWave);
+        G[s] = ld_wide(g + s * kWave);
+        M[s] = ld_wide(m + s * kWave);
+        V[s] = ld_wide(v + s * kWave);
+      }
+#pragma unroll
+      for (int s = 0; s < kSlices; ++s) {
+        float p4[4], g4[4], m4[4], v4[4];
+        unpack4(P[s], p4);
+        unpack4(G[s], g4);
+        unpack4(M[s], m4);
+        unpack4(V[s], v4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p4[j] = adam_element(k, p4[j], g4[j], m4[j], v4[j], m4[j], v4[j]);
+        PV pv;
+        f32x4 mv, vv;
+        pack4(p4, pv);
+        pack4(m4, mv);
+        pack4(v4, vv);
+        st_wide(p + s * kWave, pv);
+        st_wide(m + s * kWave, mv);
+        st_wide(v + s * kWave, vv);
+      }
+    } else {
+      const int len = rem < QOPT_BLOCK ? static_cast<int>(rem) : QOPT_BLOCK;
+      for (int e = lane; e < len; e += kWave) {
+        float m = mb[e], v = vb[e];
+        const float p = adam_element(k, load1<PT>(pb, e), load1<GT>(gb, e), m, v, m, v);
+        store1<PT>(pb, e, p);
+        mb[e] = m;
+        vb[e] = v;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ host helpers
 
 struct DeviceInfo {
@@ -1181,7 +1294,7 @@ double pow_by_squaring(double b, int64_t t) {
 bool finite(float x) { return x == x && x - x == 0.0f; }
 
 // Splits a list of tensors into launches of equal block counts (the last may be
-// shorter), each holding at most kMaxTensors pieces; a piece is a run of whole blocks
+// shorter), each holding at most Chunk::kMax pieces; a piece is a run of whole blocks
 // of one tensor.  For a given launch count the pieces are assigned greedily in
 // tensor order.  size_of(i) gives tensor i's length; fill(chunk, slot, i) writes its
 // pointers and length into the slot and says whether it may take the vector path;
@@ -1202,7 +1315,7 @@ int plan_chunks(int32_t ntensors, const SizeOf& size_of, const Fill& fill, uint6
     const uint64_t nb = (static_cast<uint64_t>(n) + QOPT_BLOCK - 1) / QOPT_BLOCK;
     uint64_t lo = 0;
     while (lo < nb) {
-      if (c.npieces == static_cast<uint32_t>(kMaxTensors)) {
+      if (c.npieces == static_cast<uint32_t>(Chunk::kMax)) {
         *fits = false;
         return QOPT_OK;
       }
@@ -1243,12 +1356,13 @@ constexpr uint64_t kCodecLongLaunchBlocks = uint64_t{1} << 16;
 
 template <typename Chunk> uint64_t launch_block_cap(uint64_t total);
 template <> uint64_t launch_block_cap<StepChunk>(uint64_t) { return kMaxLaunchBlocks; }
+template <> uint64_t launch_block_cap<Step32Chunk>(uint64_t) { return kMaxLaunchBlocks; }
 template <> uint64_t launch_block_cap<CodecChunk>(uint64_t total) {
   return total > kMaxLaunchBlocks ? kCodecLongLaunchBlocks : kMaxLaunchBlocks;
 }
 
 // Launch count of the plan: the smallest count (from the piece and block bounds up)
-// whose greedy assignment keeps every launch within kMaxTensors pieces and the block
+// whose greedy assignment keeps every launch within Chunk::kMax pieces and the block
 // bound of launch_block_cap.
 template <typename Chunk, typename SizeOf, typename Fill>
 int count_chunks(int32_t ntensors, const SizeOf& size_of, const Fill& fill,
@@ -1265,7 +1379,7 @@ int count_chunks(int32_t ntensors, const SizeOf& size_of, const Fill& fill,
   *total_out = total;
   *nchunks_out = 0;
   if (total == 0) return QOPT_OK;
-  uint64_t nchunks = (pieces + kMaxTensors - 1) / kMaxTensors;
+  uint64_t nchunks = (pieces + Chunk::kMax - 1) / Chunk::kMax;
   const uint64_t cap = launch_block_cap<Chunk>(total);
   const uint64_t by_size = (total + cap - 1) / cap;
   if (nchunks < by_size) nchunks = by_size;
@@ -1287,7 +1401,18 @@ int count_chunks(int32_t ntensors, const SizeOf& size_of, const Fill& fill,
 // the call.  The launches touch disjoint blocks, so their order does not matter.
 // Measured in one process on the same buffers: the 20B bf16 step (38 launches)
 // 4.8-5.8 % faster (three processes); the fp32-parameter steps 1-1.6 % slower, so they
-// keep one stream.
+// keep one stream.  A stream under graph capture keeps one stream too: the second stream
+// is shared by every caller on the device, and drawing it into one caller's capture would
+// put another caller's eager launches into that graph.
+bool capturing(hipStream_t stream) {
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
+    (void)hipGetLastError();  // the query's own error: launch_status must not report it
+    return true;
+  }
+  return st != hipStreamCaptureStatusNone;
+}
+
 template <typename Chunk, bool kFork = false, typename Kernel, typename SizeOf, typename Fill,
           typename... Args>
 int launch_planned(Kernel kernel, int cap, uint32_t run, int32_t ntensors, const SizeOf& size_of,
@@ -1297,7 +1422,7 @@ int launch_planned(Kernel kernel, int cap, uint32_t run, int32_t ntensors, const
   if (rc != QOPT_OK || total == 0) return rc;
   hipStream_t second = stream;
   hipEvent_t before = nullptr, after = nullptr;
-  const bool fork = kFork && nchunks > 1;
+  const bool fork = kFork && nchunks > 1 && !capturing(stream);
   if (fork) {
     rc = side_stream(&second);
     if (rc != QOPT_OK) return rc;
@@ -1360,6 +1485,26 @@ struct StepSize {
   int64_t operator()(int32_t i) const { return t[i].n; }
 };
 
+struct Step32Fill {
+  const qopt_tensor32* t;
+  size_t psize, gsize;
+  bool operator()(Step32Chunk& c, uint32_t slot, int32_t i) const {
+    const qopt_tensor32& x = t[i];
+    c.param[slot] = x.param;
+    c.grad[slot] = x.grad;
+    c.m[slot] = x.m;
+    c.v[slot] = x.v;
+    c.n[slot] = x.n;
+    return aligned(x.param, 4 * psize) && aligned(x.grad, 4 * gsize) && aligned(x.m, 16) &&
+           aligned(x.v, 16);
+  }
+};
+
+struct Step32Size {
+  const qopt_tensor32* t;
+  int64_t operator()(int32_t i) const { return t[i].n; }
+};
+
 struct CodecFill {
   const qopt_codec_tensor* t;
   bool operator()(CodecChunk& c, uint32_t slot, int32_t i) const {
@@ -1377,19 +1522,19 @@ struct CodecSize {
   int64_t operator()(int32_t i) const { return t[i].n; }
 };
 
-template <typename PT, typename GT, int kMode>
+template <typename PT, typename GT, int kMode, typename K>
 int launch_step_mode(const qopt_tensor* tensors, int32_t ntensors, size_t psize, size_t gsize,
-                     const AdamScalars& k, const qopt_codebook* cbm, const qopt_codebook* cbv,
+                     const K& k, const qopt_codebook* cbm, const qopt_codebook* cbv,
                      hipStream_t stream) {
   return launch_planned<StepChunk, std::is_same<PT, uint16_t>::value>(
-      adam8bit_kernel<PT, GT, kMode>, 0, step_run<PT, GT>(), ntensors, StepSize{tensors},
+      adam8bit_kernel<PT, GT, kMode, K>, 0, step_run<PT, GT>(), ntensors, StepSize{tensors},
       StepFill{tensors, psize, gsize}, stream, k, cbm, cbv);
 }
 
 // mode: a ScreenMode, which only bf16 parameters use.
-template <typename PT, typename GT>
+template <typename PT, typename GT, typename K>
 int launch_step_chunks(const qopt_tensor* tensors, int32_t ntensors, size_t psize, size_t gsize,
-                       const AdamScalars& k, int mode, const qopt_codebook* cbm,
+                       const K& k, int mode, const qopt_codebook* cbm,
                        const qopt_codebook* cbv, hipStream_t stream) {
   if constexpr (std::is_same<PT, uint16_t>::value) {
     if (mode == kScreen)
@@ -1399,6 +1544,34 @@ int launch_step_chunks(const qopt_tensor* tensors, int32_t ntensors, size_t psiz
                                                        stream);
   }
   return launch_step_mode<PT, GT, kNoScreen>(tensors, ntensors, psize, gsize, k, cbm, cbv, stream);
+}
+
+template <typename PT, typename GT>
+int launch_step32(const qopt_tensor32* tensors, int32_t ntensors, const AdamWScalars& k,
+                  hipStream_t stream) {
+  return launch_planned<Step32Chunk>(adamw32_kernel<PT, GT>, 0, 1, ntensors, Step32Size{tensors},
+                                     Step32Fill{tensors, sizeof(PT), sizeof(GT)}, stream, k);
+}
+
+int check_step32_tensors(const qopt_tensor32* tensors, int32_t ntensors, int param_dtype,
+                         int grad_dtype, bool* any) {
+  if (ntensors < 0) return QOPT_EINVAL;
+  if (ntensors > 0 && tensors == nullptr) return QOPT_EINVAL;
+  if ((param_dtype != QOPT_F32 && param_dtype != QOPT_BF16) ||
+      (grad_dtype != QOPT_F32 && grad_dtype != QOPT_BF16))
+    return QOPT_EUNSUPPORTED;
+  *any = false;
+  for (int32_t i = 0; i < ntensors; ++i) {
+    const qopt_tensor32& t = tensors[i];
+    if (t.n < 0) return QOPT_EINVAL;
+    if (t.n == 0) continue;
+    *any = true;
+    if (!t.param || !t.grad || !t.m || !t.v) return QOPT_EINVAL;
+    if (!aligned(t.param, param_dtype == QOPT_F32 ? 4 : 2) ||
+        !aligned(t.grad, grad_dtype == QOPT_F32 ? 4 : 2) || !aligned(t.m, 4) || !aligned(t.v, 4))
+      return QOPT_EALIGN;
+  }
+  return QOPT_OK;
 }
 
 int check_step_tensors(const qopt_tensor* tensors, int32_t ntensors, int param_dtype,
@@ -1506,33 +1679,24 @@ extern "C" int qopt_dequantize_blockwise(const qopt_codebook* cb_dev, const uint
   return codec_multi(dequantize_kernel, 0, cb_dev, &t, 1, stream);
 }
 
-extern "C" int qopt_adam8bit_step(const qopt_tensor* tensors, int32_t ntensors, int param_dtype,
-                                  int grad_dtype, const qopt_codebook* cb_m_dev,
-                                  const qopt_codebook* cb_v_dev, const qopt_adam_hparams* hp,
-                                  void* stream) {
-  if (hp == nullptr) return QOPT_EINVAL;
-  bool any = false;
-  int rc = check_step_tensors(tensors, ntensors, param_dtype, grad_dtype, &any);
-  if (rc != QOPT_OK) return rc;
-  if (!finite(hp->lr) || !finite(hp->eps) || hp->eps < 0.0f) return QOPT_EINVAL;
-  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
-    return QOPT_EINVAL;
-  if (hp->step < 1) return QOPT_EINVAL;
-  if (!any) return QOPT_OK;
-  if (!cb_m_dev || !cb_v_dev) return QOPT_EINVAL;
-  if (!aligned(cb_m_dev, 16) || !aligned(cb_v_dev, 16)) return QOPT_EALIGN;
-  const size_t psize = param_dtype == QOPT_F32 ? 4 : 2;
-  const size_t gsize = grad_dtype == QOPT_F32 ? 4 : 2;
+namespace {
 
-  AdamScalars k;
-  k.b1 = hp->beta1;
-  k.b2 = hp->beta2;
-  k.omb1 = 1.0f - hp->beta1;
-  k.omb2 = 1.0f - hp->beta2;
-  k.eps = hp->eps;
-  const double bc1 = 1.0 - pow_by_squaring(static_cast<double>(hp->beta1), hp->step);
-  const double bc2 = 1.0 - pow_by_squaring(static_cast<double>(hp->beta2), hp->step);
-  k.step_size = static_cast<float>(static_cast<double>(hp->lr) / bc1);
+// What both kinds of step ask of their hyper-parameters.
+bool bad_hparams(float lr, float beta1, float beta2, float eps, int64_t step) {
+  return !finite(lr) || !finite(eps) || eps < 0.0f || !(beta1 >= 0.0f && beta1 < 1.0f) ||
+         !(beta2 >= 0.0f && beta2 < 1.0f) || step < 1;
+}
+
+// The scalars of an Adam update at step `step`, for the long and the short path.
+void set_scalars(AdamScalars& k, float lr, float beta1, float beta2, float eps, int64_t step) {
+  k.b1 = beta1;
+  k.b2 = beta2;
+  k.omb1 = 1.0f - beta1;
+  k.omb2 = 1.0f - beta2;
+  k.eps = eps;
+  const double bc1 = 1.0 - pow_by_squaring(static_cast<double>(beta1), step);
+  const double bc2 = 1.0 - pow_by_squaring(static_cast<double>(beta2), step);
+  k.step_size = static_cast<float>(static_cast<double>(lr) / bc1);
   k.inv_sqrt_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
   // The bf16 short path's folded scalars, each one rounding of an exact quotient of
   // binary32 values.  Its error bound needs a and b normal (or b zero) and a
@@ -1545,6 +1709,11 @@ extern "C" int qopt_adam8bit_step(const qopt_tensor* tensors, int32_t ntensors, 
   k.short_a = ss > 0.0 ? static_cast<float>(static_cast<double>(k.inv_sqrt_bc2) / ss) : 0.0f;
   k.short_b = ss > 0.0 ? static_cast<float>(static_cast<double>(k.eps) / ss) : 0.0f;
   k.t_limit = static_cast<float>((ss < 1.0 ? ss : 1.0) * 0x1p127);
+}
+
+// Whether the step may take the bf16 short path with these scalars: a ScreenMode.
+int screen_mode(const AdamScalars& k) {
+  const double ss = static_cast<double>(k.step_size);
   const bool a_ok = k.short_a >= 0x1p-63f && k.short_a <= 0x1p61f;
   const bool b_ok = k.short_b == 0.0f || (k.short_b >= 0x1p-126f && k.short_b <= 0x1p125f);
   const bool screen = ss > 0.0 && ss <= 0x1p20 && a_ok && b_ok;
@@ -1557,20 +1726,98 @@ extern "C" int qopt_adam8bit_step(const qopt_tensor* tensors, int32_t ntensors, 
   const bool sub_check =
       k.eps != 0.0f &&
       !(static_cast<double>(k.eps) >= static_cast<double>(k.inv_sqrt_bc2) * 0x1p-39);
-  const int mode = !screen ? kNoScreen : (sub_check ? kScreenSubCheck : kScreen);
+  return !screen ? kNoScreen : (sub_check ? kScreenSubCheck : kScreen);
+}
 
+// One 8-bit step with the scalars of either kind, over the dtype pairs.
+template <typename K>
+int step_8bit(const qopt_tensor* tensors, int32_t ntensors, int param_dtype, int grad_dtype,
+              const K& k, const qopt_codebook* cb_m, const qopt_codebook* cb_v, hipStream_t s) {
+  const size_t psize = param_dtype == QOPT_F32 ? 4 : 2;
+  const size_t gsize = grad_dtype == QOPT_F32 ? 4 : 2;
+  const int mode = screen_mode(k);
+  if (param_dtype == QOPT_F32 && grad_dtype == QOPT_F32)
+    return launch_step_chunks<float, float>(tensors, ntensors, psize, gsize, k, mode, cb_m, cb_v, s);
+  if (param_dtype == QOPT_F32 && grad_dtype == QOPT_BF16)
+    return launch_step_chunks<float, uint16_t>(tensors, ntensors, psize, gsize, k, mode, cb_m,
+                                               cb_v, s);
+  if (param_dtype == QOPT_BF16 && grad_dtype == QOPT_F32)
+    return launch_step_chunks<uint16_t, float>(tensors, ntensors, psize, gsize, k, mode, cb_m,
+                                               cb_v, s);
+  return launch_step_chunks<uint16_t, uint16_t>(tensors, ntensors, psize, gsize, k, mode, cb_m,
+                                                cb_v, s);
+}
+
+}  // namespace
+
+extern "C" int qopt_adam8bit_step(const qopt_tensor* tensors, int32_t ntensors, int param_dtype,
+                                  int grad_dtype, const qopt_codebook* cb_m_dev,
+                                  const qopt_codebook* cb_v_dev, const qopt_adam_hparams* hp,
+                                  void* stream) {
+  if (hp == nullptr) return QOPT_EINVAL;
+  bool any = false;
+  int rc = check_step_tensors(tensors, ntensors, param_dtype, grad_dtype, &any);
+  if (rc != QOPT_OK) return rc;
+  if (bad_hparams(hp->lr, hp->beta1, hp->beta2, hp->eps, hp->step)) return QOPT_EINVAL;
+  if (!any) return QOPT_OK;
+  if (!cb_m_dev || !cb_v_dev) return QOPT_EINVAL;
+  if (!aligned(cb_m_dev, 16) || !aligned(cb_v_dev, 16)) return QOPT_EALIGN;
+  AdamScalars k;
+  set_scalars(k, hp->lr, hp->beta1, hp->beta2, hp->eps, hp->step);
+  return step_8bit(tensors, ntensors, param_dtype, grad_dtype, k, cb_m_dev, cb_v_dev,
+                   static_cast<hipStream_t>(stream));
+}
+
+namespace {
+
+int check_adamw(const qopt_adamw_hparams* hp, const float* grad_scale_dev) {
+  if (bad_hparams(hp->lr, hp->beta1, hp->beta2, hp->eps, hp->step)) return QOPT_EINVAL;
+  if (!finite(hp->weight_decay) || hp->weight_decay < 0.0f) return QOPT_EINVAL;
+  return aligned(grad_scale_dev, 4) ? QOPT_OK : QOPT_EALIGN;
+}
+
+AdamWScalars adamw_scalars(const qopt_adamw_hparams* hp, const float* grad_scale_dev) {
+  AdamWScalars k;
+  set_scalars(k, hp->lr, hp->beta1, hp->beta2, hp->eps, hp->step);
+  k.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) *
+                                         static_cast<double>(hp->weight_decay));
+  k.gscale = 1.0f;
+  k.grad_scale = grad_scale_dev;
+  return k;
+}
+
+}  // namespace
+
+extern "C" int qopt_adamw8bit_step(const qopt_tensor* tensors, int32_t ntensors, int param_dtype,
+                                   int grad_dtype, const qopt_codebook* cb_m_dev,
+                                   const qopt_codebook* cb_v_dev, const qopt_adamw_hparams* hp,
+                                   const float* grad_scale_dev, void* stream) {
+  if (hp == nullptr) return QOPT_EINVAL;
+  bool any = false;
+  int rc = check_step_tensors(tensors, ntensors, param_dtype, grad_dtype, &any);
+  if (rc == QOPT_OK) rc = check_adamw(hp, grad_scale_dev);
+  if (rc != QOPT_OK || !any) return rc;
+  if (!cb_m_dev || !cb_v_dev) return QOPT_EINVAL;
+  if (!aligned(cb_m_dev, 16) || !aligned(cb_v_dev, 16)) return QOPT_EALIGN;
+  return step_8bit(tensors, ntensors, param_dtype, grad_dtype, adamw_scalars(hp, grad_scale_dev),
+                   cb_m_dev, cb_v_dev, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int qopt_adamw32bit_step(const qopt_tensor32* tensors, int32_t ntensors,
+                                    int param_dtype, int grad_dtype, const qopt_adamw_hparams* hp,
+                                    const float* grad_scale_dev, void* stream) {
+  if (hp == nullptr) return QOPT_EINVAL;
+  bool any = false;
+  int rc = check_step32_tensors(tensors, ntensors, param_dtype, grad_dtype, &any);
+  if (rc == QOPT_OK) rc = check_adamw(hp, grad_scale_dev);
+  if (rc != QOPT_OK || !any) return rc;
+  const AdamWScalars k = adamw_scalars(hp, grad_scale_dev);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (param_dtype == QOPT_F32 && grad_dtype == QOPT_F32)
-    return launch_step_chunks<float, float>(tensors, ntensors, psize, gsize, k, mode, cb_m_dev,
-                                            cb_v_dev, s);
-  if (param_dtype == QOPT_F32 && grad_dtype == QOPT_BF16)
-    return launch_step_chunks<float, uint16_t>(tensors, ntensors, psize, gsize, k, mode, cb_m_dev,
-                                               cb_v_dev, s);
-  if (param_dtype == QOPT_BF16 && grad_dtype == QOPT_F32)
-    return launch_step_chunks<uint16_t, float>(tensors, ntensors, psize, gsize, k, mode, cb_m_dev,
-                                               cb_v_dev, s);
-  return launch_step_chunks<uint16_t, uint16_t>(tensors, ntensors, psize, gsize, k, mode, cb_m_dev,
-                                                  cb_v_dev, s);
+    return launch_step32<float, float>(tensors, ntensors, k, s);
+  if (param_dtype == QOPT_F32) return launch_step32<float, uint16_t>(tensors, ntensors, k, s);
+  if (grad_dtype == QOPT_F32) return launch_step32<uint16_t, float>(tensors, ntensors, k, s);
+  return launch_step32<uint16_t, uint16_t>(tensors, ntensors, k, s);
 }
 
 // Workgroups per CU the step itself runs with (its occupancy), so that the traffic
@@ -1578,7 +1825,7 @@ extern "C" int qopt_adam8bit_step(const qopt_tensor* tensors, int32_t ntensors, 
 template <typename PT, typename GT>
 int step_wg_per_cu(int* per_cu) {
   constexpr int kMode = std::is_same<PT, uint16_t>::value ? kScreen : kNoScreen;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(per_cu, adam8bit_kernel<PT, GT, kMode>,
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(per_cu, adam8bit_kernel<PT, GT, kMode, AdamScalars>,
                                                    kThreads, 0) != hipSuccess ||
       *per_cu <= 0)
     return QOPT_ELAUNCH;

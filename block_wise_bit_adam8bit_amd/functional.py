@@ -231,6 +231,121 @@ def qopt_adam8bit_step(tensors, *, lr, beta1, beta2, eps, step, _prepared=None):
     _lib.check("qopt_adam8bit_step", rc)
 
 
+class AdamWPlan:
+    """The launch descriptors of an AdamW step over one list of tensors, made by
+    qopt_adamw8bit_plan or qopt_adamw32bit_plan and stepped any number of times.  It holds
+    references to the tensors, whose storage must stay where it is."""
+
+    __slots__ = ("bits", "tensors", "array", "pdtype", "gdtype", "device")
+
+    def __init__(self, bits, tensors, array, pdtype, gdtype, device):
+        self.bits, self.tensors, self.array = bits, tensors, array
+        self.pdtype, self.gdtype, self.device = pdtype, gdtype, device
+
+
+def _check_disjoint(tensors):
+    """Refuse lists in which a tensor that the step writes shares memory with another:
+    its blocks would be updated by two waves at once."""
+    spans = []
+    for t in tensors:
+        for i, x in enumerate(t):
+            n = x.numel() * x.element_size()
+            if n:
+                spans.append((x.data_ptr(), x.data_ptr() + n, i != 1))
+    spans.sort()
+    end, end_written = 0, 0  # furthest end of all spans so far, and of the written ones
+    for lo, hi, written in spans:
+        if lo < (end if written else end_written):
+            raise ValueError("the tensors of one step must not overlap (a parameter listed twice?)")
+        end = max(end, hi)
+        if written:
+            end_written = max(end_written, hi)
+
+
+def qopt_adamw8bit_plan(tensors):
+    """Plan of an 8-bit AdamW step over a list of (param, grad, m_codes, v_codes, m_absmax,
+    v_absmax) tuples, checked as for qopt_adam8bit_step; none may overlap another."""
+    tensors = [tuple(t) for t in tensors]
+    arr, pdt, gdt, dev = make_tensor_array(tensors)
+    _check_disjoint(tensors)
+    return AdamWPlan(8, tensors, arr, pdt, gdt, dev)
+
+
+def qopt_adamw32bit_plan(tensors):
+    """Plan of an AdamW step with 32-bit moments over a list of (param, grad, m, v) tuples
+    (fp32 or bf16 params and grads, fp32 moments); none may overlap another."""
+    tensors = [tuple(t) for t in tensors]
+    arr = (_lib.qopt_tensor32 * len(tensors))()
+    pdt = gdt = dev = None
+    for i, (p, g, m, v) in enumerate(tensors):
+        n = p.numel()
+        if p.dtype not in _DTYPES or g.dtype not in _DTYPES:
+            raise TypeError("params and grads must be float32 or bfloat16")
+        if pdt is None:
+            pdt, gdt = _DTYPES[p.dtype], _DTYPES[g.dtype]
+        elif (_DTYPES[p.dtype], _DTYPES[g.dtype]) != (pdt, gdt):
+            raise TypeError("one call takes one (param dtype, grad dtype) pair")
+        if m.dtype != torch.float32 or v.dtype != torch.float32:
+            raise TypeError("moments must be float32")
+        if g.numel() != n or m.numel() != n or v.numel() != n:
+            raise ValueError("param, grad and moments must have the same size")
+        d = _check_cuda(p, g, m, v)
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError("all tensors of one call must be on the same GPU")
+        arr[i] = _lib.qopt_tensor32(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), n)
+    _check_disjoint(tensors)
+    return AdamWPlan(32, tensors, arr, QOPT_F32 if pdt is None else pdt,
+                     QOPT_F32 if gdt is None else gdt, dev)
+
+
+def _adamw_args(plan, bits, lr, beta1, beta2, eps, weight_decay, step, grad_scale):
+    if plan.bits != bits:
+        raise ValueError(f"the plan is one of a step with {plan.bits}-bit moments")
+    if grad_scale is not None:
+        if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
+            raise ValueError("grad_scale must be one float32 value")
+        if plan.device is not None and grad_scale.device != plan.device:
+            raise ValueError("grad_scale must be on the tensors' GPU")
+    hp = _lib.qopt_adamw_hparams(float(lr), float(beta1), float(beta2), float(eps),
+                                 float(weight_decay), int(step))
+    return ctypes.byref(hp), None if grad_scale is None else grad_scale.data_ptr()
+
+
+def qopt_adamw8bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, grad_scale=None):
+    """One fused 8-bit AdamW step over a list of (param, grad, m_codes, v_codes, m_absmax,
+    v_absmax) tuples, or a plan of it, updated in place on torch's current stream.
+    ``grad_scale``: a float32 GPU tensor of one value that every gradient is multiplied
+    with, read when the step runs (a clipping factor, for instance)."""
+    plan = tensors if isinstance(tensors, AdamWPlan) else qopt_adamw8bit_plan(tensors)
+    hp, gs = _adamw_args(plan, 8, lr, beta1, beta2, eps, weight_decay, step, grad_scale)
+    dev = plan.device
+    if dev is None:
+        return
+    with torch.cuda.device(dev):
+        rc = LIB.qopt_adamw8bit_step(plan.array, len(plan.array), plan.pdtype, plan.gdtype,
+                                     codebook(SIGNED, dev).data_ptr(),
+                                     codebook(UNSIGNED, dev).data_ptr(), hp, gs,
+                                     _lib.stream_handle(dev))
+    _lib.check("qopt_adamw8bit_step", rc)
+
+
+def qopt_adamw32bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, grad_scale=None):
+    """One AdamW step with 32-bit moments over a list of (param, grad, m, v) tuples, or a
+    plan of it, updated in place on torch's current stream; ``grad_scale`` as for
+    qopt_adamw8bit_step."""
+    plan = tensors if isinstance(tensors, AdamWPlan) else qopt_adamw32bit_plan(tensors)
+    hp, gs = _adamw_args(plan, 32, lr, beta1, beta2, eps, weight_decay, step, grad_scale)
+    dev = plan.device
+    if dev is None:
+        return
+    with torch.cuda.device(dev):
+        rc = LIB.qopt_adamw32bit_step(plan.array, len(plan.array), plan.pdtype, plan.gdtype, hp,
+                                      gs, _lib.stream_handle(dev))
+    _lib.check("qopt_adamw32bit_step", rc)
+
+
 def qopt_pattern_probe_names():
     """Descriptions of the bytes-only access patterns (a measurement aid)."""
     return [LIB.qopt_pattern_probe_name(i).decode() for i in range(LIB.qopt_pattern_probe_count())]

@@ -15,6 +15,10 @@ codes starting on a 256-byte boundary.  A few large allocations map to larger pa
 fragments than one allocation per tensor: measured on the Llama-7B set, per-tensor
 allocations took 7 times the address-translation misses and a flat state was up to
 4 % faster, never slower.
+
+AdamW: the step with decoupled weight decay, for which each parameter keeps either that
+8-bit state or fp32 moments (``exp_avg`` / ``exp_avg_sq``), chosen per parameter group
+and by size.
 """
 
 from collections import defaultdict
@@ -22,7 +26,8 @@ from collections import defaultdict
 import torch
 
 from .checkpoint import compress_moments_multi, decompress_moments_multi
-from .functional import make_tensor_array, nblocks, qopt_adam8bit_step
+from .functional import (make_tensor_array, nblocks, qopt_adam8bit_step, qopt_adamw8bit_plan,
+                         qopt_adamw8bit_step, qopt_adamw32bit_plan, qopt_adamw32bit_step)
 
 _STATE_KEYS = ("m_codes", "v_codes", "m_absmax", "v_absmax")
 _CODE_ALIGN = 256  # bytes between the starts of consecutive parameters' codes
@@ -219,3 +224,219 @@ class Adam8bit(torch.optim.Optimizer):
                       amsgrad=False, params=list(g["params"]))
             groups.append(ng)
         return {"state": out_state, "param_groups": groups}
+
+
+_MOMENT_KEYS = ("exp_avg", "exp_avg_sq")
+_MOMENT_ALIGN = 64  # fp32 values between the starts of consecutive parameters' moments
+
+
+def _flat_moments(device, shapes):
+    """Zero-filled (exp_avg, exp_avg_sq) per parameter shape, views of two flat buffers."""
+    off, c = [], 0
+    for s in shapes:
+        off.append(c)
+        c += -(-s.numel() // _MOMENT_ALIGN) * _MOMENT_ALIGN
+    m = torch.zeros(max(c, 1), dtype=torch.float32, device=device)
+    v = torch.zeros_like(m)
+    return [(m[o:o + s.numel()].view(s), v[o:o + s.numel()].view(s))
+            for s, o in zip(shapes, off)]
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW (decoupled weight decay) with moments held in 8 bits or in 32.
+
+    ``state_bits`` (8 or 32) and ``min_8bit_size`` are per-group options: a parameter of
+    a group with ``state_bits=8`` keeps block-wise dynamic-tree codes as ``Adam8bit``
+    does, unless it has fewer than ``min_8bit_size`` elements; every other parameter
+    keeps fp32 moments.  The choice is made at a parameter's first step and travels with
+    its state.  Each kind takes one fused multi-tensor step per (device, dtypes).
+
+    ``step(grad_scale=t)`` multiplies every gradient with the float32 GPU value ``t``
+    inside the step, so that clipping needs neither a pass over the gradients nor a
+    synchronisation.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, *,
+                 state_bits=8, min_8bit_size=4096):
+        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
+                                      weight_decay=weight_decay, state_bits=state_bits,
+                                      min_8bit_size=min_8bit_size))
+        self._plans = {}
+
+    def add_param_group(self, param_group):
+        g = {**self.defaults, **param_group}
+        if not 0.0 <= g["lr"]:
+            raise ValueError(f"invalid learning rate {g['lr']}")
+        if not 0.0 <= g["eps"]:
+            raise ValueError(f"invalid epsilon {g['eps']}")
+        if not (0.0 <= g["betas"][0] < 1.0 and 0.0 <= g["betas"][1] < 1.0):
+            raise ValueError(f"invalid betas {g['betas']}")
+        if not 0.0 <= g["weight_decay"]:
+            raise ValueError(f"invalid weight decay {g['weight_decay']}")
+        if g["state_bits"] not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, not {g['state_bits']}")
+        super().add_param_group(param_group)
+
+    def _init_states(self, group, params):
+        """Zero state for parameters without one, in flat buffers per device and kind."""
+        by_kind = defaultdict(list)
+        for p in params:
+            coded = group["state_bits"] == 8 and p.numel() >= group["min_8bit_size"]
+            by_kind[p.device, coded].append(p)
+        for (dev, coded), ps in by_kind.items():
+            keys = _STATE_KEYS if coded else _MOMENT_KEYS
+            views = _flat_state(dev, [p.numel() for p in ps]) if coded \
+                else _flat_moments(dev, [p.shape for p in ps])
+            for p, ts in zip(ps, views):
+                st = self.state[p]
+                st["step"] = 0
+                st.update(zip(keys, ts))
+
+    @torch.no_grad()
+    def step(self, closure=None, *, grad_scale=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:  # checked before any state changes
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.is_sparse:
+                    raise RuntimeError("AdamW does not take sparse gradients")
+                if not p.is_contiguous() or not p.grad.is_contiguous():
+                    raise RuntimeError("AdamW needs contiguous parameters and gradients")
+        plans = {}
+        for gi, group in enumerate(self.param_groups):
+            live = [p for p in group["params"] if p.grad is not None]
+            self._init_states(group, [p for p in live if not self.state[p]])
+            batches = {}
+            for p in live:
+                st = self.state[p]
+                keys = _STATE_KEYS if "m_codes" in st else _MOMENT_KEYS
+                key = (p.device, p.dtype, p.grad.dtype, len(keys), st["step"] + 1)
+                batches.setdefault(key, []).append((p, p.grad, *(st[k] for k in keys)))
+            b1, b2 = group["betas"]
+            for key, items in batches.items():
+                # a batch's plan is kept while its tensors stay where they are; plans that
+                # this step does not use are dropped with what they hold
+                ident = (gi, key[:4], tuple(x.data_ptr() for t in items for x in t))
+                coded = key[3] == len(_STATE_KEYS)
+                plan = self._plans.get(ident)
+                if plan is None:
+                    plan = (qopt_adamw8bit_plan if coded else qopt_adamw32bit_plan)(items)
+                plans[ident] = plan
+                run = qopt_adamw8bit_step if coded else qopt_adamw32bit_step
+                run(plan, lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
+                    weight_decay=group["weight_decay"], step=key[4], grad_scale=grad_scale)
+                for t in items:
+                    self.state[t[0]]["step"] = key[4]
+        self._plans = plans
+        return loss
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}
+
+    _params_by_saved_id = Adam8bit._params_by_saved_id
+
+    def _take_state(self, state, groups, keys):
+        """Adopt ``state`` (param -> dict) in flat buffers, and ``keys`` of the saved groups."""
+        _repack({p: st for p, st in state.items() if "m_codes" in st})
+        by_device = defaultdict(list)
+        for p, st in state.items():
+            if "m_codes" not in st:
+                by_device[p.device].append(p)
+        for dev, ps in by_device.items():
+            for p, views in zip(ps, _flat_moments(dev, [p.shape for p in ps])):
+                for k, t in zip(_MOMENT_KEYS, views):
+                    t.copy_(state[p][k].view(p.shape))
+                    state[p][k] = t
+        self.state = state
+        for group, saved in zip(self.param_groups, groups):
+            for k in (saved if keys is None else keys):
+                if k != "params":
+                    group[k] = saved[k]
+        self._plans = {}
+
+    def load_state_dict(self, state_dict):
+        """Load a state dict of ``AdamW`` or ``Adam8bit``; each parameter keeps the kind of
+        state that was saved, in its own dtypes (torch's loader would cast the codes and
+        moments to the parameter's dtype)."""
+        groups = state_dict["param_groups"]
+        by_id = self._params_by_saved_id(groups)
+        state = defaultdict(dict)
+        for pid, st in state_dict["state"].items():
+            p = by_id[pid]
+            n = p.numel()
+            want = (("m_codes", torch.uint8, n), ("v_codes", torch.uint8, n),
+                    ("m_absmax", torch.float32, nblocks(n)),
+                    ("v_absmax", torch.float32, nblocks(n))) if "m_codes" in st else \
+                tuple((k, torch.float32, n) for k in _MOMENT_KEYS)
+            new = {"step": int(st["step"])}
+            for k, dt, size in want:
+                t = st.get(k)
+                if t is None or t.dtype != dt or t.numel() != size:
+                    raise ValueError(f"state '{k}' of a parameter with {n} elements must be "
+                                     f"{dt} with {size} elements")
+                new[k] = t.to(device=p.device)
+            state[p] = new
+        self._take_state(state, groups, None)
+
+    @torch.no_grad()
+    def load_fp32_adam_state(self, adam_state_dict):
+        """Take over the state of a ``torch.optim.AdamW`` (or plain ``Adam``) state dict
+        with the same parameter groups.  Parameters that keep codes here get their moments
+        quantized block-wise, the others get them as they are, in fp32; steps, lr, betas, eps
+        and weight decay are kept.  amsgrad, maximize and Adam's coupled weight decay have
+        no equivalent here and are refused."""
+        groups = adam_state_dict["param_groups"]
+        for g in groups:
+            if g.get("amsgrad", False) or g.get("maximize", False):
+                raise ValueError("amsgrad and maximize have no equivalent here")
+            if g.get("weight_decay", 0.0) != 0.0 and not g.get("decoupled_weight_decay", True):
+                raise ValueError("Adam's weight decay is not AdamW's; only plain Adam converts")
+        by_id = self._params_by_saved_id(groups)
+        group_of = {p: g for g in self.param_groups for p in g["params"]}
+        state = defaultdict(dict)
+        by_device = defaultdict(list)
+        for pid, st in adam_state_dict["state"].items():
+            p = by_id[pid]
+            if st["exp_avg"].numel() != p.numel() or st["exp_avg_sq"].numel() != p.numel():
+                raise ValueError("moment size differs from its parameter")
+            m, v = (st[k].to(p.device, torch.float32) for k in _MOMENT_KEYS)
+            state[p] = {"step": int(st["step"]), "exp_avg": m, "exp_avg_sq": v}
+            g = group_of[p]
+            if g["state_bits"] == 8 and p.numel() >= g["min_8bit_size"]:
+                by_device[p.device].append(p)
+        for ps in by_device.values():
+            codes = compress_moments_multi([tuple(state[p][k] for k in _MOMENT_KEYS) for p in ps])
+            for p, new in zip(ps, codes):
+                state[p] = {"step": state[p]["step"], **new}
+        self._take_state(state, groups, ("lr", "betas", "eps", "weight_decay"))
+
+    @torch.no_grad()
+    def fp32_adam_state_dict(self):
+        """A ``torch.optim.AdamW``-loadable state dict: every moment in fp32 and its
+        parameter's shape, the step as a float tensor."""
+        sd = self.state_dict()
+        out_state = {}
+        params = [p for g in self.param_groups for p in g["params"]]
+        by_device = defaultdict(list)
+        for pid, st in sd["state"].items():
+            if "m_codes" in st:
+                by_device[st["m_codes"].device].append((pid, st))
+            else:
+                out_state[pid] = {"step": torch.tensor(float(st["step"])),
+                                  **{k: st[k].clone() for k in _MOMENT_KEYS}}
+        for items in by_device.values():
+            moments = decompress_moments_multi([st for _, st in items],
+                                               shapes=[params[pid].shape for pid, _ in items])
+            for (pid, st), (m, v) in zip(items, moments):
+                out_state[pid] = {"step": torch.tensor(float(st["step"])), "exp_avg": m,
+                                  "exp_avg_sq": v}
+        defaults = torch.optim.AdamW([torch.zeros(1)]).defaults  # this torch's keys
+        groups = [{**defaults, "lr": g["lr"], "betas": tuple(g["betas"]), "eps": g["eps"],
+                   "weight_decay": g["weight_decay"], "amsgrad": False,
+                   "params": list(g["params"])} for g in sd["param_groups"]]
+        return {"state": dict(sorted(out_state.items())), "param_groups": groups}

@@ -220,7 +220,7 @@ typedef struct qopt_adam_hparams {
  * launches of equal block counts (qopt_adam8bit_launch_count), on `stream`; with bf16
  * parameters and more than one launch, every other launch goes on a second stream
  * that the library creates once per device (non-blocking, default priority, kept
- * until the process ends).  That stream first waits for the work enqueued on `stream`
+ * until the process ends), unless `stream` is being captured into a graph.  That stream first waits for the work enqueued on `stream`
  * before the call, and `stream` waits for its launches before any work enqueued after
  * the call, so the call orders on `stream` as one unit.
  */
@@ -228,6 +228,61 @@ int qopt_adam8bit_step(const qopt_tensor* tensors, int32_t ntensors, int param_d
                        int grad_dtype, const qopt_codebook* cb_m_dev,
                        const qopt_codebook* cb_v_dev, const qopt_adam_hparams* hp,
                        void* stream);
+
+/* AdamW hyper-parameters (binary32) and the 1-based step number after increment. */
+typedef struct qopt_adamw_hparams {
+  float lr;
+  float beta1;
+  float beta2;
+  float eps;
+  float weight_decay;
+  int64_t step;
+} qopt_adamw_hparams;
+
+/*
+ * One fused 8-bit AdamW step: qopt_adam8bit_step with decoupled weight decay and an
+ * optional factor of the gradients.  Per element, binary32, one rounding per operation:
+ *   g = grad * s                          p = param * decay
+ *   then m, v and p exactly as qopt_adam8bit_step computes them from g and p,
+ * with decay = fl32(1 - lr * weight_decay) evaluated in binary64 from the binary32
+ * hyper-parameters, and s the fp32 value at grad_scale_dev (device memory, 4-byte
+ * aligned, read when the work runs; NULL for 1): a clipping factor that the host need
+ * not know.  A bf16 parameter is rounded once, after the update.  With weight_decay 0
+ * and s = 1 the results are those of qopt_adam8bit_step.
+ * Everything else is as for qopt_adam8bit_step (state, launches, streams, checks);
+ * also checked: weight_decay finite and >= 0.  Under graph capture the hyper-parameters
+ * and the step number are captured as they are, and every replay takes that same step.
+ */
+int qopt_adamw8bit_step(const qopt_tensor* tensors, int32_t ntensors, int param_dtype,
+                        int grad_dtype, const qopt_codebook* cb_m_dev,
+                        const qopt_codebook* cb_v_dev, const qopt_adamw_hparams* hp,
+                        const float* grad_scale_dev, void* stream);
+
+/*
+ * One parameter tensor of an AdamW step with 32-bit moments.  All pointers are device
+ * memory: param and grad as in qopt_tensor; m and v hold n fp32 moments each, 4-byte
+ * aligned, updated in place (zero before the first step).  Buffers of different tensors,
+ * and of one tensor, must not overlap.  Tensors whose param / grad are 16-byte (fp32) or
+ * 8-byte (bf16) aligned and whose moments are 16-byte aligned take the vector path.
+ */
+typedef struct qopt_tensor32 {
+  void* param;
+  const void* grad;
+  float* m;
+  float* v;
+  int64_t n;
+} qopt_tensor32;
+
+/*
+ * One AdamW step with 32-bit moments, for the parameters whose state stays in full
+ * precision (embeddings, small tensors): the arithmetic of qopt_adamw8bit_step with
+ * m_prev and v_prev read from m and v, and the new moments stored there.  Launches of
+ * at most 64 tensor pieces and 2^18 blocks of 2048 elements, on `stream` only.  Checks
+ * as for qopt_adamw8bit_step, without the codebooks.
+ */
+int qopt_adamw32bit_step(const qopt_tensor32* tensors, int32_t ntensors, int param_dtype,
+                         int grad_dtype, const qopt_adamw_hparams* hp,
+                         const float* grad_scale_dev, void* stream);
 
 /*
  * Number of kernel launches qopt_adam8bit_step enqueues for this tensor list and

@@ -58,3 +58,8 @@ from .adam8bit import (  # noqa: F401
     bf16_to_f32,
     f32_to_bf16_rne,
 )
+from .adamw import (  # noqa: F401
+    adamw8bit_step,
+    adamw32bit_step,
+    decay_factor,
+)
