@@ -1,8 +1,9 @@
 """block_wise_bit_adam8bit_amd: block-wise dynamic-tree 8-bit Adam for MI355X.
 
 The compute lives in libqopt.so (HIP kernels for gfx950 behind the C ABI of
-include/qopt.h, include/qopt_embedding.h); this package is its thin Python binding
-plus a torch optimizer and the Stable Embedding module.
+include/qopt.h, include/qopt_embedding.h, include/qopt_fp8.h); this package is its thin Python binding
+plus torch optimizers, the Stable Embedding module and a linear layer whose products run
+in 8-bit floating point.
 Importing it loads the library and fails with ImportError if it is not built.
 """
 
@@ -27,6 +28,10 @@ from .optim import Adam8bit, AdamW  # noqa: F401
 from .embedding import (  # noqa: F401
     StableEmbedding, StableEmbeddingFunction, qopt_embedding_xavier_init,
     qopt_stable_embedding_forward, qopt_stable_embedding_backward,
+)
+from .fp8 import (  # noqa: F401
+    Fp8Linear, Fp8LinearFunction, Fp8Matrix, fp8_linear, qopt_fp8_linear, qopt_fp8_matmul,
+    qopt_fp8_quantize,
 )
 
 __version__ = "0.1.0"

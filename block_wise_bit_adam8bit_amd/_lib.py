@@ -15,6 +15,7 @@ import torch  # noqa: F401  (must be loaded before libqopt.so; see module docstr
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqopt.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt.h")
+FP8_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_fp8.h")
 EMB_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_embedding.h")
 
 QOPT_BLOCK = 2048
@@ -25,6 +26,10 @@ QOPT_F32, QOPT_BF16 = 0, 1
 QOPT_CODEBOOK_MAGIC = 0x31424351
 QOPT_MAX_BUCKETS = 7168
 QOPT_THRESH_LEN = 272
+QOPT_FP8_ROWS, QOPT_FP8_TILES = 0, 1
+QOPT_FP8_BLOCK = 128
+QOPT_FP8_MAX_DIM = 8388608
+QOPT_FP8_FEW_ROWS = 32
 QOPT_EMB_VEC_MAX_DIM = 4096
 QOPT_EMB_STATIC_SCRATCH_BYTES = 64 << 20
 
@@ -161,6 +166,24 @@ _SIGNATURES = {
                                                               ctypes.c_int, ctypes.c_void_p,
                                                               ctypes.c_void_p, ctypes.c_void_p,
                                                               ctypes.c_void_p]),
+    "qopt_fp8_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "qopt_fp8_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qopt_fp8_matmul_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "qopt_fp8_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qopt_fp8_linear_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "qopt_pattern_probe_count": (ctypes.c_int, []),
     "qopt_pattern_probe_name": (ctypes.c_char_p, [ctypes.c_int]),
     "qopt_pattern_probe": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
@@ -187,7 +210,7 @@ def _load():
 LIB = _load()
 
 
-def header_constants(paths=(HEADER, EMB_HEADER)):
+def header_constants(paths=(HEADER, EMB_HEADER, FP8_HEADER)):
     """#define values of include/*.h (used by tests to check this mirror)."""
     out = {}
     for path in paths:

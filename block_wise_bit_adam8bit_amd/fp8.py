@@ -1,0 +1,273 @@
+"""Linear products in 8-bit floating point: wrappers with the C ABI's names
+(include/qopt_fp8.h), an autograd function and a torch module.
+
+The block-wise quantization of the 8-bit optimizers summary page (§2 "Block-wise
+Quantization") for the products of a linear layer: e4m3 codes with one power-of-two
+scale per 128 values along the summed axis (activations, upstream gradients) or per
+tile of 128 x 128 (weights).  Every step runs in libqopt's HIP kernels; torch allocates
+outputs and workspaces and supplies the current stream.
+"""
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from ._lib import (LIB, QOPT_BF16, QOPT_F32, QOPT_FP8_BLOCK, QOPT_FP8_FEW_ROWS, QOPT_FP8_ROWS,
+                   QOPT_FP8_TILES)
+from .embedding import qopt_embedding_xavier_init
+
+_DT = {torch.float32: QOPT_F32, torch.bfloat16: QOPT_BF16}
+CODE_DTYPE = torch.float8_e4m3fn
+
+
+class Fp8Matrix(NamedTuple):
+    """A quantized matrix: float8_e4m3fn codes [rows, columns up to a multiple of 128] and
+    uint8 scales, each standing for 2^(scale - 127): [rows, columns / 128], or one per tile
+    of 128 x 128, [ceil(rows / 128), columns / 128]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _blocks(n):
+    return -(-int(n) // QOPT_FP8_BLOCK)
+
+
+def _check_dtype(dtype, what):
+    if dtype not in _DT:
+        raise TypeError(f"{what} must be float32 or bfloat16, not {dtype}")
+    return _DT[dtype]
+
+
+def _same_gpu(*ts):
+    dev = ts[0].device
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("all tensors must be on a GPU")
+        if t.device != dev:
+            raise ValueError("all tensors must be on the same GPU")
+    return dev
+
+
+def _row_stride(t, what):
+    """Elements between the rows of a 2-D tensor whose rows are contiguous."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {what} must be contiguous")
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"the rows of {what} must not overlap")
+    return t.stride(0)
+
+
+def _quantized(codes, scales, what):
+    """Checks a (codes, scales) pair; returns its form."""
+    if codes.dtype != CODE_DTYPE or scales.dtype != torch.uint8:
+        raise TypeError(f"{what}: codes must be float8_e4m3fn and scales uint8")
+    if codes.dim() != 2 or codes.shape[1] % QOPT_FP8_BLOCK:
+        raise ValueError(f"{what}: codes must be 2-D with a multiple of {QOPT_FP8_BLOCK} columns")
+    rows, kb = codes.shape[0], codes.shape[1] // QOPT_FP8_BLOCK
+    if tuple(scales.shape) not in ((rows, kb), (_blocks(rows), kb)):
+        raise ValueError(f"{what}: scales must be {(rows, kb)} or {(_blocks(rows), kb)}, not "
+                         f"{tuple(scales.shape)}")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{what}: codes and scales must be contiguous")
+    return QOPT_FP8_ROWS if scales.shape[0] == rows else QOPT_FP8_TILES
+
+
+def _empty_matrix(rows, cols, tiles, device):
+    kb = _blocks(cols)
+    return Fp8Matrix(
+        torch.empty(rows, kb * QOPT_FP8_BLOCK, dtype=CODE_DTYPE, device=device),
+        torch.empty(_blocks(rows) if tiles else rows, kb, dtype=torch.uint8, device=device))
+
+
+def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
+    """Quantize a 2-D float32 or bfloat16 tensor in blocks of 128 along its rows, or in
+    tiles of 128 x 128 (``tiles``).  Returns the Fp8Matrix of x (``normal``), of its transpose
+    (``transposed``), or the pair of both."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    if not normal and not transposed:
+        raise ValueError("nothing to return")
+    dt = _check_dtype(x.dtype, "x")
+    dev = _same_gpu(x)
+    ldx = _row_stride(x, "x")
+    rows, cols = x.shape
+    a = _empty_matrix(rows, cols, tiles, dev) if normal else None
+    b = _empty_matrix(cols, rows, tiles, dev) if transposed else None
+    if rows and cols:
+        ptrs = [None if m is None else t.data_ptr() for m in (a, b) for t in (m or (None, None))]
+        with torch.cuda.device(dev):
+            rc = LIB.qopt_fp8_quantize(x.data_ptr(), dt, rows, cols, ldx,
+                                       QOPT_FP8_TILES if tiles else QOPT_FP8_ROWS, *ptrs,
+                                       _lib.stream_handle(dev))
+        _lib.check("qopt_fp8_quantize", rc)
+    return (a, b) if normal and transposed else a if normal else b
+
+
+def _workspace(query, name, m, n, k, dt, dev):
+    need = ctypes.c_size_t(0)
+    _lib.check(name, query(m, n, k, dt, ctypes.byref(need)))
+    return torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+
+
+def _output(out, shape, dtype, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if out.shape != shape or out.dtype != dtype:
+        raise ValueError(f"out must have shape {tuple(shape)} and dtype {dtype}")
+    return out
+
+
+def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, *, out=None):
+    """a b^T of two quantized matrices [m, k] and [n, k] (either form each): [m, n] in
+    ``out_dtype`` (bfloat16 or float32), into ``out`` if given."""
+    fa, fb = _quantized(a_codes, a_scales, "a"), _quantized(b_codes, b_scales, "b")
+    dt = _check_dtype(out_dtype, "out_dtype")
+    (m, k), n = a_codes.shape, b_codes.shape[0]
+    if b_codes.shape[1] != k:
+        raise ValueError("a and b must have the same number of columns")
+    dev = _same_gpu(a_codes, a_scales, b_codes, b_scales)
+    out = _output(out, torch.Size((m, n)), out_dtype, dev)
+    _same_gpu(a_codes, out)
+    ldo = _row_stride(out, "out")
+    with torch.cuda.device(dev):
+        ws = _workspace(LIB.qopt_fp8_matmul_workspace, "qopt_fp8_matmul_workspace", m, n, k, dt, dev)
+        rc = LIB.qopt_fp8_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(),
+                                 b_scales.data_ptr(), fb, m, n, k, out.data_ptr(), dt, ldo,
+                                 None if ws is None else ws.data_ptr(),
+                                 0 if ws is None else ws.numel(), _lib.stream_handle(dev))
+    _lib.check("qopt_fp8_matmul", rc)
+    return out
+
+
+def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
+    """x w^T for x [..., k] in float32 or bfloat16, quantized on the way, and a quantized
+    weight [n, k]: [..., n] in ``out_dtype`` (default: x's).  One launch for up to
+    QOPT_FP8_FEW_ROWS rows of x."""
+    form = _quantized(w_codes, w_scales, "w")
+    dx = _check_dtype(x.dtype, "x")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    do = _check_dtype(out_dtype, "out_dtype")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    k, n = x.shape[-1], w_codes.shape[0]
+    if _blocks(k) * QOPT_FP8_BLOCK != w_codes.shape[1]:
+        raise ValueError(f"x has {k} columns, the weight {w_codes.shape[1]} with its padding")
+    if x.dim() == 2:
+        ldx = _row_stride(x, "x")
+    elif x.is_contiguous():
+        ldx = k
+    else:
+        raise ValueError("x must be 2-D with contiguous rows, or contiguous")
+    m = x.numel() // k if k else x.shape[:-1].numel()
+    dev = _same_gpu(x, w_codes, w_scales)
+    shape = torch.Size((*x.shape[:-1], n))
+    out = _output(out, shape, out_dtype, dev)
+    _same_gpu(x, out)
+    if out.dim() == 2:
+        ldo = _row_stride(out, "out")
+    elif out.is_contiguous():
+        ldo = n
+    else:
+        raise ValueError("out must be 2-D with contiguous rows, or contiguous")
+    with torch.cuda.device(dev):
+        ws = None
+        if m > QOPT_FP8_FEW_ROWS:
+            ws = _workspace(LIB.qopt_fp8_linear_workspace, "qopt_fp8_linear_workspace", m, n, k, do, dev)
+        rc = LIB.qopt_fp8_linear(x.data_ptr(), dx, m, k, ldx, w_codes.data_ptr(),
+                                 w_scales.data_ptr(), form, n, out.data_ptr(), do, ldo,
+                                 None if ws is None else ws.data_ptr(),
+                                 0 if ws is None else ws.numel(), _lib.stream_handle(dev))
+    _lib.check("qopt_fp8_linear", rc)
+    return out
+
+
+class Fp8LinearFunction(torch.autograd.Function):
+    """y = x w^T with both gradients, every product over e4m3 codes: x and the upstream
+    gradient in blocks of 128 along the axis of each sum, w in tiles of 128 x 128."""
+
+    @staticmethod
+    def forward(ctx, x, w):
+        need_x, need_w = ctx.needs_input_grad
+        x2 = x.reshape(-1, w.shape[1]).contiguous()
+        wq = qopt_fp8_quantize(w.contiguous(), tiles=True, transposed=need_x)
+        wq, wt = wq if need_x else (wq, None)
+        if need_w:
+            xq, xt = qopt_fp8_quantize(x2, transposed=True)
+            y = qopt_fp8_matmul(*xq, *wq, x.dtype)
+        else:
+            xt = None
+            y = qopt_fp8_linear(x2, *wq)
+        ctx.dtypes = x.dtype, w.dtype
+        ctx.x_shape = x.shape
+        ctx.save_for_backward(*(wt or (None, None)), *(xt or (None, None)))
+        return y.view(*x.shape[:-1], w.shape[0])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        w_codes_t, w_scales_t, x_codes_t, x_scales_t = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad
+        dy = dy.reshape(-1, dy.shape[-1]).contiguous()
+        if dy.dtype not in _DT:
+            dy = dy.float()
+        if not need_x and not need_w:
+            return None, None
+        dq = qopt_fp8_quantize(dy, normal=need_x, transposed=need_w)
+        dq, dt = dq if need_x and need_w else (dq, dq)
+        dx = dw = None
+        if need_x:
+            k = ctx.x_shape[-1]
+            dx = qopt_fp8_matmul(*dq, w_codes_t, w_scales_t, ctx.dtypes[0])
+            dx = dx.view(*ctx.x_shape[:-1], k)
+        if need_w:
+            dw = qopt_fp8_matmul(*dt, x_codes_t, x_scales_t, ctx.dtypes[1])
+        return dx, dw
+
+
+def fp8_linear(x, w):
+    """x w^T with gradients: x [..., k] and w [n, k] in float32 or bfloat16.  The result and
+    x's gradient have x's type, w's gradient has w's.  The weight is quantized anew in every
+    call; a server quantizes it once and calls ``qopt_fp8_linear``."""
+    _check_dtype(x.dtype, "x")
+    _check_dtype(w.dtype, "w")
+    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
+        raise ValueError("x must be [..., k] and w [n, k]")
+    _same_gpu(x, w)
+    return Fp8LinearFunction.apply(x, w)
+
+
+class Fp8Linear(torch.nn.Module):
+    """Linear layer without bias whose products, forward and backward, run in 8-bit
+    floating point (``fp8_linear``).  The weight itself stays in ``dtype`` (float32 or
+    bfloat16), Xavier-uniform from ``seed`` as the Stable Embedding's table."""
+
+    def __init__(self, in_features, out_features, *, device=None, dtype=torch.float32, seed=0):
+        super().__init__()
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.seed = int(seed)
+        self.weight = torch.nn.Parameter(
+            torch.empty(self.out_features, self.in_features, dtype=dtype, device=device))
+        self.reset_parameters()
+
+    def reset_parameters(self):
+        with torch.no_grad():
+            qopt_embedding_xavier_init(self.weight, self.seed)
+
+    @torch.no_grad()
+    def pack(self):
+        """The weight as ``qopt_fp8_linear`` takes it: quantized in tiles, for serving."""
+        return qopt_fp8_quantize(self.weight.contiguous(), tiles=True)
+
+    def forward(self, x):
+        return fp8_linear(x, self.weight)
+
+    def extra_repr(self):
+        return f"{self.in_features}, {self.out_features}, dtype={self.weight.dtype}"

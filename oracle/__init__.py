@@ -63,3 +63,4 @@ from .adamw import (  # noqa: F401
     adamw32bit_step,
     decay_factor,
 )
+from . import fp8  # noqa: F401,E402
