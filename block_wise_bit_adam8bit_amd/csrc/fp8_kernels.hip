@@ -108,6 +108,7 @@ struct QuantArgs {
   int64_t rows, cols, ldx;
   uint8_t *codes, *scales, *codes_t, *scales_t;
   int64_t kp, kpt;  // bytes per row of codes and codes_t
+  int64_t sr, srt;  // bytes per block row of scales and scales_t
   uint32_t wide;    // rows of x allow 16-byte loads
   uint32_t tiles;   // tiles along a row
 };
@@ -147,7 +148,6 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
       cmax[j] = umax(cmax[j], m);
     }
   }
-  const int64_t kb = q.kp / kBlock, kbt = q.kpt / kBlock;
   uint32_t rs[8], cs[8];
   if constexpr (kTiles) {
     uint32_t m = 0;
@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) rs[i] = cs[i] = s;
     if (t == 0) {
-      if (q.codes) q.scales[tr * kb + tc] = static_cast<uint8_t>(s);
-      if (q.codes_t) q.scales_t[tc * kbt + tr] = static_cast<uint8_t>(s);
+      if (q.codes) q.scales[tr * q.sr + tc] = static_cast<uint8_t>(s);
+      if (q.codes_t) q.scales_t[tc * q.srt + tr] = static_cast<uint8_t>(s);
     }
   } else {
 #pragma unroll
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
       rs[i] = scale_byte(rmax[i]);
       const int64_t row = row0 + 8 * r + i;
       if (q.codes && c == i && row < q.rows)
-        q.scales[row * kb + tc] = static_cast<uint8_t>(rs[i]);
+        q.scales[tc * q.sr + row] = static_cast<uint8_t>(rs[i]);
     }
     if (q.codes_t) {
 #pragma unroll
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
         const int k = 8 * c + j;
         cs[j] = scale_byte(umax(umax(colmax[0][k], colmax[1][k]), umax(colmax[2][k], colmax[3][k])));
         if (r == j && col + j < q.cols)
-          q.scales_t[(col + j) * kbt + tr] = static_cast<uint8_t>(cs[j]);
+          q.scales_t[tr * q.srt + col + j] = static_cast<uint8_t>(cs[j]);
       }
     }
   }
@@ -253,6 +253,7 @@ struct FewArgs {
   int64_t m, k, ldx;
   const uint8_t *w, *ws;
   int64_t n, kp;
+  int64_t ws_row, ws_block;  // distances between the scales of rows (>> w_shift) and of blocks
   int32_t kb, w_shift;
   void* out;
   int64_t ldo;
@@ -275,14 +276,14 @@ __global__ void __launch_bounds__(kFewWaves * kWave) few_rows_kernel(FewArgs g) 
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
   const int64_t wrow = n0 + r < g.n ? n0 + r : g.n - 1;
   const uint8_t* w = g.w + wrow * g.kp + h * 32;
-  const uint8_t* ws = g.ws + (wrow >> g.w_shift) * g.kb;
+  const uint8_t* ws = g.ws + (wrow >> g.w_shift) * g.ws_row;
   f32x4 acc[kFrags];
 #pragma unroll
   for (int f = 0; f < kFrags; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int b = wave; b < g.kb; b += kFewWaves) {
     const u32x4 w0 = *reinterpret_cast<const u32x4*>(w + static_cast<int64_t>(b) * kBlock);
     const u32x4 w1 = *reinterpret_cast<const u32x4*>(w + static_cast<int64_t>(b) * kBlock + 16);
-    const float wscale = scale_value(ws[b]);
+    const float wscale = scale_value(ws[b * g.ws_block]);
     bf16x8 wv[4] = {widen(w0[0], w0[1], wscale), widen(w0[2], w0[3], wscale),
                     widen(w1[0], w1[1], wscale), widen(w1[2], w1[3], wscale)};
 #pragma unroll
@@ -330,79 +331,162 @@ __global__ void __launch_bounds__(kFewWaves * kWave) few_rows_kernel(FewArgs g) 
 
 // ------------------------------------------------------------------ product
 
+// f(i, j) for all i < kA, j < kB, with the numbers as types (for operands that are literals).
+template <int kA, int kB, int kI = 0, typename F> __device__ __forceinline__ void each_pair(F&& f) {
+  if constexpr (kI < kA * kB) {
+    f(std::integral_constant<int, kI / kB>{}, std::integral_constant<int, kI % kB>{});
+    each_pair<kA, kB, kI + 1>(f);
+  }
+}
+
 struct GemmArgs {
   const uint8_t *a, *as, *b, *bs;
   int64_t m, n;
-  uint32_t kp;  // bytes per row of codes
-  int32_t kb;   // blocks along k
-  int32_t a_shift, b_shift;
+  uint32_t kp;                  // bytes per row of codes
+  int32_t kb;                   // blocks along k
+  uint32_t a_stride, b_stride;  // bytes between the scales of two blocks (kTilesB: of two tile rows)
+  uint32_t as_bytes, bs_bytes;  // bytes of scales
   void* out;
   int64_t ldo;
-  uint32_t wide;  // rows of out allow 16-byte stores
-  uint32_t tiles_m, tiles_n;
+  uint32_t wide;                // rows of out allow 16-byte stores
+  uint32_t tiles_m, tiles_n, splits;
+  int64_t split_stride;         // elements between the outputs of two splits
 };
 
-// 16 codes-bytes of this lane's part of rows, from memory into LDS without passing through
-// registers: lane l of the wave fills bytes 16 l .. 16 l + 15 from `lds` on.  Reads past the
-// buffer's end give 0.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t src, uint8_t* lds, uint32_t lane_offset,
-                                            uint32_t offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void*)lds, 16, lane_offset, offset, 0, 0);
+// The tile of a workgroup.  Consecutive workgroups go to the 8 XCDs in turn, each with its own L2:
+// every XCD takes one contiguous run of the tiles, in an order that walks kGroup tiles down before
+// the next one across, so that the tiles it has in work share rows of both operands.  Measured on
+// 8192 x 11008 x 4096: against one run over all XCDs 6 % faster, groups of 8 against 4 another 3-5 %.
+constexpr uint32_t kGroup = 8;
+struct TileAt {
+  uint32_t m, n, split;
+};
+__device__ __forceinline__ TileAt tile_at(uint32_t wg, uint32_t tiles_m, uint32_t tiles_n, uint32_t splits) {
+  const uint32_t tiles = tiles_m * tiles_n, all = tiles * splits;
+  const uint32_t xcd = wg % 8, each = all / 8, more = all % 8;
+  const uint32_t i = xcd * each + (xcd < more ? xcd : more) + wg / 8;
+  const uint32_t t = i % tiles, group = t / (kGroup * tiles_n), left = tiles_m - group * kGroup;
+  const uint32_t rows = left < kGroup ? left : kGroup, in = t % (kGroup * tiles_n);
+  return {group * kGroup + in % rows, in / rows, i / tiles};
 }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00027000);
+}
+// The code rows of one tile: at most `most` of them, 2^31 bytes or less.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint8_t* p, int64_t row0,
                                                               int64_t rows, int64_t most, uint32_t kp) {
   const int64_t left = rows - row0 < most ? rows - row0 : most;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + row0 * kp), 0,
-                                           static_cast<int>(static_cast<uint32_t>(left * kp)), 0x00027000);
+  return buffer(p + row0 * kp, static_cast<uint32_t>(left * kp));
 }
 
-// One workgroup per tile of kM x kN outputs, one step per block of 128 along k: the tiles'
-// code rows (128 bytes each) are loaded into one of two LDS buffers while the other one is
-// multiplied.  The 16-byte piece c of a row lies at place c ^ (row % 8), so that 8
-// consecutive rows' reads of one piece touch all banks once.
-template <int kM, int kN, int kWavesM, int kWavesN, bool kExact, typename OT>
+// kCount (1, 2 or 4) consecutive scale bytes; reads past the buffer's end give 0.
+template <int kCount>
+__device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src, uint32_t at) {
+  if constexpr (kCount == 4) return __builtin_amdgcn_raw_buffer_load_b32(src, at, 0, 0);
+  else if constexpr (kCount == 2) return __builtin_amdgcn_raw_buffer_load_b16(src, at, 0, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b8(src, at, 0, 0);
+}
+
+// One workgroup per tile of kM x kN outputs (and split of k), one step per block of 128 along k.
+//
+// A step's kM + kN rows of 128 codes are loaded from memory straight into one of two LDS buffers
+// (no registers), two steps ahead; its fragments are read from LDS half a step ahead, into one of
+// two register sets:
+//     multiply half 0 of step t   | read half 1 of step t
+//     wait: step t + 1 has landed, every wave has read all of step t (one barrier per step)
+//     multiply half 1 of step t   | read half 0 of step t + 1, start loading step t + 2
+// with the LDS reads and loads spread between the matrix instructions, which take 64 cycles each
+// (reads issued ahead of them in one go kept the matrix units waiting: 4 % slower).
+//
+// A wave's fragment i of 32 rows holds rows kF * r + i (r = 0 .. 31), so that the scales of a lane's
+// fragments are consecutive bytes: one load per operand and step, of which the matrix instruction
+// picks its byte.  (A byte load per fragment from scales laid out row by row touched 32 cache lines
+// each and cost a third of the time: 8192 x 4096 x 11008 at 1.7 PFLOP/s instead of 2.3.)  It also
+// leaves each lane with kFn * 4 consecutive columns of the result.
+// The 16-byte piece c of a row lies at place c ^ (row / kF % 8): 8 lanes that read one piece of
+// their rows touch all banks once.
+//
+// Measured (8-bit, 256 x 256 tiles of 8 waves): 8192 x 4096 x 11008 in 293 us, 2.52 PFLOP/s, of
+// which the matrix instructions alone take 206 us and the loads alone 280 us (193 us where the
+// operands lie in the last-level cache); three and four steps of 64 in flight were no faster, and
+// tiles of 4 waves of 128 x 128 6 % slower.
+template <int kM, int kN, int kWavesM, int kWavesN, bool kExact, bool kTilesB, typename OT>
 __global__ void __launch_bounds__(kWavesM* kWavesN* kWave) gemm_kernel(GemmArgs g) {
   constexpr int kWaves = kWavesM * kWavesN;
-  constexpr int kFm = kM / kWavesM / 32, kFn = kN / kWavesN / 32;  // fragments of 32 per wave
+  constexpr int kWm = kM / kWavesM, kWn = kN / kWavesN;  // a wave's part of the tile
+  constexpr int kFm = kWm / 32, kFn = kWn / 32;          // fragments of 32 per wave
+  constexpr int kShiftM = kFm == 4 ? 2 : kFm - 1, kShiftN = kFn == 4 ? 2 : kFn - 1;
   constexpr int kRows = kM + kN;
-  constexpr int kLoads = kRows / 8 / kWaves;                       // 8 rows per wave and load
+  constexpr int kLoads = kRows / 8 / kWaves;             // 8 rows per wave and load
   static_assert(kM % (8 * kWaves) == 0 && kN % (8 * kWaves) == 0, "whole loads per operand");
-  __shared__ __align__(16) uint8_t lds[2][kRows * kBlock];
+  static_assert((kFm == 1 || kFm == 2 || kFm == 4) && (kFn == 1 || kFn == 2 || kFn == 4), "scale loads");
+  static_assert(kBlock % kWn == 0 || !kTilesB, "a wave's columns lie in one tile of scales");
+  // the places that a lane's loads fill must not depend on the load: rows 8 * kWaves apart differ by
+  // a multiple of 8 in row / kF
+  static_assert((8 * kWaves >> kShiftM) % 8 == 0 && (8 * kWaves >> kShiftN) % 8 == 0, "places");
+  __shared__ __align__(16) uint8_t lds[2 * kRows * kBlock];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const uint32_t tile = blockIdx.x;
-  const int64_t m0 = static_cast<int64_t>(tile % g.tiles_m) * kM;
-  const int64_t n0 = static_cast<int64_t>(tile / g.tiles_m) * kN;
+  const TileAt tile = tile_at(blockIdx.x, g.tiles_m, g.tiles_n, g.splits);
+  const int64_t m0 = static_cast<int64_t>(tile.m) * kM, n0 = static_cast<int64_t>(tile.n) * kN;
+  // this split's steps
+  const int first = static_cast<int>(static_cast<int64_t>(g.kb) * tile.split / g.splits);
+  const int last = static_cast<int>(static_cast<int64_t>(g.kb) * (tile.split + 1) / g.splits) - 1;
+
   const __amdgpu_buffer_rsrc_t ra = rows_buffer(g.a, m0, g.m, kM, g.kp);
   const __amdgpu_buffer_rsrc_t rb = rows_buffer(g.b, n0, g.n, kN, g.kp);
-  const uint32_t piece = ((lane & 7) ^ (lane >> 3)) * 16;
-  auto load_step = [&](int buf, int b) {
+  const uint32_t row8 = wave * 8 + (lane >> 3);
+  const uint32_t piece_a = ((lane & 7) ^ ((row8 >> kShiftM) & 7)) * 16;
+  const uint32_t piece_b = ((lane & 7) ^ ((row8 >> kShiftN) & 7)) * 16;
+  // Lane l of a wave fills bytes 16 l .. 16 l + 15 of its 8 rows in LDS.  A row past the operand's
+  // last one lies past its buffer's end and reads as 0.
+  auto load_step = [&](int buf, int t) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int row = (i * kWaves + wave) * 8;  // first of the 8 rows of this load
+      const int row = (i * kWaves + wave) * 8;  // first of this load's 8 rows
       const bool is_a = i * kWaves * 8 < kM;
-      const uint32_t src_row = static_cast<uint32_t>((is_a ? row : row - kM) + (lane >> 3));
-      load_to_lds(is_a ? ra : rb, &lds[buf][row * kBlock], src_row * g.kp + piece,
-                  static_cast<uint32_t>(b) * kBlock);
+      const uint32_t from = static_cast<uint32_t>((is_a ? row : row - kM) + (lane >> 3)) * g.kp;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_void*)(lds + (buf * kRows + row) * kBlock), 16,
+                                               from + (is_a ? piece_a : piece_b), t * kBlock, 0, 0);
     }
   };
-  // scale bytes of this lane's rows
-  const uint8_t* sa[kFm];
-  const uint8_t* sb[kFn];
+
+  const __amdgpu_buffer_rsrc_t rsa = buffer(g.as, g.as_bytes), rsb = buffer(g.bs, g.bs_bytes);
+  const uint32_t sa = static_cast<uint32_t>(m0) + wm * kWm + kFm * (lane & 31);
+  const uint32_t sb = kTilesB ? static_cast<uint32_t>((n0 + wn * kWn) / kBlock) * g.b_stride
+                              : static_cast<uint32_t>(n0) + wn * kWn + kFn * (lane & 31);
+  struct Scales {
+    uint32_t a, b;  // byte i is fragment i's (kTilesB: byte 0 of b is every fragment's)
+  };
+  auto load_scales = [&](int t) {
+    return Scales{load_scale_bytes<kFm>(rsa, sa + t * g.a_stride),
+                  kTilesB ? load_scale_bytes<1>(rsb, sb + t) : load_scale_bytes<kFn>(rsb, sb + t * g.b_stride)};
+  };
+
+  const int h = lane >> 5;
+  const uint32_t at = ((2 * h) ^ (lane & 7)) << 4;
+  uint32_t oa = (wm * kWm + (lane & 31) * kFm) * kBlock + at;
+  uint32_t ob = (kM + wn * kWn + (lane & 31) * kFn) * kBlock + at;
+  struct Frags {
+    i32x4 a[kFm][2], b[kFn][2];
+  };
+  auto read_half = [&](Frags& f, int buf, int half) {
+    asm volatile("" : "+v"(oa), "+v"(ob));  // addresses are made anew, not kept in registers
+    const uint32_t a0 = (oa ^ (half * 64)) + buf * (kRows * kBlock), b0 = (ob ^ (half * 64)) + buf * (kRows * kBlock);
 #pragma unroll
-  for (int i = 0; i < kFm; ++i) {
-    int64_t row = m0 + (wm * kFm + i) * 32 + (lane & 31);
-    row = row < g.m ? row : g.m - 1;
-    sa[i] = g.as + (row >> g.a_shift) * g.kb;
-  }
+    for (int j = 0; j < kFn; ++j) {
+      f.b[j][0] = *reinterpret_cast<const i32x4*>(lds + b0 + j * kBlock);
+      f.b[j][1] = *reinterpret_cast<const i32x4*>(lds + (b0 ^ 16) + j * kBlock);
+    }
 #pragma unroll
-  for (int j = 0; j < kFn; ++j) {
-    int64_t row = n0 + (wn * kFn + j) * 32 + (lane & 31);
-    row = row < g.n ? row : g.n - 1;
-    sb[j] = g.bs + (row >> g.b_shift) * g.kb;
-  }
+    for (int i = 0; i < kFm; ++i) {
+      f.a[i][0] = *reinterpret_cast<const i32x4*>(lds + a0 + i * kBlock);
+      f.a[i][1] = *reinterpret_cast<const i32x4*>(lds + (a0 ^ 16) + i * kBlock);
+    }
+  };
+
   f32x16 acc[kFm][kFn];
 #pragma unroll
   for (int i = 0; i < kFm; ++i)
@@ -410,127 +494,137 @@ __global__ void __launch_bounds__(kWavesM* kWavesN* kWave) gemm_kernel(GemmArgs 
     for (int j = 0; j < kFn; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-
-  const int h = lane >> 5;
-  const uint32_t frag = (lane & 31) * kBlock + (((2 * h) ^ (lane & 7)) << 4);
-  load_step(0, 0);
-  int ca[kFm], cb[kFn];
+  auto multiply = [&](const Frags& f, const Scales& c) {
+    if constexpr (kExact) {
+      float va[kFm], vb[kFn];
 #pragma unroll
-  for (int i = 0; i < kFm; ++i) ca[i] = sa[i][0];
+      for (int i = 0; i < kFm; ++i) va[i] = scale_value((c.a >> (8 * i)) & 255);
 #pragma unroll
-  for (int j = 0; j < kFn; ++j) cb[j] = sb[j][0];
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  for (int b = 0; b < g.kb; ++b) {
-    const int buf = b & 1;
-    int na[kFm], nb[kFn];
-    const int next = b + 1 < g.kb ? b + 1 : b;
-    if (b + 1 < g.kb) load_step(buf ^ 1, next);
+      for (int j = 0; j < kFn; ++j) vb[j] = scale_value(kTilesB ? c.b : (c.b >> (8 * j)) & 255);
 #pragma unroll
-    for (int i = 0; i < kFm; ++i) na[i] = sa[i][next];
+      for (int e = 0; e < 4; ++e) {  // 8 codes each, in the same places of both operands
+        bf16x8 wa[kFm], wb[kFn];
 #pragma unroll
-    for (int j = 0; j < kFn; ++j) nb[j] = sb[j][next];
-    const uint8_t* pa = &lds[buf][wm * kFm * 32 * kBlock];
-    const uint8_t* pb = &lds[buf][(kM + wn * kFn * 32) * kBlock];
+        for (int i = 0; i < kFm; ++i)
+          wa[i] = widen(f.a[i][e >> 1][2 * (e & 1)], f.a[i][e >> 1][2 * (e & 1) + 1], va[i]);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {  // halves of 64 along k
-      i32x4 fa[kFm][2], fb[kFn][2];
-#pragma unroll
-      for (int i = 0; i < kFm; ++i) {
-        fa[i][0] = *reinterpret_cast<const i32x4*>(pa + i * 32 * kBlock + (frag ^ (s * 64)));
-        fa[i][1] = *reinterpret_cast<const i32x4*>(pa + i * 32 * kBlock + (frag ^ (s * 64) ^ 16));
-      }
-#pragma unroll
-      for (int j = 0; j < kFn; ++j) {
-        fb[j][0] = *reinterpret_cast<const i32x4*>(pb + j * 32 * kBlock + (frag ^ (s * 64)));
-        fb[j][1] = *reinterpret_cast<const i32x4*>(pb + j * 32 * kBlock + (frag ^ (s * 64) ^ 16));
-      }
-      if constexpr (kExact) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // 8 codes each, in the same places of both operands
-          bf16x8 va[kFm], vb[kFn];
-#pragma unroll
-          for (int i = 0; i < kFm; ++i)
-            va[i] = widen(fa[i][e >> 1][2 * (e & 1)], fa[i][e >> 1][2 * (e & 1) + 1], scale_value(ca[i]));
-#pragma unroll
-          for (int j = 0; j < kFn; ++j)
-            vb[j] = widen(fb[j][e >> 1][2 * (e & 1)], fb[j][e >> 1][2 * (e & 1) + 1], scale_value(cb[j]));
-#pragma unroll
-          for (int i = 0; i < kFm; ++i)
-#pragma unroll
-            for (int j = 0; j < kFn; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vb[j], va[i], acc[i][j], 0, 0, 0);
-        }
-      } else {
+        for (int j = 0; j < kFn; ++j)
+          wb[j] = widen(f.b[j][e >> 1][2 * (e & 1)], f.b[j][e >> 1][2 * (e & 1) + 1], vb[j]);
 #pragma unroll
         for (int i = 0; i < kFm; ++i)
 #pragma unroll
-          for (int j = 0; j < kFn; ++j) {
-            const i32x8 va = __builtin_shufflevector(fa[i][0], fa[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            const i32x8 vb = __builtin_shufflevector(fb[j][0], fb[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(vb, va, acc[i][j], 0, 0, 0,
-                                                                        cb[j], 0, ca[i]);
-          }
+          for (int j = 0; j < kFn; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
       }
+    } else {
+      each_pair<kFm, kFn>([&](auto i, auto j) {
+        constexpr int I = decltype(i)::value, J = decltype(j)::value;
+        const i32x8 wa = __builtin_shufflevector(f.a[I][0], f.a[I][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const i32x8 wb = __builtin_shufflevector(f.b[J][0], f.b[J][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        // formats 0: e4m3; the scale bytes are chosen by number
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wb, wa, acc[I][J], 0, 0, kTilesB ? 0 : J, c.b, I,
+                                                                    c.a);
+      });
     }
+  };
+  // The order of a half step's instructions: LDS reads and loads by threes between the matrix
+  // instructions.
+  constexpr int kMatrix = kFm * kFn * (kExact ? 4 : 1), kReads = 2 * (kFm + kFn);
+  auto spread = [&](bool loads) {
 #pragma unroll
-    for (int i = 0; i < kFm; ++i) ca[i] = na[i];
-#pragma unroll
-    for (int j = 0; j < kFn; ++j) cb[j] = nb[j];
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-  }
+    for (int i = 0; i < kMatrix; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < (kReads + 2) / 3) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+      if (loads) __builtin_amdgcn_sched_group_barrier(0x010, 3, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step_barrier = [&] {  // this wave's loads have landed and its reads are done; then all waves'
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
 
-  // Lane (r, h) holds row r of a fragment, columns 8 q + 4 h + (0 .. 3) for q = 0 .. 3.
-  OT* out = static_cast<OT*>(g.out);
+  auto upto_last = [&](int t) { return t < last ? t : last; };
+  Scales c0 = load_scales(first), c1 = load_scales(upto_last(first + 1));
+  load_step(0, first);
+  __builtin_amdgcn_sched_barrier(0);
+  step_barrier();
+  load_step(1, upto_last(first + 1));
+  Frags f0, f1;
+  read_half(f0, 0, 0);
+  for (int t = first; t <= last; ++t) {
+    // past the last step the last one is loaded again: no branch, which would keep the compiler from
+    // spreading the loads
+    const int buf = (t - first) & 1, ahead = upto_last(t + 2);
+    read_half(f1, buf, 1);
+    multiply(f0, c0);
+    spread(false);
+    step_barrier();
+    asm volatile("" : "+v"(c1.a), "+v"(c1.b));  // not used before the wait that it landed with
+    read_half(f0, buf ^ 1, 0);
+    const Scales c2 = load_scales(ahead);
+    load_step(buf, ahead);
+    multiply(f1, c0);
+    spread(true);
+    c0 = c1;
+    c1 = c2;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0070);  // no load is on its way into LDS when the workgroup ends
+
+  // Lane (r, h) holds row kFm r + i; its columns kFn (8 q + 4 h + e) + j for e = 0 .. 3 and all j are
+  // consecutive.
+  OT* out = static_cast<OT*>(g.out) + tile.split * g.split_stride;
 #pragma unroll
   for (int i = 0; i < kFm; ++i) {
-    const int64_t row = m0 + (wm * kFm + i) * 32 + (lane & 31);
-    const bool in = row < g.m;
-    OT* po = out + (in ? row : 0) * g.ldo;
+    const int64_t row = m0 + wm * kWm + kFm * (lane & 31) + i;
+    if (row < g.m) {
+      OT* po = out + row * g.ldo;
 #pragma unroll
-    for (int j = 0; j < kFn; ++j) {
-      const int64_t col0 = n0 + (wn * kFn + j) * 32;
-      if constexpr (sizeof(OT) == 4) {
+      for (int q = 0; q < 4; ++q) {
+        const int64_t col = n0 + wn * kWn + kFn * (8 * q + 4 * h);
+        float v[4 * kFn];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t col = col0 + 8 * q + 4 * h;
-          const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                           acc[i][j][4 * q + 3]};
-          if (in && g.wide && col + 4 <= g.n) {
-            *reinterpret_cast<f32x4*>(po + col) = v;
-          } else if (in) {
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (col + e < g.n) po[col + e] = v[e];
+          for (int j = 0; j < kFn; ++j) v[e * kFn + j] = acc[i][j][4 * q + e];
+        if (g.wide && col + 4 * kFn <= g.n) {
+          if constexpr (sizeof(OT) == 4) {
+#pragma unroll
+            for (int e = 0; e < kFn; ++e)
+              reinterpret_cast<f32x4*>(po + col)[e] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+          } else {
+            static_assert(sizeof(OT) == 4 || kFn >= 2, "8 bf16 values per store");
+#pragma unroll
+            for (int e = 0; e < 4 * kFn; e += 8)
+              *reinterpret_cast<u32x4*>(po + col + e) =
+                  u32x4{pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
+                        pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7])};
           }
-        }
-      } else {
-        // the halves of the wave exchange what they hold of two q, so that each lane has 8
-        // consecutive columns: 8 (q + h) on
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          uint32_t x[2], y[2];
-#pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            const uint32_t p0 = pack_bf16(acc[i][j][4 * q + 2 * d], acc[i][j][4 * q + 2 * d + 1]);
-            const uint32_t p1 = pack_bf16(acc[i][j][4 * q + 4 + 2 * d], acc[i][j][4 * q + 4 + 2 * d + 1]);
-            const auto sw = __builtin_amdgcn_permlane32_swap(p0, p1, false, false);
-            x[d] = sw[0];
-            y[d] = sw[1];
-          }
-          const int64_t col = col0 + 8 * (q + h);
-          const u32x4 v = {x[0], x[1], y[0], y[1]};
-          if (in && g.wide && col + 8 <= g.n) {
-            *reinterpret_cast<u32x4*>(po + col) = v;
-          } else if (in) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (col + e < g.n) po[col + e] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
-          }
+          for (int e = 0; e < 4 * kFn; ++e)
+            if (col + e < g.n) store1(po + col + e, v[e]);
         }
       }
     }
+  }
+}
+
+// out = the sum of `splits` binary32 partial results [m, ldp], in their order.
+template <typename OT>
+__global__ void __launch_bounds__(256) join_kernel(const float* part, int64_t m, int64_t n, int64_t ldp, int splits,
+                                                   OT* out, int64_t ldo) {
+  const int64_t quads = ldp / 4, all = m * quads;
+  for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < all; i += gridDim.x * int64_t{256}) {
+    const int64_t row = i / quads, col = (i % quads) * 4;
+    const float* p = part + row * ldp + col;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * m * ldp);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < n) store1(out + row * ldo + col + e, v[e]);
   }
 }
 
@@ -542,19 +636,24 @@ template <typename OT> __global__ void __launch_bounds__(256) zero_kernel(OT* ou
 
 // ------------------------------------------------------------------ host
 
+// Workgroups that one launch may hold (its threads, at most 512 each, are counted in 32 bits).
+constexpr int64_t kMaxGrid = int64_t{1} << 22;
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int launch_status() { return hipGetLastError() == hipSuccess ? QOPT_OK : QOPT_ELAUNCH; }
 bool bad_dim(int64_t d) { return d < 0 || d > QOPT_FP8_MAX_DIM; }
 bool bad_dtype(int d) { return d != QOPT_F32 && d != QOPT_BF16; }
 bool bad_form(int f) { return f != QOPT_FP8_ROWS && f != QOPT_FP8_TILES; }
 int64_t padded(int64_t d) { return ceil_div(d, kBlock) * kBlock; }
-
-// Workgroups of 256 threads that one launch may hold (its threads are counted in 32 bits).
-constexpr int64_t kMaxGrid = int64_t{1} << 23;
+// bytes between the scales of two blocks in QOPT_FP8_ROWS
+int64_t scale_stride(int64_t rows) { return ceil_div(rows, 16) * 16; }
+int64_t rows_scale_bytes(int64_t rows, int64_t cols) { return scale_stride(rows) * ceil_div(cols, kBlock); }
+bool too_many_tiles(int64_t rows, int64_t cols) {
+  return ceil_div(rows, kBlock) * ceil_div(cols, kBlock) > kMaxGrid;
+}
 
 template <typename XT, bool kTiles> int launch_quantize(const QuantArgs& q, hipStream_t s) {
   const int64_t tiles = q.tiles * ceil_div(q.rows, kBlock);
-  if (tiles > kMaxGrid) return QOPT_EINVAL;
   hipLaunchKernelGGL((quantize_kernel<XT, kTiles>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, q);
   return launch_status();
 }
@@ -566,14 +665,54 @@ template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t
   return launch_status();
 }
 
+// How a product is cut up: tiles of 256 x 256 or 128 x 128, and the splits of k.
+struct Plan {
+  bool big;
+  int splits;
+};
+
+// The plan of least time by this model, in microseconds on 256 CUs.  A step (128 along k) takes a CU
+//   1.70 for one tile of 256 x 256 (2.52 PFLOP/s with all CUs busy),
+//   1.06 for two tiles of 128 x 128 side by side (2.03), 0.70 for one;
+//   the exact path 1.67 and 0.96.
+// Small tiles cost a quarter more per product but fill the chip at a quarter of the size: 2048 x 11008
+// x 4096 takes 100 us with them (3 rounds of 1376 tiles) and 109 us with the big ones (2 rounds of
+// 344), 8192 x 4096 x 11008 363 us and 293 us.  Splitting k, for products of too few tiles, adds a
+// launch that joins the partial results (4) and their way to memory and back (4 TB/s).
+Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
+  const int64_t kb = ceil_div(k, kBlock);
+  const int64_t small = ceil_div(m, 128) * ceil_div(n, 128), large = ceil_div(m, 256) * ceil_div(n, 256);
+  const double two = exact ? 1.67 : 1.06, one = exact ? 0.96 : 0.70;
+  Plan best = {false, 1};
+  double least = 0;
+  for (int splits = 1; splits <= 16 && splits <= kb; splits *= 2) {
+    const int64_t wgs = small * splits, steps = ceil_div(kb, splits);
+    const int64_t rounds = wgs / 512, rest = wgs % 512;
+    double us = static_cast<double>(steps) * (rounds * two + (rest == 0 ? 0.0 : rest <= 256 ? one : two));
+    if (splits > 1) us += 4.0 + static_cast<double>(splits) * m * n * 8 / 4e6;
+    if (splits == 1 || us < least) {
+      least = us;
+      best.splits = splits;
+    }
+    if (wgs > 512) break;
+  }
+  if (!exact && static_cast<double>(kb) * ceil_div(large, 256) * 1.70 <= least) best = {true, 1};
+  return best;
+}
+
+int64_t partial_stride(int64_t n) { return ceil_div(n, 4) * 4; }
+
 template <int kM, int kN, int kWavesM, int kWavesN, bool kExact, typename OT>
-int launch_gemm(GemmArgs g, hipStream_t s) {
+int launch_gemm(GemmArgs g, bool b_tiles, hipStream_t s) {
   g.tiles_m = static_cast<uint32_t>(ceil_div(g.m, kM));
   g.tiles_n = static_cast<uint32_t>(ceil_div(g.n, kN));
-  const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
-  if (tiles > kMaxGrid) return QOPT_EINVAL;
-  hipLaunchKernelGGL((gemm_kernel<kM, kN, kWavesM, kWavesN, kExact, OT>), dim3(static_cast<unsigned>(tiles)),
-                     dim3(kWavesM * kWavesN * kWave), 0, s, g);
+  const int64_t wgs = static_cast<int64_t>(g.tiles_m) * g.tiles_n * g.splits;
+  if (wgs > kMaxGrid) return QOPT_EINVAL;
+  const dim3 grid(static_cast<unsigned>(wgs)), block(kWavesM * kWavesN * kWave);
+  if (b_tiles)
+    hipLaunchKernelGGL((gemm_kernel<kM, kN, kWavesM, kWavesN, kExact, true, OT>), grid, block, 0, s, g);
+  else
+    hipLaunchKernelGGL((gemm_kernel<kM, kN, kWavesM, kWavesN, kExact, false, OT>), grid, block, 0, s, g);
   return launch_status();
 }
 
@@ -604,6 +743,7 @@ extern "C" int qopt_fp8_quantize(const void* x_dev, int dtype, int64_t rows, int
   if (bad_dim(rows) || bad_dim(cols) || ldx < cols) return QOPT_EINVAL;
   if (bad_dtype(dtype) || bad_form(form)) return QOPT_EUNSUPPORTED;
   if (rows == 0 || cols == 0) return QOPT_OK;
+  if (too_many_tiles(rows, cols)) return QOPT_EINVAL;
   if (!x_dev || (!codes_dev) != (!scales_dev) || (!codes_t_dev) != (!scales_t_dev) ||
       (!codes_dev && !codes_t_dev))
     return QOPT_EINVAL;
@@ -611,6 +751,8 @@ extern "C" int qopt_fp8_quantize(const void* x_dev, int dtype, int64_t rows, int
   if (!aligned(x_dev, size) || !aligned(codes_dev, 16) || !aligned(codes_t_dev, 16)) return QOPT_EALIGN;
   const QuantArgs q = {x_dev, rows, cols, ldx, codes_dev, scales_dev, codes_t_dev, scales_t_dev,
                        padded(cols), padded(rows),
+                       form == QOPT_FP8_TILES ? ceil_div(cols, kBlock) : scale_stride(rows),
+                       form == QOPT_FP8_TILES ? ceil_div(rows, kBlock) : scale_stride(cols),
                        aligned(x_dev, 16) && (ldx * size) % 16 == 0 ? 1u : 0u,
                        static_cast<uint32_t>(ceil_div(cols, kBlock))};
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -624,42 +766,86 @@ extern "C" int qopt_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k, int ou
   if (!bytes || bad_dim(m) || bad_dim(n) || bad_dim(k)) return QOPT_EINVAL;
   if (bad_dtype(out_dtype)) return QOPT_EUNSUPPORTED;
   *bytes = 0;
+  if (m == 0 || n == 0 || k == 0) return QOPT_OK;
+  if (too_many_tiles(m, k) || too_many_tiles(n, k) || too_many_tiles(m, n)) return QOPT_EINVAL;
+  const Plan p = plan_for(m, n, k, out_dtype == QOPT_F32);
+  if (p.splits > 1) *bytes = static_cast<size_t>(p.splits) * m * partial_stride(n) * sizeof(float);
   return QOPT_OK;
 }
 
-extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int a_form,
+extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev,
                                const uint8_t* b_codes_dev, const uint8_t* b_scales_dev, int b_form,
                                int64_t m, int64_t n, int64_t k, void* out_dev, int out_dtype,
                                int64_t ldo, void* workspace_dev, size_t workspace_bytes, void* stream) {
   size_t need = 0;
   int rc = qopt_fp8_matmul_workspace(m, n, k, out_dtype, &need);
   if (rc != QOPT_OK) return rc;
-  if (bad_form(a_form) || bad_form(b_form)) return QOPT_EUNSUPPORTED;
+  if (bad_form(b_form)) return QOPT_EUNSUPPORTED;
   rc = check_out(out_dev, m, n, ldo, out_dtype);
   if (rc != QOPT_OK || m == 0 || n == 0) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (k == 0) return zero_out(out_dev, out_dtype, m, n, ldo, s);
   if (!a_codes_dev || !a_scales_dev || !b_codes_dev || !b_scales_dev) return QOPT_EINVAL;
-  if (!aligned(a_codes_dev, 16) || !aligned(b_codes_dev, 16) || !aligned(workspace_dev, 16)) return QOPT_EALIGN;
+  if (!aligned(a_codes_dev, 16) || !aligned(b_codes_dev, 16) || !aligned(a_scales_dev, 4) ||
+      !aligned(b_scales_dev, 4) || !aligned(workspace_dev, 16))
+    return QOPT_EALIGN;
   if (need > 0 && (!workspace_dev || workspace_bytes < need)) return QOPT_EINVAL;
-  const size_t osize = out_dtype == QOPT_F32 ? 4 : 2;
-  const GemmArgs g = {a_codes_dev, a_scales_dev, b_codes_dev, b_scales_dev, m, n,
-                      static_cast<uint32_t>(padded(k)), static_cast<int32_t>(ceil_div(k, kBlock)),
-                      a_form == QOPT_FP8_TILES ? 7 : 0, b_form == QOPT_FP8_TILES ? 7 : 0, out_dev, ldo,
-                      aligned(out_dev, 16) && (ldo * osize) % 16 == 0 ? 1u : 0u, 0, 0};
-  if (out_dtype == QOPT_F32) return launch_gemm<128, 128, 2, 2, true, float>(g, s);
-  return launch_gemm<128, 128, 2, 2, false, uint16_t>(g, s);
+  const bool exact = out_dtype == QOPT_F32, tiles = b_form == QOPT_FP8_TILES;
+  const Plan plan = plan_for(m, n, k, exact);
+  const size_t osize = exact ? 4 : 2;
+  const int64_t kb = ceil_div(k, kBlock);
+  GemmArgs g = {};
+  g.a = a_codes_dev;
+  g.as = a_scales_dev;
+  g.b = b_codes_dev;
+  g.bs = b_scales_dev;
+  g.m = m;
+  g.n = n;
+  g.kp = static_cast<uint32_t>(padded(k));
+  g.kb = static_cast<int32_t>(kb);
+  g.a_stride = static_cast<uint32_t>(scale_stride(m));
+  g.b_stride = static_cast<uint32_t>(tiles ? kb : scale_stride(n));
+  g.as_bytes = static_cast<uint32_t>(rows_scale_bytes(m, k));
+  g.bs_bytes = static_cast<uint32_t>(tiles ? ceil_div(n, kBlock) * kb : rows_scale_bytes(n, k));
+  g.splits = static_cast<uint32_t>(plan.splits);
+  if (plan.splits > 1) {
+    g.out = workspace_dev;
+    g.ldo = partial_stride(n);
+    g.split_stride = m * g.ldo;
+    g.wide = 1;
+    rc = exact ? launch_gemm<128, 128, 2, 2, true, float>(g, tiles, s)
+               : launch_gemm<128, 128, 2, 2, false, float>(g, tiles, s);
+    if (rc != QOPT_OK) return rc;
+    const int64_t wgs = ceil_div(m * (g.ldo / 4), 256);
+    const dim3 grid(static_cast<unsigned>(wgs < 4096 ? wgs : 4096));
+    const float* part = static_cast<const float*>(workspace_dev);
+    if (exact)
+      hipLaunchKernelGGL(join_kernel<float>, grid, dim3(256), 0, s, part, m, n, g.ldo, plan.splits,
+                         static_cast<float*>(out_dev), ldo);
+    else
+      hipLaunchKernelGGL(join_kernel<uint16_t>, grid, dim3(256), 0, s, part, m, n, g.ldo, plan.splits,
+                         static_cast<uint16_t*>(out_dev), ldo);
+    return launch_status();
+  }
+  g.out = out_dev;
+  g.ldo = ldo;
+  g.wide = aligned(out_dev, 16) && (ldo * osize) % 16 == 0 ? 1u : 0u;
+  if (exact) return launch_gemm<128, 128, 2, 2, true, float>(g, tiles, s);
+  return plan.big ? launch_gemm<256, 256, 2, 4, false, uint16_t>(g, tiles, s)
+                  : launch_gemm<128, 128, 2, 2, false, uint16_t>(g, tiles, s);
 }
+
+namespace {
+// The codes of x and its scales at the start of qopt_fp8_linear's workspace, in multiples of 16 bytes.
+size_t linear_codes_bytes(int64_t m, int64_t k) { return static_cast<size_t>(m) * padded(k); }
+size_t linear_own_bytes(int64_t m, int64_t k) { return linear_codes_bytes(m, k) + rows_scale_bytes(m, k); }
+}  // namespace
 
 extern "C" int qopt_fp8_linear_workspace(int64_t m, int64_t n, int64_t k, int out_dtype, size_t* bytes) {
   const int rc = qopt_fp8_matmul_workspace(m, n, k, out_dtype, bytes);
   if (rc != QOPT_OK) return rc;
-  if (m <= QOPT_FP8_FEW_ROWS || n == 0) {
-    *bytes = 0;
-    return QOPT_OK;
-  }
-  // the codes of x, its scales (rounded up to 16 bytes), the product's own workspace
-  *bytes += static_cast<size_t>(m) * padded(k) + static_cast<size_t>(ceil_div(m * (padded(k) / kBlock), 16)) * 16;
+  if (m <= QOPT_FP8_FEW_ROWS || n == 0 || k == 0) *bytes = 0;
+  else *bytes += linear_own_bytes(m, k);
   return QOPT_OK;
 }
 
@@ -678,20 +864,22 @@ extern "C" int qopt_fp8_linear(const void* x_dev, int dtype, int64_t m, int64_t 
   if (k == 0) return zero_out(out_dev, out_dtype, m, n, ldo, s);
   if (!x_dev || !w_codes_dev || !w_scales_dev) return QOPT_EINVAL;
   const size_t size = dtype == QOPT_F32 ? 4 : 2;
-  if (!aligned(x_dev, size) || !aligned(w_codes_dev, 16) || !aligned(workspace_dev, 16)) return QOPT_EALIGN;
+  if (!aligned(x_dev, size) || !aligned(w_codes_dev, 16) || !aligned(w_scales_dev, 4) || !aligned(workspace_dev, 16))
+    return QOPT_EALIGN;
   if (need > 0 && (!workspace_dev || workspace_bytes < need)) return QOPT_EINVAL;
+  const bool tiles = w_form == QOPT_FP8_TILES;
   if (m > QOPT_FP8_FEW_ROWS) {
     uint8_t* codes = static_cast<uint8_t*>(workspace_dev);
-    uint8_t* scales = codes + m * padded(k);
+    uint8_t* scales = codes + linear_codes_bytes(m, k);
     rc = qopt_fp8_quantize(x_dev, dtype, m, k, ldx, QOPT_FP8_ROWS, codes, scales, nullptr, nullptr, stream);
     if (rc != QOPT_OK) return rc;
-    const size_t used = static_cast<size_t>(m) * padded(k) +
-                        static_cast<size_t>(ceil_div(m * (padded(k) / kBlock), 16)) * 16;
-    return qopt_fp8_matmul(codes, scales, QOPT_FP8_ROWS, w_codes_dev, w_scales_dev, w_form, m, n, k, out_dev,
-                           out_dtype, ldo, codes + used, workspace_bytes - used, stream);
+    const size_t used = linear_own_bytes(m, k);
+    return qopt_fp8_matmul(codes, scales, w_codes_dev, w_scales_dev, w_form, m, n, k, out_dev, out_dtype, ldo,
+                           codes + used, workspace_bytes - used, stream);
   }
-  const FewArgs g = {x_dev, m, k, ldx, w_codes_dev, w_scales_dev, n, padded(k),
-                     static_cast<int32_t>(ceil_div(k, kBlock)), w_form == QOPT_FP8_TILES ? 7 : 0, out_dev, ldo,
+  const int64_t kb = ceil_div(k, kBlock);
+  const FewArgs g = {x_dev, m, k, ldx, w_codes_dev, w_scales_dev, n, padded(k), tiles ? kb : 1,
+                     tiles ? 1 : scale_stride(n), static_cast<int32_t>(kb), tiles ? 7 : 0, out_dev, ldo,
                      aligned(x_dev, 16) && (ldx * size) % 16 == 0 ? 1u : 0u};
   if (dtype == QOPT_F32)
     return out_dtype == QOPT_F32 ? launch_few<float, float>(g, s) : launch_few<float, uint16_t>(g, s);

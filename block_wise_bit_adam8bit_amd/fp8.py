@@ -25,8 +25,9 @@ CODE_DTYPE = torch.float8_e4m3fn
 
 class Fp8Matrix(NamedTuple):
     """A quantized matrix: float8_e4m3fn codes [rows, columns up to a multiple of 128] and
-    uint8 scales, each standing for 2^(scale - 127): [rows, columns / 128], or one per tile
-    of 128 x 128, [ceil(rows / 128), columns / 128]."""
+    uint8 scales, each standing for 2^(scale - 127): one per 128 values of a row,
+    [columns / 128, rows up to a multiple of 16], or one per tile of 128 x 128,
+    [ceil(rows / 128), columns / 128]."""
     codes: torch.Tensor
     scales: torch.Tensor
 
@@ -70,19 +71,23 @@ def _quantized(codes, scales, what):
     if codes.dim() != 2 or codes.shape[1] % QOPT_FP8_BLOCK:
         raise ValueError(f"{what}: codes must be 2-D with a multiple of {QOPT_FP8_BLOCK} columns")
     rows, kb = codes.shape[0], codes.shape[1] // QOPT_FP8_BLOCK
-    if tuple(scales.shape) not in ((rows, kb), (_blocks(rows), kb)):
-        raise ValueError(f"{what}: scales must be {(rows, kb)} or {(_blocks(rows), kb)}, not "
+    by_rows, by_tiles = (kb, -(-rows // 16) * 16), (_blocks(rows), kb)
+    if tuple(scales.shape) not in (by_rows, by_tiles):
+        raise ValueError(f"{what}: scales must be {by_rows} or {by_tiles}, not "
                          f"{tuple(scales.shape)}")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{what}: codes and scales must be contiguous")
-    return QOPT_FP8_ROWS if scales.shape[0] == rows else QOPT_FP8_TILES
+    # the two shapes differ for every matrix with elements: rows <= 16 has 16 columns in the
+    # first and one row in the second, more rows have fewer than rows / 16 tiles
+    return QOPT_FP8_ROWS if tuple(scales.shape) == by_rows else QOPT_FP8_TILES
 
 
 def _empty_matrix(rows, cols, tiles, device):
     kb = _blocks(cols)
     return Fp8Matrix(
         torch.empty(rows, kb * QOPT_FP8_BLOCK, dtype=CODE_DTYPE, device=device),
-        torch.empty(_blocks(rows) if tiles else rows, kb, dtype=torch.uint8, device=device))
+        torch.empty((_blocks(rows), kb) if tiles else (kb, -(-rows // 16) * 16),
+                    dtype=torch.uint8, device=device))
 
 
 def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
@@ -124,11 +129,13 @@ def _output(out, shape, dtype, dev):
 
 
 def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, *, out=None):
-    """a b^T of two quantized matrices [m, k] and [n, k] (either form each): [m, n] in
-    ``out_dtype`` (bfloat16 or float32), into ``out`` if given."""
+    """a b^T of two quantized matrices [m, k] (scales by rows) and [n, k] (by rows or tiles):
+    [m, n] in ``out_dtype`` (bfloat16 or float32), into ``out`` if given."""
     fa, fb = _quantized(a_codes, a_scales, "a"), _quantized(b_codes, b_scales, "b")
     dt = _check_dtype(out_dtype, "out_dtype")
     (m, k), n = a_codes.shape, b_codes.shape[0]
+    if fa != QOPT_FP8_ROWS:
+        raise ValueError("a must have its scales by rows")
     if b_codes.shape[1] != k:
         raise ValueError("a and b must have the same number of columns")
     dev = _same_gpu(a_codes, a_scales, b_codes, b_scales)
@@ -137,7 +144,7 @@ def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat
     ldo = _row_stride(out, "out")
     with torch.cuda.device(dev):
         ws = _workspace(LIB.qopt_fp8_matmul_workspace, "qopt_fp8_matmul_workspace", m, n, k, dt, dev)
-        rc = LIB.qopt_fp8_matmul(a_codes.data_ptr(), a_scales.data_ptr(), fa, b_codes.data_ptr(),
+        rc = LIB.qopt_fp8_matmul(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
                                  b_scales.data_ptr(), fb, m, n, k, out.data_ptr(), dt, ldo,
                                  None if ws is None else ws.data_ptr(),
                                  0 if ws is None else ws.numel(), _lib.stream_handle(dev))

@@ -13,7 +13,9 @@
  *           the bytes behind a row's end 0;
  *   scales  one byte s (0 .. 247) per block, standing for 2^(s - 127):
  *           QOPT_FP8_ROWS   a block is 128 consecutive values of a row:
- *                           [rows, kp / 128]
+ *                           [kp / 128, rp], rp = rows rounded up to a multiple of 16: the
+ *                           scales of consecutive rows lie side by side, as a product
+ *                           reads them (those from rows on are not read for a result)
  *           QOPT_FP8_TILES  a block is a tile of 128 x 128 values:
  *                           [ceil(rows / 128), kp / 128]
  * An element is the value of its code times its block's 2^(s - 127).
@@ -24,7 +26,7 @@
  * of the current HIP device, caller-owned buffers, host-side argument checks before
  * anything is enqueued, asynchronous work on `stream`).  Every entry point may be
  * captured into a graph.  Sizes are at most QOPT_FP8_MAX_DIM each, and a matrix of
- * more than 2^23 tiles of 128 x 128 is refused (QOPT_EINVAL).
+ * more than 2^22 tiles of 128 x 128 is refused (QOPT_EINVAL).
  */
 #ifndef QOPT_FP8_H
 #define QOPT_FP8_H
@@ -57,7 +59,7 @@ typedef enum { QOPT_FP8_ROWS = 0, QOPT_FP8_TILES = 1 } qopt_fp8_form;
  *   codes_t_dev, scales_t_dev  its transpose [cols, rows] in `form`, or both NULL
  *                              (blocks along the rows of the transpose; the tiles of
  *                              QOPT_FP8_TILES are the same ones, so their codes are too).
- * Codes are 16-byte aligned.  rows or cols 0: nothing is written.
+ * Codes are 16-byte aligned.  The outputs must not overlap x or each other.  rows or cols 0: nothing is written.
  * Errors: QOPT_EINVAL (null x with elements, no output or half of one, sizes negative
  * or too large, ldx < cols), QOPT_EUNSUPPORTED (dtype, form), QOPT_EALIGN, QOPT_ELAUNCH.
  */
@@ -67,8 +69,9 @@ int qopt_fp8_quantize(const void* x_dev, int dtype, int64_t rows, int64_t cols, 
 
 /*
  * out[i, j] = sum over l < k of A[i, l] * B[j, l]: the product of a quantized A [m, k]
- * with the transpose of a quantized B [n, k].  Sums are binary32 and rounded once, to
- * out_dtype, and their order is fixed: equal calls give equal bits.
+ * with the transpose of a quantized B [n, k], A in QOPT_FP8_ROWS and B in `b_form`.  Sums
+ * are binary32 and rounded once, to out_dtype, and their order is fixed: equal calls give
+ * equal bits.  Codes are 16-byte aligned, scales 4-byte.
  *   out_dtype QOPT_BF16: 8-bit matrix instructions, which align the 64 products of one
  *     step to the largest of them and keep about 18 bits of each: within 2^-15 of the
  *     result's size, an eighth of half a bf16 step or less.
@@ -82,7 +85,7 @@ int qopt_fp8_quantize(const void* x_dev, int dtype, int64_t rows, int64_t cols, 
  * m or n 0: nothing is written; k 0: out is all 0.
  * Errors as for qopt_fp8_quantize, and QOPT_EINVAL for a workspace that is too small.
  */
-int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int a_form,
+int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev,
                     const uint8_t* b_codes_dev, const uint8_t* b_scales_dev, int b_form, int64_t m,
                     int64_t n, int64_t k, void* out_dev, int out_dtype, int64_t ldo,
                     void* workspace_dev, size_t workspace_bytes, void* stream);

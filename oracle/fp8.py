@@ -53,7 +53,7 @@ def _pad(x, r, c):
 
 
 def quantize(x, tiles=False):
-    """(codes [rows, padded columns], scales) of a 2-D array, laid out as the library's."""
+    """(codes [rows, padded columns], scales [rows, blocks] or [tile rows, blocks]) of a 2-D array."""
     x = np.asarray(x, dtype=np.float64)
     rows = x.shape[0]
     r = KBLOCK if tiles else 1

@@ -42,7 +42,11 @@ def host(t):
 
 
 def pair(m):
-    return host(m.codes), host(m.scales)
+    """Codes and scales as the oracle lays them out: [rows, blocks] or [tile rows, blocks]."""
+    codes, scales = host(m.codes), host(m.scales)
+    rows, kb = codes.shape[0], codes.shape[1] // 128
+    by_rows = scales.shape == (kb, -(-rows // 16) * 16)
+    return codes, scales.T[:rows] if by_rows else scales
 
 
 def reals(rng, rows, cols, dtype):
@@ -149,22 +153,25 @@ def test_quantize_rounds_every_midpoint(q):
 
 # ------------------------------------------------------------------ products
 
+# one tile, ragged tiles, products that split k (long, few tiles), and ones of big tiles (the last
+# three: enough tiles of 256 x 256 to be worth it)
 MNK = [(1, 1, 1), (33, 31, 129), (128, 128, 128), (129, 257, 300), (40, 1000, 520), (300, 200, 4096),
-       (513, 260, 640), (256, 512, 1152), (700, 36, 96)]
+       (513, 260, 640), (256, 512, 1152), (700, 36, 96), (65, 130, 9000), (2300, 7000, 130),
+       (4096, 4096, 256), (4000, 4100, 640)]
 
 
-@pytest.mark.parametrize("forms", [(False, False), (False, True), (True, True)])
+@pytest.mark.parametrize("tiles", [False, True])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("m,n,k", MNK)
-def test_matmul(q, m, n, k, dtype, forms):
-    say(f"matmul {m}x{n}x{k} {dtype} tiles {forms}")
+def test_matmul(q, m, n, k, dtype, tiles):
+    say(f"matmul {m}x{n}x{k} {dtype} tiles {tiles}")
     rng = np.random.default_rng(m + n + k)
-    a = q.qopt_fp8_quantize(integers(rng, m, k, F32), tiles=forms[0])
-    b = q.qopt_fp8_quantize(integers(rng, n, k, F32), tiles=forms[1])
+    a = q.qopt_fp8_quantize(integers(rng, m, k, F32))
+    b = q.qopt_fp8_quantize(integers(rng, n, k, F32), tiles=tiles)
     got = host(q.qopt_fp8_matmul(*a, *b, dtype))
     assert np.array_equal(got, rounded(fp8.matmul(pair(a), pair(b))[0], dtype)), "integers"
-    a = q.qopt_fp8_quantize(reals(rng, m, k, F32), tiles=forms[0])
-    b = q.qopt_fp8_quantize(reals(rng, n, k, F32), tiles=forms[1])
+    a = q.qopt_fp8_quantize(reals(rng, m, k, F32))
+    b = q.qopt_fp8_quantize(reals(rng, n, k, F32), tiles=tiles)
     got = q.qopt_fp8_matmul(*a, *b, dtype)
     want, tol = bound(pair(a), pair(b), dtype, dtype == F32)
     err = np.abs(host(got) - want)
@@ -202,7 +209,7 @@ def test_nan_stays_in_its_row_and_column(q, dtype):
 
 def test_empty_products(q):
     z = lambda r, k: q.Fp8Matrix(torch.empty(r, k, dtype=torch.float8_e4m3fn, device="cuda"),  # noqa: E731
-                                 torch.empty(r, k // 128, dtype=torch.uint8, device="cuda"))
+                                 torch.empty(k // 128, -(-r // 16) * 16, dtype=torch.uint8, device="cuda"))
     assert q.qopt_fp8_matmul(*z(0, 128), *z(5, 128)).shape == (0, 5)
     assert q.qopt_fp8_matmul(*z(5, 128), *z(0, 128)).shape == (5, 0)
     for dtype in (F32, BF16):
@@ -268,9 +275,9 @@ def test_past_32_bit_offsets(q):
     g = torch.Generator(device="cuda").manual_seed(1)
     codes = torch.randint(0, 4, (n, k), dtype=torch.uint8, device="cuda", generator=g).mul_(8).add_(0x30)
     codes = codes.view(torch.float8_e4m3fn)
-    scales = torch.full((n, k // 128), 120, dtype=torch.uint8, device="cuda")
+    scales = torch.randint(118, 122, (k // 128, n), dtype=torch.uint8, device="cuda", generator=g)
     spots = [0, 1000, (1 << 20) - 1, 1 << 20, n - 1]
-    part = (host(codes[spots]), host(scales[spots]))
+    part = (host(codes[spots]), host(scales[:, spots].t()))
     rng = np.random.default_rng(2)
     for m in (2, 2100):
         x = integers(rng, m, k, BF16, 2)

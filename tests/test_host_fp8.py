@@ -38,16 +38,17 @@ def test_quantize_checks():
 
 
 def test_matmul_checks():
-    def call(a=P, sa=P, fa=0, b=P, sb=P, fb=0, m=4, n=8, k=256, out=P, dt=1, ldo=8, ws=None, nws=0):
-        return L.qopt_fp8_matmul(a, sa, fa, b, sb, fb, m, n, k, out, dt, ldo, ws, nws, None)
+    def call(a=P, sa=P, b=P, sb=P, fb=0, m=4, n=8, k=256, out=P, dt=1, ldo=8, ws=None, nws=0):
+        return L.qopt_fp8_matmul(a, sa, b, sb, fb, m, n, k, out, dt, ldo, ws, nws, None)
 
     assert call(m=0) == OK and call(n=0, ldo=0, out=None) == OK
     for bad in (dict(m=-1), dict(n=-1), dict(k=-1), dict(ldo=7), dict(a=None), dict(sa=None),
                 dict(b=None), dict(sb=None), dict(out=None), dict(k=_lib.QOPT_FP8_MAX_DIM + 1)):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(dt=2), dict(fa=2), dict(fb=-1)):
+    for bad in (dict(dt=2), dict(fb=2), dict(fb=-1)):
         assert call(**bad) == EUNSUPPORTED, bad
-    for bad in (dict(a=P + 8), dict(b=P + 4), dict(out=P + 1), dict(out=P + 2, dt=0), dict(ws=P + 8)):
+    for bad in (dict(a=P + 8), dict(b=P + 4), dict(out=P + 1), dict(out=P + 2, dt=0), dict(ws=P + 8),
+                dict(sa=P + 2), dict(sb=P + 1)):
         assert call(**bad) == EALIGN, bad
 
 
@@ -61,7 +62,7 @@ def test_linear_checks():
         assert call(**bad) == EINVAL, bad
     for bad in (dict(dt=3), dict(odt=3), dict(f=2)):
         assert call(**bad) == EUNSUPPORTED, bad
-    for bad in (dict(x=P + 1), dict(x=P + 2, dt=0), dict(w=P + 8), dict(out=P + 1),
+    for bad in (dict(x=P + 1), dict(x=P + 2, dt=0), dict(w=P + 8), dict(sw=P + 2), dict(out=P + 1),
                 dict(m=33, ws=P + 8, nws=1 << 30)):
         assert call(**bad) == EALIGN, bad
 
@@ -76,7 +77,8 @@ def test_workspace_queries():
         assert q(4, 4, 4, 9, ctypes.byref(n)) == EUNSUPPORTED
     assert L.qopt_fp8_linear_workspace(32, 512, 300, 1, ctypes.byref(n)) == OK and n.value == 0
     assert L.qopt_fp8_linear_workspace(33, 512, 300, 1, ctypes.byref(n)) == OK
-    assert n.value >= 33 * 384 + 33 * 3
+    assert n.value >= 33 * 384 + 48 * 3
+    assert q(1 << 23, 1 << 23, 128, 1, ctypes.byref(n)) == EINVAL  # too many tiles of results
 
 
 def test_wrappers_refuse_what_is_not_a_matrix_on_a_gpu():
