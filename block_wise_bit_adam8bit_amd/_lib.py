@@ -231,3 +231,18 @@ def check(fn, status):
 def stream_handle(device=None):
     """hipStream_t of torch's current stream on ``device`` (as an int)."""
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def call(name, device, *args):
+    """LIB.name(*args, stream) on torch's current stream of ``device``, with that device
+    current; raises QoptError unless it returns QOPT_OK.  (torch.cuda.device and
+    current_stream make objects; a call that is already on its device goes without them:
+    13 us instead of 20 for a small product.)"""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = getattr(LIB, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = getattr(LIB, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != QOPT_OK:
+        raise QoptError(name, status)

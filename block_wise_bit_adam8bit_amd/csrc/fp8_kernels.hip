@@ -45,57 +45,92 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
   const int s = static_cast<int>(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return amax == 0 ? 127u : static_cast<uint32_t>(s < 0 ? 0 : s);
 }
-// 2^-e and 2^e of a scale byte e + 127 (0 .. 247) as binary32; 2^-127 is subnormal.
-__device__ __forceinline__ float inverse_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+// 2^e of a scale byte e + 127 (0 .. 247) as binary32; 2^-127 is subnormal.
 __device__ __forceinline__ float scale_value(uint32_t s) {
-  return __uint_as_float(s == 0 ? 0x400000u : s << 23);  // 255 gives infinity: see widen
+  return __uint_as_float(s == 0 ? 0x400000u : s << 23);
 }
 
-// |x| for a block maximum: infinities and NaN do not count.
-__device__ __forceinline__ uint32_t finite_magnitude(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-  return u < 0x7F800000u ? u : 0u;
-}
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x, int d) { return static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), d)); }
 
-// Four values scaled by a power of two (exact; what falls below binary32's range is far
-// below e4m3's least step) and rounded to e4m3, ties to even: 4 code bytes.  No finite
-// value of a block exceeds 448 here, so nothing saturates; infinities and NaN come out
-// as NaN codes.
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
-  return static_cast<uint32_t>(w);
+// Consecutive elements of a row as they are kept in registers: bf16 in pairs, binary32 by
+// themselves.  `Max` is a running maximum of magnitudes over any of them: for bf16 of both halves
+// of a register at once, as 16-bit integers, whose order is that of the magnitudes.  Infinities and
+// NaN lie above every finite value and do not count for a block's scale; they are rare, so they
+// are looked for once the maximum is known (`finite`), and only a block that holds one is gone
+// over again (`finite_only`).
+template <typename XT> struct Elements;
+
+template <> struct Elements<uint16_t> {
+  static constexpr int kPer = 2;  // elements per register
+  typedef uint32_t Reg;
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  static __device__ __forceinline__ uint32_t magnitude(uint32_t x) { return x & 0x7FFF7FFFu; }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+  }
+  static __device__ __forceinline__ uint32_t both(uint32_t m) { return max(m, m >> 16) & 0xFFFFu; }
+  static __device__ __forceinline__ uint32_t finite_only(uint32_t x) {
+    const uint32_t lo = x & 0x7FFFu, hi = x & 0x7FFF0000u;
+    return (lo < 0x7F80u ? lo : 0u) | (hi < 0x7F800000u ? hi : 0u);
+  }
+  static constexpr uint32_t kInf = 0x7F80u;
+  static __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m) { return m << 16; }
+};
+
+template <> struct Elements<float> {
+  static constexpr int kPer = 1;
+  typedef float Reg;
+  static __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) { return umax(a, b); }
+  static __device__ __forceinline__ uint32_t both(uint32_t m) { return m; }
+  static __device__ __forceinline__ uint32_t finite_only(float x) {
+    const uint32_t u = magnitude(x);
+    return u < kInf ? u : 0u;
+  }
+  static constexpr uint32_t kInf = 0x7F800000u;
+  static __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m) { return m; }
+};
+
+// Four elements over a power of two, rounded to e4m3, ties to even: 4 code bytes.  One instruction
+// per pair; it agrees with multiplying by 2^-e and rounding on every bf16 (checked on the hardware).
+// No finite value of a block exceeds 448 2^e, so nothing saturates; infinities and NaN come out as
+// NaN codes.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t encode4(uint32_t ab, uint32_t cd, float scale) {
+  s16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2, ab), scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2, cd), scale, true);
+  return __builtin_bit_cast(uint32_t, w);
+}
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float scale) {
+  s16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, w);
 }
 
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
-
-// Eight consecutive elements of a row; those from `left` on are 0.
-template <typename XT>
-__device__ __forceinline__ void load8(const XT* p, bool wide, int64_t left, float x[8]) {
-  if (wide && left >= 8) {
-    if constexpr (sizeof(XT) == 4) {
-      const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+// kCount (a multiple of 8) consecutive elements of a row; those from `left` on are 0.
+template <typename XT, int kCount>
+__device__ __forceinline__ void load_row(const XT* p, bool wide, int64_t left,
+                                         typename Elements<XT>::Reg (&x)[kCount / Elements<XT>::kPer]) {
+  if (wide && left >= kCount) {
+    constexpr int kWide = 16 / sizeof(XT) / Elements<XT>::kPer;  // registers per 16 bytes: 4
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = a[j];
-        x[4 + j] = b[j];
-      }
-    } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(p);
+    for (int i = 0; i < kCount / Elements<XT>::kPer / kWide; ++i) {
+      typedef typename Elements<XT>::Reg Quad __attribute__((ext_vector_type(4)));
+      const Quad q = reinterpret_cast<const Quad*>(p)[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[2 * j] = bf16_to_f32(a[j] & 0xFFFFu);
-        x[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
-      }
+      for (int j = 0; j < kWide; ++j) x[kWide * i + j] = q[j];
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = 0.0f;
-      if (j < left) {
-        if constexpr (sizeof(XT) == 4) x[j] = p[j];
-        else x[j] = bf16_to_f32(p[j]);
+    for (int j = 0; j < kCount / Elements<XT>::kPer; ++j) {
+      if constexpr (sizeof(XT) == 4) {
+        x[j] = j < left ? p[j] : 0.0f;
+      } else {
+        const uint32_t lo = 2 * j < left ? p[2 * j] : 0u, hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
+        x[j] = lo | hi << 16;
       }
     }
   }
@@ -113,12 +148,18 @@ struct QuantArgs {
   uint32_t tiles;   // tiles along a row
 };
 
+// Rows r and r + 1 of one column of bf16 pairs, as a pair.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
 // One workgroup per tile of 128 x 128: thread (r, c) of 16 x 16 holds rows 8r .. 8r + 7 of
 // columns 8c .. 8c + 7, so every row of the tile is read in whole 16-byte pieces, a row's
 // code bytes are 8 bytes per thread, and a column's 8 rows are one 8-byte write into the
 // transposed tile in LDS.
 template <typename XT, bool kTiles>
 __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
+  typedef Elements<XT> E;
+  constexpr int kRegs = 8 / E::kPer;  // registers per 8 elements
   __shared__ __align__(16) u32x2 tile[kBlock * 16];  // [column][16 groups of 8 rows]
   __shared__ uint32_t colmax[4][kBlock];
   const int t = threadIdx.x, c = t & 15, r = t >> 4, wave = t / kWave;
@@ -127,38 +168,44 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
   const int64_t col0 = static_cast<int64_t>(tc) * kBlock;
   const int64_t col = col0 + 8 * c;
   const XT* x = static_cast<const XT*>(q.x);
-  float v[8][8];
-  uint32_t rmax[8];
+  typename E::Reg v[8][kRegs];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = row0 + 8 * r + i;
-    load8<XT>(x + (row < q.rows ? row : 0) * q.ldx + col, q.wide != 0,
-              row < q.rows ? q.cols - col : 0, v[i]);
+    load_row<XT, 8>(x + (row < q.rows ? row : 0) * q.ldx + col, q.wide != 0, row < q.rows ? q.cols - col : 0, v[i]);
   }
-  uint32_t cmax[8];
+  uint32_t rmax[8], cmax[kRegs];  // cmax: of a pair of columns for bf16
+  auto maxima = [&](auto magnitude) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cmax[j] = 0;
+    for (int j = 0; j < kRegs; ++j) cmax[j] = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    rmax[i] = 0;
+    for (int i = 0; i < 8; ++i) {
+      rmax[i] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t m = finite_magnitude(v[i][j]);
-      rmax[i] = umax(rmax[i], m);
-      cmax[j] = umax(cmax[j], m);
+      for (int j = 0; j < kRegs; ++j) {
+        const uint32_t m = magnitude(v[i][j]);
+        rmax[i] = E::max(rmax[i], m);
+        cmax[j] = E::max(cmax[j], m);
+      }
+      rmax[i] = E::both(rmax[i]);
     }
-  }
+  };
+  maxima([](typename E::Reg e) { return E::magnitude(e); });
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = umax(top, rmax[i]);
+  if (top >= E::kInf) maxima([](typename E::Reg e) { return E::finite_only(e); });
   uint32_t rs[8], cs[8];
   if constexpr (kTiles) {
-    uint32_t m = 0;
+    top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = umax(m, rmax[i]);
+    for (int i = 0; i < 8; ++i) top = umax(top, rmax[i]);
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) m = umax(m, __shfl_xor(m, d));
-    if ((t & 63) == 0) colmax[0][wave] = m;
+    for (int d = 1; d < kWave; d *= 2) top = umax(top, lane_xor(top, d));
+    if ((t & 63) == 0) colmax[0][wave] = top;
     __syncthreads();
-    m = umax(umax(colmax[0][0], colmax[0][1]), umax(colmax[0][2], colmax[0][3]));
-    const uint32_t s = scale_byte(m);
+    top = umax(umax(colmax[0][0], colmax[0][1]), umax(colmax[0][2], colmax[0][3]));
+    const uint32_t s = scale_byte(E::as_f32_bits(top));
 #pragma unroll
     for (int i = 0; i < 8; ++i) rs[i] = cs[i] = s;
     if (t == 0) {
@@ -166,30 +213,41 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
       if (q.codes_t) q.scales_t[tc * q.srt + tr] = static_cast<uint8_t>(s);
     }
   } else {
+    if (q.codes) {
+      uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {
 #pragma unroll
-      for (int d = 1; d < 16; d *= 2) rmax[i] = umax(rmax[i], __shfl_xor(rmax[i], d));
-      rs[i] = scale_byte(rmax[i]);
-      const int64_t row = row0 + 8 * r + i;
-      if (q.codes && c == i && row < q.rows)
-        q.scales[tc * q.sr + row] = static_cast<uint8_t>(rs[i]);
+        for (int d = 1; d < 16; d *= 2) rmax[i] = umax(rmax[i], lane_xor(rmax[i], d));
+        rs[i] = scale_byte(E::as_f32_bits(rmax[i]));
+        mine = c == i ? rs[i] : mine;
+      }
+      const int64_t row = row0 + 8 * r + c;  // thread c of a row group stores row c's
+      if (c < 8 && row < q.rows) q.scales[tc * q.sr + row] = static_cast<uint8_t>(mine);
     }
     if (q.codes_t) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        cmax[j] = umax(cmax[j], __shfl_xor(cmax[j], 16));
-        cmax[j] = umax(cmax[j], __shfl_xor(cmax[j], 32));
-        if ((t & 63) < 16) colmax[wave][8 * c + j] = cmax[j];
+      for (int j = 0; j < kRegs; ++j) {
+        cmax[j] = E::max(cmax[j], lane_xor(cmax[j], 16));
+        cmax[j] = E::max(cmax[j], lane_xor(cmax[j], 32));
+        if ((t & 63) < 16) colmax[wave][kRegs * c + j] = cmax[j];
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = 8 * c + j;
-        cs[j] = scale_byte(umax(umax(colmax[0][k], colmax[1][k]), umax(colmax[2][k], colmax[3][k])));
-        if (r == j && col + j < q.cols)
-          q.scales_t[tr * q.srt + col + j] = static_cast<uint8_t>(cs[j]);
+      for (int j = 0; j < kRegs; ++j) {
+        const int k = kRegs * c + j;
+        const uint32_t m = E::max(E::max(colmax[0][k], colmax[1][k]), E::max(colmax[2][k], colmax[3][k]));
+        if constexpr (E::kPer == 2) {
+          cs[2 * j] = scale_byte(m << 16);
+          cs[2 * j + 1] = scale_byte(m & 0xFFFF0000u);
+        } else {
+          cs[j] = scale_byte(m);
+        }
       }
+      uint32_t mine = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mine = r == j ? cs[j] : mine;
+      if (r < 8 && col + r < q.cols) q.scales_t[tr * q.srt + col + r] = static_cast<uint8_t>(mine);
     }
   }
   if (q.codes) {
@@ -197,9 +255,13 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
     for (int i = 0; i < 8; ++i) {
       const int64_t row = row0 + 8 * r + i;
       if (row < q.rows) {
-        const float inv = inverse_scale(rs[i]);
-        const u32x2 w = {encode4(v[i][0], v[i][1], v[i][2], v[i][3], inv),
-                         encode4(v[i][4], v[i][5], v[i][6], v[i][7], inv)};
+        const float scale = scale_value(rs[i]);
+        u32x2 w;
+        if constexpr (E::kPer == 2)
+          w = u32x2{encode4(v[i][0], v[i][1], scale), encode4(v[i][2], v[i][3], scale)};
+        else
+          w = u32x2{encode4(v[i][0], v[i][1], v[i][2], v[i][3], scale),
+                    encode4(v[i][4], v[i][5], v[i][6], v[i][7], scale)};
         *reinterpret_cast<u32x2*>(q.codes + row * q.kp + col) = w;
       }
     }
@@ -209,9 +271,18 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
     // 16 different columns at one j, and so to 16 different places (all 32 banks).
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float inv = inverse_scale(cs[j]);
-      const u32x2 w = {encode4(v[0][j], v[1][j], v[2][j], v[3][j], inv),
-                       encode4(v[4][j], v[5][j], v[6][j], v[7][j], inv)};
+      const float scale = scale_value(cs[j]);
+      u32x2 w;
+      if constexpr (E::kPer == 2) {
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[i] = j & 1 ? high_halves(v[2 * i][j / 2], v[2 * i + 1][j / 2]) : low_halves(v[2 * i][j / 2], v[2 * i + 1][j / 2]);
+        w = u32x2{encode4(p[0], p[1], scale), encode4(p[2], p[3], scale)};
+      } else {
+        w = u32x2{encode4(v[0][j], v[1][j], v[2][j], v[3][j], scale),
+                  encode4(v[4][j], v[5][j], v[6][j], v[7][j], scale)};
+      }
       tile[(8 * c + j) * 16 + (r ^ c)] = w;
     }
     __syncthreads();
@@ -248,83 +319,185 @@ template <typename OT> __device__ __forceinline__ void store1(OT* p, float x) {
 
 // ------------------------------------------------------------------ few rows
 
+// Memory by 32-bit offsets; reads past its end give 0 and go nowhere.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00027000);
+}
+constexpr uint32_t kPastEnd = 0x80000000u;  // past the end of every buffer that it is used with (2^31 bytes or less)
+
 struct FewArgs {
   const void* x;
   int64_t m, k, ldx;
   const uint8_t *w, *ws;
-  int64_t n, kp;
-  int64_t ws_row, ws_block;  // distances between the scales of rows (>> w_shift) and of blocks
+  int64_t n;
+  uint32_t kp, x_bytes, ws_bytes;
+  uint32_t ws_row, ws_block;  // distances between the scales of rows (>> w_shift) and of blocks
   int32_t kb, w_shift;
   void* out;
   int64_t ldo;
-  uint32_t wide;
 };
 
-constexpr int kFewWaves = 8;
+// Waves per workgroup by the runs of 16 weight rows that it takes: measured 4 against 8, 1 row of
+// 4096 x 4096 (one run) 7.6 and 6.7 us, 24 rows of 11008 x 4096 (three) 16.0 and 17.2 us.
+constexpr int few_waves(int runs) { return runs == 1 ? 8 : 4; }
 
 // x w^T for at most 16 * kFrags rows of x: the time of reading the weights.  A workgroup owns
-// 16 rows of w; its waves take turns at the blocks of 128 along k, and their sums are added
-// in LDS in the order of the waves.  Lane (r, h) holds 32 consecutive codes of weight row r,
-// and quantizes the same 32 places of row r of x in registers (a block's maximum is a
-// maximum over 4 lanes), so nothing but the weights is read from memory more than once per
-// workgroup and there is no launch before this one.
-template <typename XT, typename OT, int kFrags>
-__global__ void __launch_bounds__(kFewWaves * kWave) few_rows_kernel(FewArgs g) {
-  __shared__ f32x4 sums[kFewWaves][kFrags][kWave];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
+// 16 * kRuns rows of w; its waves take turns at the blocks of 128 along k, and their sums are added
+// in LDS in the order of the waves.  Lane (r, h) holds 32 consecutive codes of weight row r, and
+// quantizes the same 32 places of row r of x in registers (a block's maximum is a maximum over 4
+// lanes), so there is no launch before this one.
+// The weights' bytes bound it at the rate of memory; what a workgroup adds to that is reading x from
+// the L2 and quantizing it anew.  Measured (bf16, repeated in a graph, 2.3 us of it the launch): 1 row
+// of 4096 x 4096 6.7 us, 1 of 11008 x 4096 10.8 us (4.2 TB/s), 24 of it 16.0 us, 7 of 50257 x 2048
+// 26.9 us (3.8 TB/s).
+// Nothing in the loop branches: what lies past k, past the last block or past the last row is read
+// past the end of a buffer, as 0, and a lane without a row of x takes the last one's values, which
+// no result uses.  (With branches around the loads the compiler waited for each before the next.)
+// kWide: rows of x are read in pieces of 16 bytes, of which k is a multiple.
+template <typename XT, typename OT, int kFrags, int kRuns, bool kWide>
+__global__ void __launch_bounds__(few_waves(kRuns) * kWave) few_rows_kernel(FewArgs g) {
+  typedef Elements<XT> E;
+  typedef typename E::Reg Reg;
+  constexpr int kFewWaves = few_waves(kRuns);
+  constexpr int kRegs = 32 / E::kPer;
+  constexpr bool kExact = sizeof(OT) == 4;
+  __shared__ f32x4 sums[kFewWaves][kFrags * kRuns][kWave];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, h = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const int64_t wrow = n0 + r < g.n ? n0 + r : g.n - 1;
-  const uint8_t* w = g.w + wrow * g.kp + h * 32;
-  const uint8_t* ws = g.ws + (wrow >> g.w_shift) * g.ws_row;
-  f32x4 acc[kFrags];
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * kRuns);
+  const int64_t rows = g.n - n0 < 16 * kRuns ? g.n - n0 : 16 * kRuns;
+  const __amdgpu_buffer_rsrc_t bx = buffer(g.x, g.x_bytes), bs = buffer(g.ws, g.ws_bytes);
+  const __amdgpu_buffer_rsrc_t bw = buffer(g.w + n0 * g.kp, static_cast<uint32_t>(rows * g.kp));
+  const uint32_t k = static_cast<uint32_t>(g.k);
+  uint32_t ws[kRuns], xs[kFrags];
 #pragma unroll
-  for (int f = 0; f < kFrags; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b = wave; b < g.kb; b += kFewWaves) {
-    const u32x4 w0 = *reinterpret_cast<const u32x4*>(w + static_cast<int64_t>(b) * kBlock);
-    const u32x4 w1 = *reinterpret_cast<const u32x4*>(w + static_cast<int64_t>(b) * kBlock + 16);
-    const float wscale = scale_value(ws[b * g.ws_block]);
-    bf16x8 wv[4] = {widen(w0[0], w0[1], wscale), widen(w0[2], w0[3], wscale),
-                    widen(w1[0], w1[1], wscale), widen(w1[2], w1[3], wscale)};
+  for (int i = 0; i < kRuns; ++i) ws[i] = (static_cast<uint32_t>(n0 + 16 * i + r) >> g.w_shift) * g.ws_row;
+#pragma unroll
+  for (int f = 0; f < kFrags; ++f)
+    xs[f] = static_cast<uint32_t>((f * 16 + r < g.m ? f * 16 + r : g.m - 1) * g.ldx * static_cast<int64_t>(sizeof(XT)));
+  f32x4 acc[kFrags][kRuns];
+#pragma unroll
+  for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) acc[f][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // A wave's blocks go through kAhead register sets in turn: a set is loaded again as soon as its
+  // block is multiplied, so that the loads of kAhead blocks are on their way at the start and
+  // kAhead - 1 all along.
+  struct Block {
+    Reg x[kFrags][kRegs];
+    i32x4 c[kRuns][2];
+    uint32_t s[kRuns];
+  };
+  constexpr int kAhead = 2;  // 4 measured 7.9 us against 6.7 (1 row of 4096 x 4096)
+  auto load = [&](Block& v, int b) {
+    const uint32_t col = static_cast<uint32_t>(b) * kBlock + h * 32;
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
-      const int64_t row = f * 16 + r, col = static_cast<int64_t>(b) * kBlock + h * 32;
-      const XT* x = static_cast<const XT*>(g.x) + (row < g.m ? row : 0) * g.ldx + col;
-      const int64_t left = row < g.m ? g.k - col : 0;
-      float v[4][8];
+      if constexpr (kWide) {
+        constexpr int kPiece = 16 / sizeof(XT);  // elements
+        typedef Reg Quad __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int i = 0; i < 32 / kPiece; ++i) {
+          const uint32_t at = col + i * kPiece;
+          const Quad q = __builtin_bit_cast(Quad, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      bx, at < k ? xs[f] + at * sizeof(XT) : kPastEnd, 0, 0));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v.x[f][4 * i + j] = q[j];
+        }
+      } else {
+        auto one = [&](uint32_t at) { return at < k ? xs[f] + at * static_cast<uint32_t>(sizeof(XT)) : kPastEnd; };
+#pragma unroll
+        for (int j = 0; j < kRegs; ++j) {
+          if constexpr (E::kPer == 2) {
+            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(bx, one(col + 2 * j), 0, 0);
+            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(bx, one(col + 2 * j + 1), 0, 0);
+            v.x[f][j] = (lo & 0xFFFFu) | hi << 16;
+          } else {
+            v.x[f][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bx, one(col + j), 0, 0));
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      const uint32_t at = b < g.kb ? (16 * i + r) * g.kp + col : kPastEnd;
+      v.c[i][0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bw, at, 0, 0));
+      v.c[i][1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bw, at, 16, 0));
+      v.s[i] = __builtin_amdgcn_raw_buffer_load_b8(bs, ws[i] + static_cast<uint32_t>(b) * g.ws_block, 0, 0);
+    }
+  };
+  auto multiply = [&](const Block& v) {
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+      const auto& x = v.x[f];
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        load8<XT>(x + 8 * i, g.wide != 0, left - 8 * i, v[i]);
+      for (int i = 0; i < kRegs; ++i) m = E::max(m, E::magnitude(x[i]));
+      m = E::both(m);
+      if (m >= E::kInf) {
+        m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = umax(m, finite_magnitude(v[i][j]));
+        for (int i = 0; i < kRegs; ++i) m = E::max(m, E::finite_only(x[i]));
+        m = E::both(m);
       }
-      m = umax(m, __shfl_xor(m, 16));
-      m = umax(m, __shfl_xor(m, 32));
-      const uint32_t s = scale_byte(m);
-      const float inv = inverse_scale(s), xscale = scale_value(s);
+      m = umax(m, lane_xor(m, 16));
+      m = umax(m, lane_xor(m, 32));
+      const uint32_t s = scale_byte(E::as_f32_bits(m));
+      const float scale = scale_value(s);
+      uint32_t code[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = encode4(v[i][0], v[i][1], v[i][2], v[i][3], inv);
-        const uint32_t hi = encode4(v[i][4], v[i][5], v[i][6], v[i][7], inv);
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(lo, hi, xscale), wv[i], acc[f], 0, 0, 0);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (E::kPer == 2) code[i] = encode4(x[2 * i], x[2 * i + 1], scale);
+        else code[i] = encode4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], scale);
       }
+      if constexpr (kExact) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bf16x8 xv = widen(code[2 * e], code[2 * e + 1], scale);
+#pragma unroll
+          for (int i = 0; i < kRuns; ++i) {
+            const bf16x8 wv = widen(v.c[i][e >> 1][2 * (e & 1)], v.c[i][e >> 1][2 * (e & 1) + 1], scale_value(v.s[i]));
+            acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv, acc[f][i], 0, 0, 0);
+          }
+        }
+      } else {
+        i32x8 xv;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xv[i] = static_cast<int>(code[i]);
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+          const i32x8 wv = __builtin_shufflevector(v.c[i][0], v.c[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          acc[f][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xv, wv, acc[f][i], 0, 0, 0, s, 0, v.s[i]);
+        }
+      }
+    }
+  };
+  Block set[kAhead];
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) load(set[d], wave + d * kFewWaves);
+  for (int b0 = wave; b0 < g.kb; b0 += kAhead * kFewWaves) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      multiply(set[d]);  // of a block past the last one: zeros
+      load(set[d], b0 + (kAhead + d) * kFewWaves);
     }
   }
 #pragma unroll
-  for (int f = 0; f < kFrags; ++f) sums[wave][f][lane] = acc[f];
+  for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) sums[wave][f * kRuns + i][lane] = acc[f][i];
   __syncthreads();
-  // acc[f][i] of lane (r, h) is row 16 f + 4 h + i, column r
-  for (int e = threadIdx.x; e < kFrags * kWave; e += kFewWaves * kWave) {
-    const int f = e / kWave, l = e & 63;
-    f32x4 a = sums[0][f][l];
+  // acc[f][i][e] of lane (r, h) is row 16 f + 4 h + e, column 16 i + r
+  for (int a = threadIdx.x; a < kFrags * kRuns * kWave; a += kFewWaves * kWave) {
+    const int p = a / kWave, l = a & 63;
+    f32x4 v = sums[0][p][l];
 #pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) a += sums[v][f][l];
-    const int64_t col = n0 + (l & 15);
+    for (int u = 1; u < kFewWaves; ++u) v += sums[u][p][l];
+    const int64_t col = n0 + (p % kRuns) * 16 + (l & 15);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = f * 16 + 4 * (l >> 4) + i;
-      if (row < g.m && col < g.n) store1(static_cast<OT*>(g.out) + row * g.ldo + col, a[i]);
+    for (int e = 0; e < 4; ++e) {
+      const int64_t row = (p / kRuns) * 16 + 4 * (l >> 4) + e;
+      if (row < g.m && col < g.n) store1(static_cast<OT*>(g.out) + row * g.ldo + col, v[e]);
     }
   }
 }
@@ -370,9 +543,6 @@ __device__ __forceinline__ TileAt tile_at(uint32_t wg, uint32_t tiles_m, uint32_
   return {group * kGroup + in % rows, in / rows, i / tiles};
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00027000);
-}
 // The code rows of one tile: at most `most` of them, 2^31 bytes or less.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint8_t* p, int64_t row0,
                                                               int64_t rows, int64_t most, uint32_t kp) {
@@ -658,11 +828,35 @@ template <typename XT, bool kTiles> int launch_quantize(const QuantArgs& q, hipS
   return launch_status();
 }
 
-template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(g.n, 16)));
-  if (g.m <= 16) hipLaunchKernelGGL((few_rows_kernel<XT, OT, 1>), grid, dim3(kFewWaves * kWave), 0, s, g);
-  else hipLaunchKernelGGL((few_rows_kernel<XT, OT, 2>), grid, dim3(kFewWaves * kWave), 0, s, g);
+template <typename XT, typename OT, int kRuns, bool kWide> int launch_few_runs(const FewArgs& g, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(g.n, 16 * kRuns))), block(few_waves(kRuns) * kWave);
+  if (g.m <= 16) hipLaunchKernelGGL((few_rows_kernel<XT, OT, 1, kRuns, kWide>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((few_rows_kernel<XT, OT, 2, kRuns, kWide>), grid, block, 0, s, g);
   return launch_status();
+}
+
+// More weight rows per workgroup let more of them share one reading of x, fewer fill the chip more
+// evenly.  The time goes by what a CU has to read, per column of k: its rounds of workgroups times
+// their rows of weights and of x.  Measured for 24 rows of 11008 x 4096, 1 to 4 runs of 16: 31.9, 23.4,
+// 16.0 and 17.5 us; for 1 row of 4096 x 4096 6.7, 8.3, 9.9 and 11.7 us; the rule takes the least of each.
+template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t s) {
+  const bool wide = aligned(g.x, 16) && (g.ldx * sizeof(XT)) % 16 == 0 && (g.k * sizeof(XT)) % 16 == 0;
+  if (!wide) return launch_few_runs<XT, OT, 2, false>(g, s);  // bound by loads of single elements
+  int runs = 1;
+  int64_t least = 0;
+  for (int r = 1; r <= 4; ++r) {
+    const int64_t bytes = ceil_div(ceil_div(g.n, 16 * r), 256) * (16 * r + g.m * static_cast<int64_t>(sizeof(XT)));
+    if (r == 1 || bytes < least) {
+      least = bytes;
+      runs = r;
+    }
+  }
+  switch (runs) {
+    case 1: return launch_few_runs<XT, OT, 1, true>(g, s);
+    case 2: return launch_few_runs<XT, OT, 2, true>(g, s);
+    case 3: return launch_few_runs<XT, OT, 3, true>(g, s);
+    default: return launch_few_runs<XT, OT, 4, true>(g, s);
+  }
 }
 
 // How a product is cut up: tiles of 256 x 256 or 128 x 128, and the splits of k.
@@ -868,6 +1062,8 @@ extern "C" int qopt_fp8_linear(const void* x_dev, int dtype, int64_t m, int64_t 
     return QOPT_EALIGN;
   if (need > 0 && (!workspace_dev || workspace_bytes < need)) return QOPT_EINVAL;
   const bool tiles = w_form == QOPT_FP8_TILES;
+  // the few rows' kernel addresses x by 31-bit offsets
+  if (m <= QOPT_FP8_FEW_ROWS && ldx > QOPT_FP8_MAX_DIM) return QOPT_EINVAL;
   if (m > QOPT_FP8_FEW_ROWS) {
     uint8_t* codes = static_cast<uint8_t*>(workspace_dev);
     uint8_t* scales = codes + linear_codes_bytes(m, k);
@@ -878,9 +1074,11 @@ extern "C" int qopt_fp8_linear(const void* x_dev, int dtype, int64_t m, int64_t 
                            codes + used, workspace_bytes - used, stream);
   }
   const int64_t kb = ceil_div(k, kBlock);
-  const FewArgs g = {x_dev, m, k, ldx, w_codes_dev, w_scales_dev, n, padded(k), tiles ? kb : 1,
-                     tiles ? 1 : scale_stride(n), static_cast<int32_t>(kb), tiles ? 7 : 0, out_dev, ldo,
-                     aligned(x_dev, 16) && (ldx * size) % 16 == 0 ? 1u : 0u};
+  const FewArgs g = {x_dev, m, k, ldx, w_codes_dev, w_scales_dev, n, static_cast<uint32_t>(padded(k)),
+                     static_cast<uint32_t>(((m - 1) * ldx + k) * static_cast<int64_t>(size)),
+                     static_cast<uint32_t>(tiles ? ceil_div(n, kBlock) * kb : rows_scale_bytes(n, k)),
+                     static_cast<uint32_t>(tiles ? kb : 1), static_cast<uint32_t>(tiles ? 1 : scale_stride(n)),
+                     static_cast<int32_t>(kb), tiles ? 7 : 0, out_dev, ldo};
   if (dtype == QOPT_F32)
     return out_dtype == QOPT_F32 ? launch_few<float, float>(g, s) : launch_few<float, uint16_t>(g, s);
   return out_dtype == QOPT_F32 ? launch_few<uint16_t, float>(g, s) : launch_few<uint16_t, uint16_t>(g, s);

@@ -15,8 +15,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._lib import (LIB, QOPT_BF16, QOPT_F32, QOPT_FP8_BLOCK, QOPT_FP8_FEW_ROWS, QOPT_FP8_ROWS,
-                   QOPT_FP8_TILES)
+from ._lib import (LIB, QOPT_BF16, QOPT_F32, QOPT_FP8_BLOCK, QOPT_FP8_FEW_ROWS,
+                   QOPT_FP8_MAX_DIM, QOPT_FP8_ROWS, QOPT_FP8_TILES)
 from .embedding import qopt_embedding_xavier_init
 
 _DT = {torch.float32: QOPT_F32, torch.bfloat16: QOPT_BF16}
@@ -90,6 +90,50 @@ def _empty_matrix(rows, cols, tiles, device):
                     dtype=torch.uint8, device=device))
 
 
+# The launches behind the functions below, for operands that are known to be right.
+
+def _quantize(x, dt, ldx, tiles, normal, transposed):
+    rows, cols = x.shape
+    dev = x.device
+    a = _empty_matrix(rows, cols, tiles, dev) if normal else None
+    b = _empty_matrix(cols, rows, tiles, dev) if transposed else None
+    if rows and cols:
+        _lib.call("qopt_fp8_quantize", dev, x.data_ptr(), dt, rows, cols, ldx,
+                  QOPT_FP8_TILES if tiles else QOPT_FP8_ROWS,
+                  *((a.codes.data_ptr(), a.scales.data_ptr()) if normal else (None, None)),
+                  *((b.codes.data_ptr(), b.scales.data_ptr()) if transposed else (None, None)))
+    return a, b
+
+
+def _workspace(query, name, m, n, k, dt, dev):
+    """(tensor or None, pointer, bytes)"""
+    need = ctypes.c_size_t(0)
+    _lib.check(name, query(m, n, k, dt, ctypes.byref(need)))
+    if not need.value:
+        return None, None, 0
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    return ws, ws.data_ptr(), need.value
+
+
+def _matmul(a, b, form, out, dt, ldo):
+    (m, k), n = a.codes.shape, b.codes.shape[0]
+    dev = out.device
+    ws, ptr, size = _workspace(LIB.qopt_fp8_matmul_workspace, "qopt_fp8_matmul_workspace", m, n, k, dt, dev)
+    _lib.call("qopt_fp8_matmul", dev, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+              b.scales.data_ptr(), form, m, n, k, out.data_ptr(), dt, ldo, ptr, size)
+    return out
+
+
+def _linear(x, dx, m, k, ldx, w, form, out, do, ldo):
+    n, dev = w.codes.shape[0], out.device
+    ws, ptr, size = None, None, 0
+    if m > QOPT_FP8_FEW_ROWS:
+        ws, ptr, size = _workspace(LIB.qopt_fp8_linear_workspace, "qopt_fp8_linear_workspace", m, n, k, do, dev)
+    _lib.call("qopt_fp8_linear", dev, x.data_ptr(), dx, m, k, ldx, w.codes.data_ptr(),
+              w.scales.data_ptr(), form, n, out.data_ptr(), do, ldo, ptr, size)
+    return out
+
+
 def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
     """Quantize a 2-D float32 or bfloat16 tensor in blocks of 128 along its rows, or in
     tiles of 128 x 128 (``tiles``).  Returns the Fp8Matrix of x (``normal``), of its transpose
@@ -99,33 +143,24 @@ def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
     if not normal and not transposed:
         raise ValueError("nothing to return")
     dt = _check_dtype(x.dtype, "x")
-    dev = _same_gpu(x)
-    ldx = _row_stride(x, "x")
-    rows, cols = x.shape
-    a = _empty_matrix(rows, cols, tiles, dev) if normal else None
-    b = _empty_matrix(cols, rows, tiles, dev) if transposed else None
-    if rows and cols:
-        ptrs = [None if m is None else t.data_ptr() for m in (a, b) for t in (m or (None, None))]
-        with torch.cuda.device(dev):
-            rc = LIB.qopt_fp8_quantize(x.data_ptr(), dt, rows, cols, ldx,
-                                       QOPT_FP8_TILES if tiles else QOPT_FP8_ROWS, *ptrs,
-                                       _lib.stream_handle(dev))
-        _lib.check("qopt_fp8_quantize", rc)
+    _same_gpu(x)
+    a, b = _quantize(x, dt, _row_stride(x, "x"), tiles, normal, transposed)
     return (a, b) if normal and transposed else a if normal else b
 
 
-def _workspace(query, name, m, n, k, dt, dev):
-    need = ctypes.c_size_t(0)
-    _lib.check(name, query(m, n, k, dt, ctypes.byref(need)))
-    return torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-
-
 def _output(out, shape, dtype, dev):
+    """The output tensor and the distance of its rows."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev), shape[-1]
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"out must have shape {tuple(shape)} and dtype {dtype}")
-    return out
+    if out.device != dev:
+        raise ValueError("all tensors must be on the same GPU")
+    if out.dim() == 2:
+        return out, _row_stride(out, "out")
+    if not out.is_contiguous():
+        raise ValueError("out must be 2-D with contiguous rows, or contiguous")
+    return out, shape[-1]
 
 
 def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, *, out=None):
@@ -133,23 +168,13 @@ def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat
     [m, n] in ``out_dtype`` (bfloat16 or float32), into ``out`` if given."""
     fa, fb = _quantized(a_codes, a_scales, "a"), _quantized(b_codes, b_scales, "b")
     dt = _check_dtype(out_dtype, "out_dtype")
-    (m, k), n = a_codes.shape, b_codes.shape[0]
     if fa != QOPT_FP8_ROWS:
         raise ValueError("a must have its scales by rows")
-    if b_codes.shape[1] != k:
+    if b_codes.shape[1] != a_codes.shape[1]:
         raise ValueError("a and b must have the same number of columns")
     dev = _same_gpu(a_codes, a_scales, b_codes, b_scales)
-    out = _output(out, torch.Size((m, n)), out_dtype, dev)
-    _same_gpu(a_codes, out)
-    ldo = _row_stride(out, "out")
-    with torch.cuda.device(dev):
-        ws = _workspace(LIB.qopt_fp8_matmul_workspace, "qopt_fp8_matmul_workspace", m, n, k, dt, dev)
-        rc = LIB.qopt_fp8_matmul(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
-                                 b_scales.data_ptr(), fb, m, n, k, out.data_ptr(), dt, ldo,
-                                 None if ws is None else ws.data_ptr(),
-                                 0 if ws is None else ws.numel(), _lib.stream_handle(dev))
-    _lib.check("qopt_fp8_matmul", rc)
-    return out
+    out, ldo = _output(out, torch.Size((a_codes.shape[0], b_codes.shape[0])), out_dtype, dev)
+    return _matmul(Fp8Matrix(a_codes, a_scales), Fp8Matrix(b_codes, b_scales), fb, out, dt, ldo)
 
 
 def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
@@ -171,27 +196,12 @@ def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
         ldx = k
     else:
         raise ValueError("x must be 2-D with contiguous rows, or contiguous")
-    m = x.numel() // k if k else x.shape[:-1].numel()
     dev = _same_gpu(x, w_codes, w_scales)
-    shape = torch.Size((*x.shape[:-1], n))
-    out = _output(out, shape, out_dtype, dev)
-    _same_gpu(x, out)
-    if out.dim() == 2:
-        ldo = _row_stride(out, "out")
-    elif out.is_contiguous():
-        ldo = n
-    else:
-        raise ValueError("out must be 2-D with contiguous rows, or contiguous")
-    with torch.cuda.device(dev):
-        ws = None
-        if m > QOPT_FP8_FEW_ROWS:
-            ws = _workspace(LIB.qopt_fp8_linear_workspace, "qopt_fp8_linear_workspace", m, n, k, do, dev)
-        rc = LIB.qopt_fp8_linear(x.data_ptr(), dx, m, k, ldx, w_codes.data_ptr(),
-                                 w_scales.data_ptr(), form, n, out.data_ptr(), do, ldo,
-                                 None if ws is None else ws.data_ptr(),
-                                 0 if ws is None else ws.numel(), _lib.stream_handle(dev))
-    _lib.check("qopt_fp8_linear", rc)
-    return out
+    m = x.shape[0] if x.dim() == 2 else x.shape[:-1].numel()
+    if m <= QOPT_FP8_FEW_ROWS and ldx > QOPT_FP8_MAX_DIM:  # further apart than one launch reaches
+        x, ldx = x.contiguous(), k
+    out, ldo = _output(out, torch.Size((*x.shape[:-1], n)), out_dtype, dev)
+    return _linear(x, dx, m, k, ldx, Fp8Matrix(w_codes, w_scales), form, out, do, ldo)
 
 
 class Fp8LinearFunction(torch.autograd.Function):
@@ -201,39 +211,40 @@ class Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
         need_x, need_w = ctx.needs_input_grad
-        x2 = x.reshape(-1, w.shape[1]).contiguous()
-        wq = qopt_fp8_quantize(w.contiguous(), tiles=True, transposed=need_x)
-        wq, wt = wq if need_x else (wq, None)
+        n, k = w.shape
+        x2 = x.reshape(x.shape[:-1].numel(), k).contiguous()
+        dx = _DT[x.dtype]
+        wq, wt = _quantize(w.contiguous(), _DT[w.dtype], k, True, True, need_x)
+        y = torch.empty(*x.shape[:-1], n, dtype=x.dtype, device=x.device)
         if need_w:
-            xq, xt = qopt_fp8_quantize(x2, transposed=True)
-            y = qopt_fp8_matmul(*xq, *wq, x.dtype)
+            xq, xt = _quantize(x2, dx, k, False, True, True)
+            _matmul(xq, wq, QOPT_FP8_TILES, y, dx, n)
         else:
             xt = None
-            y = qopt_fp8_linear(x2, *wq)
+            _linear(x2, dx, x2.shape[0], k, k, wq, QOPT_FP8_TILES, y, dx, n)
         ctx.dtypes = x.dtype, w.dtype
         ctx.x_shape = x.shape
         ctx.save_for_backward(*(wt or (None, None)), *(xt or (None, None)))
-        return y.view(*x.shape[:-1], w.shape[0])
+        return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        w_codes_t, w_scales_t, x_codes_t, x_scales_t = ctx.saved_tensors
+        wt, xt = Fp8Matrix(*ctx.saved_tensors[:2]), Fp8Matrix(*ctx.saved_tensors[2:])
         need_x, need_w = ctx.needs_input_grad
-        dy = dy.reshape(-1, dy.shape[-1]).contiguous()
+        n, k = dy.shape[-1], ctx.x_shape[-1]
+        dy = dy.reshape(dy.shape[:-1].numel(), n).contiguous()
         if dy.dtype not in _DT:
             dy = dy.float()
-        if not need_x and not need_w:
-            return None, None
-        dq = qopt_fp8_quantize(dy, normal=need_x, transposed=need_w)
-        dq, dt = dq if need_x and need_w else (dq, dq)
         dx = dw = None
+        if need_x or need_w:
+            dq, dt = _quantize(dy, _DT[dy.dtype], n, False, need_x, need_w)
         if need_x:
-            k = ctx.x_shape[-1]
-            dx = qopt_fp8_matmul(*dq, w_codes_t, w_scales_t, ctx.dtypes[0])
-            dx = dx.view(*ctx.x_shape[:-1], k)
+            dx = torch.empty(ctx.x_shape, dtype=ctx.dtypes[0], device=dy.device)
+            _matmul(dq, wt, QOPT_FP8_TILES, dx, _DT[dx.dtype], k)
         if need_w:
-            dw = qopt_fp8_matmul(*dt, x_codes_t, x_scales_t, ctx.dtypes[1])
+            dw = torch.empty(n, k, dtype=ctx.dtypes[1], device=dy.device)
+            _matmul(dt, xt, QOPT_FP8_ROWS, dw, _DT[dw.dtype], k)
         return dx, dw
 
 

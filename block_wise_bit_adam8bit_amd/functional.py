@@ -42,6 +42,10 @@ def codebook_bytes(kind):
 def codebook(kind, device=None):
     """Device copy of the codebook of ``kind`` on ``device`` (built and uploaded once
     per process and device; 16-byte aligned)."""
+    if isinstance(device, torch.device):
+        t = _cb_cache.get((kind, device.index))
+        if t is not None:
+            return t
     device = torch.device("cuda", torch.cuda.current_device()) if device is None \
         else torch.device(device)
     if device.type != "cuda":
@@ -89,11 +93,8 @@ def qopt_quantize_blockwise(x, kind=SIGNED, codes=None, absmax=None):
     if absmax.numel() != nblocks(n) or absmax.dtype != torch.float32:
         raise ValueError("absmax must be float32 with ceil(n / 2048) elements")
     dev = _check_cuda(x, codes, absmax)
-    cb = codebook(kind, dev)
-    with torch.cuda.device(dev):
-        rc = LIB.qopt_quantize_blockwise(_ptr(cb), _ptr(x), n, _ptr(codes), _ptr(absmax),
-                                         ctypes.c_void_p(_lib.stream_handle(dev)))
-    _lib.check("qopt_quantize_blockwise", rc)
+    _lib.call("qopt_quantize_blockwise", dev, codebook(kind, dev).data_ptr(), x.data_ptr(), n,
+              codes.data_ptr(), absmax.data_ptr())
     return codes, absmax
 
 
@@ -109,11 +110,8 @@ def qopt_dequantize_blockwise(codes, absmax, kind=SIGNED, out=None):
     if out.numel() != n or out.dtype != torch.float32:
         raise ValueError("out must be float32 with n elements")
     dev = _check_cuda(codes, absmax, out)
-    cb = codebook(kind, dev)
-    with torch.cuda.device(dev):
-        rc = LIB.qopt_dequantize_blockwise(_ptr(cb), _ptr(codes), _ptr(absmax), n, _ptr(out),
-                                           ctypes.c_void_p(_lib.stream_handle(dev)))
-    _lib.check("qopt_dequantize_blockwise", rc)
+    _lib.call("qopt_dequantize_blockwise", dev, codebook(kind, dev).data_ptr(), codes.data_ptr(),
+              absmax.data_ptr(), n, out.data_ptr())
     return out
 
 
@@ -323,12 +321,8 @@ def qopt_adamw8bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, g
     dev = plan.device
     if dev is None:
         return
-    with torch.cuda.device(dev):
-        rc = LIB.qopt_adamw8bit_step(plan.array, len(plan.array), plan.pdtype, plan.gdtype,
-                                     codebook(SIGNED, dev).data_ptr(),
-                                     codebook(UNSIGNED, dev).data_ptr(), hp, gs,
-                                     _lib.stream_handle(dev))
-    _lib.check("qopt_adamw8bit_step", rc)
+    _lib.call("qopt_adamw8bit_step", dev, plan.array, len(plan.array), plan.pdtype, plan.gdtype,
+              codebook(SIGNED, dev).data_ptr(), codebook(UNSIGNED, dev).data_ptr(), hp, gs)
 
 
 def qopt_adamw32bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, grad_scale=None):
@@ -340,10 +334,8 @@ def qopt_adamw32bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, 
     dev = plan.device
     if dev is None:
         return
-    with torch.cuda.device(dev):
-        rc = LIB.qopt_adamw32bit_step(plan.array, len(plan.array), plan.pdtype, plan.gdtype, hp,
-                                      gs, _lib.stream_handle(dev))
-    _lib.check("qopt_adamw32bit_step", rc)
+    _lib.call("qopt_adamw32bit_step", dev, plan.array, len(plan.array), plan.pdtype, plan.gdtype,
+              hp, gs)
 
 
 def qopt_pattern_probe_names():

@@ -223,6 +223,12 @@ def test_empty_products(q):
     y = q.fp8_linear(x, w)
     dx, dw = torch.autograd.grad(y, (x, w), torch.empty_like(y))
     assert dx.shape == (0, 100) and dw.shape == (7, 100) and not dw.any()
+    for n, k in ((0, 100), (7, 0)):
+        x = torch.ones(3, k, device="cuda", requires_grad=True)
+        w = torch.ones(n, k, device="cuda", requires_grad=True)
+        y = q.fp8_linear(x, w)
+        dx, dw = torch.autograd.grad(y, (x, w), torch.ones_like(y))
+        assert y.shape == (3, n) and not y.any() and not dx.any() and dw.shape == (n, k)
 
 
 # ------------------------------------------------------------------ linear
@@ -243,7 +249,7 @@ def test_linear(q, m, dtype, out_dtype):
             w = q.qopt_fp8_quantize(reals(rng, n, k, F32), tiles=tiles)
             x = reals(rng, m, k, dtype)
             got = host(q.qopt_fp8_linear(x, *w, out_dtype))
-            want, tol = bound(fp8.quantize(host(x)), pair(w), out_dtype, m <= 32 or out_dtype == F32)
+            want, tol = bound(fp8.quantize(host(x)), pair(w), out_dtype, out_dtype == F32)
             assert np.all(np.abs(got - want) <= tol)
 
 
