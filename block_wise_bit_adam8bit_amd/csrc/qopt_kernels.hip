@@ -253,6 +253,7 @@ __device__ __forceinline__ uint32_t piece_of(const uint32_t* block_start, uint32
 // one tensor (the same plan as the step's, see plan_chunks).
 struct CodecChunk {
   static constexpr int kMax = kMaxTensors;
+  static constexpr int kElements = QOPT_BLOCK;  // per block
   float* vals[kMaxTensors];               // quantize: input; dequantize: output
   uint8_t* codes[kMaxTensors];
   float* absmax[kMaxTensors];
@@ -557,6 +558,7 @@ template <uint32_t kRun> struct StepWalk {
 // of a step covers the same number of blocks.
 struct StepChunk {
   static constexpr int kMax = kMaxTensors;
+  static constexpr int kElements = QOPT_BLOCK;
   void* param[kMaxTensors];             // tensor base pointers
   const void* grad[kMaxTensors];
   uint8_t* m_codes[kMaxTensors];
@@ -1129,9 +1131,11 @@ __global__ void __launch_bounds__(kThreads) step_traffic_kernel(StepChunk c) {
 
 // ------------------------------------------------- AdamW with 32-bit moments
 
-// One launch's work, as StepChunk: fp32 moments instead of codes and block maxima.
-struct Step32Chunk {
+// One launch's work, as StepChunk, with fp32 moments instead of codes and block maxima.  Nothing ties
+// elements together here: a "block" is what a wave takes at a time.
+template <int kN> struct Step32Chunk {
   static constexpr int kMax = 64;         // pieces per launch (kernarg budget, piece_of's depth)
+  static constexpr int kElements = kN * kWave * 4;
   void* param[kMax];
   const void* grad[kMax];
   float* m[kMax];
@@ -1144,42 +1148,49 @@ struct Step32Chunk {
 };
 
 // One AdamW update with fp32 moments: per element the arithmetic of adam8bit_kernel's
-// exact path, the moments read and written as they are.  Pure streaming: a wave takes
-// one run of 2048 consecutive elements at a time and has all of its loads in flight
-// before it uses the first.
-template <typename PT, typename GT>
-__global__ void __launch_bounds__(kThreads) adamw32_kernel(Step32Chunk c, AdamWScalars k) {
+// exact path, the moments read and written as they are.  A wave has all loads of its
+// block (kN slices of 256 elements) in flight before it uses the first.
+// Bound by memory, 26 bytes per element with fp32 parameters and bf16 gradients, or by the
+// latency of one block where there are few.  Measured on 131,072,000 elements (us; 1, 2, 4 and 8
+// slices at full occupancy 700, 692, 611, 628): four slices with one workgroup of four waves per CU
+// are best, 577 us = 5.9 TB/s (two workgroups 604, three 612): the fewer waves are under way, the
+// closer together lies what they read.  Loading the next block ahead (607), or runs of consecutive
+// blocks per wave (640), did not help.  98 vectors of 2048: 11.0, 7.5, 6.1, 5.4 us with 8, 4, 2 and 1
+// slices (of which 2 launches).
+template <typename PT, typename GT, int kN>
+__global__ void __launch_bounds__(kThreads) adamw32_kernel(Step32Chunk<kN> c, AdamWScalars k) {
   typedef typename Vec4T<PT>::type PV;
   typedef typename Vec4T<GT>::type GV;
+  constexpr int kElements = Step32Chunk<kN>::kElements;
   load_grad_scale(k);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave;
   const uint32_t total = c.block_start[c.npieces];
   for (uint32_t blk = blockIdx.x * kWaves + wave; blk < total; blk += gridDim.x * kWaves) {
     const uint32_t t = piece_of(c.block_start, c.npieces, blk);
-    const int64_t base = static_cast<int64_t>(c.block_lo[t] + (blk - c.block_start[t])) * QOPT_BLOCK;
+    const int64_t base = static_cast<int64_t>(c.block_lo[t] + (blk - c.block_start[t])) * kElements;
     const int64_t rem = c.n[t] - base;
     PT* pb = static_cast<PT*>(c.param[t]) + base;
     const GT* gb = static_cast<const GT*>(c.grad[t]) + base;
     float* mb = c.m[t] + base;
     float* vb = c.v[t] + base;
-    if (rem >= QOPT_BLOCK && ((c.vector_ok >> t) & 1u)) {
+    if (rem >= kElements && ((c.vector_ok >> t) & 1u)) {
       PV* p = reinterpret_cast<PV*>(pb) + lane;
       const GV* g = reinterpret_cast<const GV*>(gb) + lane;
       f32x4* m = reinterpret_cast<f32x4*>(mb) + lane;
       f32x4* v = reinterpret_cast<f32x4*>(vb) + lane;
-      PV P[kSlices];
-      GV G[kSlices];
-      f32x4 M[kSlices], V[kSlices];
+      PV P[kN];
+      GV G[kN];
+      f32x4 M[kN], V[kN];
 #pragma unroll
-      for (int s = 0; s < kSlices; ++s) {
+      for (int s = 0; s < kN; ++s) {
         P[s] = ld_wide(p + s * kWave);
         G[s] = ld_wide(g + s * kWave);
         M[s] = ld_wide(m + s * kWave);
         V[s] = ld_wide(v + s * kWave);
       }
 #pragma unroll
-      for (int s = 0; s < kSlices; ++s) {
+      for (int s = 0; s < kN; ++s) {
         float p4[4], g4[4], m4[4], v4[4];
         unpack4(P[s], p4);
         unpack4(G[s], g4);
@@ -1197,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads) adamw32_kernel(Step32Chunk c, AdamWS
         st_wide(v + s * kWave, vv);
       }
     } else {
-      const int len = rem < QOPT_BLOCK ? static_cast<int>(rem) : QOPT_BLOCK;
+      const int len = rem < kElements ? static_cast<int>(rem) : kElements;
       for (int e = lane; e < len; e += kWave) {
         float m = mb[e], v = vb[e];
         const float p = adam_element(k, load1<PT>(pb, e), load1<GT>(gb, e), m, v, m, v);
@@ -1252,18 +1263,42 @@ int side_stream(hipStream_t* out) {
   return QOPT_OK;
 }
 
+// Workgroups of kThreads that fit a CU of the current device with this kernel, asked of the
+// runtime once per kernel and device (the question costs as much as a launch's own work).
+struct OccupancyEntry {
+  const void* kernel;
+  int dev, per_cu;
+};
+std::mutex g_occ_lock;
+OccupancyEntry g_occ[256];
+int g_occ_count = 0;
+
+int workgroups_per_cu(const void* kernel, int* per_cu) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return QOPT_ELAUNCH;
+  std::lock_guard<std::mutex> lock(g_occ_lock);
+  for (int i = 0; i < g_occ_count; ++i)
+    if (g_occ[i].kernel == kernel && g_occ[i].dev == dev) {
+      *per_cu = g_occ[i].per_cu;
+      return QOPT_OK;
+    }
+  int n = 0;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != hipSuccess || n <= 0)
+    return QOPT_ELAUNCH;
+  if (g_occ_count < static_cast<int>(sizeof(g_occ) / sizeof(g_occ[0]))) g_occ[g_occ_count++] = {kernel, dev, n};
+  *per_cu = n;
+  return QOPT_OK;
+}
+
 // Persistent grid: enough workgroups to fill every CU at the kernel's occupancy
 // (or at most cap per CU, if cap > 0), never more than there are blocks to hand out.
 // Each wave of the kernel takes `run` consecutive blocks at a time.
 template <typename K>
 int grid_for(K kernel, uint32_t nblocks, int cap, uint32_t run, unsigned* grid) {
-  int cus = 0;
+  int cus = 0, per_cu = 0;
   int rc = current_cus(&cus);
+  if (rc == QOPT_OK) rc = workgroups_per_cu(reinterpret_cast<const void*>(kernel), &per_cu);
   if (rc != QOPT_OK) return rc;
-  int per_cu = 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, kernel, kThreads, 0) != hipSuccess ||
-      per_cu <= 0)
-    return QOPT_ELAUNCH;
   if (cap > 0 && per_cu > cap) per_cu = cap;
   const uint64_t resident = static_cast<uint64_t>(cus) * static_cast<uint64_t>(per_cu);
   const uint64_t per_wg = static_cast<uint64_t>(kWaves) * run;
@@ -1312,7 +1347,7 @@ int plan_chunks(int32_t ntensors, const SizeOf& size_of, const Fill& fill, uint6
   for (int32_t i = 0; i < ntensors; ++i) {
     const int64_t n = size_of(i);
     if (n == 0) continue;
-    const uint64_t nb = (static_cast<uint64_t>(n) + QOPT_BLOCK - 1) / QOPT_BLOCK;
+    const uint64_t nb = (static_cast<uint64_t>(n) + Chunk::kElements - 1) / Chunk::kElements;
     uint64_t lo = 0;
     while (lo < nb) {
       if (c.npieces == static_cast<uint32_t>(Chunk::kMax)) {
@@ -1356,7 +1391,9 @@ constexpr uint64_t kCodecLongLaunchBlocks = uint64_t{1} << 16;
 
 template <typename Chunk> uint64_t launch_block_cap(uint64_t total);
 template <> uint64_t launch_block_cap<StepChunk>(uint64_t) { return kMaxLaunchBlocks; }
-template <> uint64_t launch_block_cap<Step32Chunk>(uint64_t) { return kMaxLaunchBlocks; }
+// as many elements as the 8-bit step's launches
+template <> uint64_t launch_block_cap<Step32Chunk<1>>(uint64_t) { return kMaxLaunchBlocks * (QOPT_BLOCK / 256); }
+template <> uint64_t launch_block_cap<Step32Chunk<4>>(uint64_t) { return kMaxLaunchBlocks * (QOPT_BLOCK / 1024); }
 template <> uint64_t launch_block_cap<CodecChunk>(uint64_t total) {
   return total > kMaxLaunchBlocks ? kCodecLongLaunchBlocks : kMaxLaunchBlocks;
 }
@@ -1371,7 +1408,7 @@ int count_chunks(int32_t ntensors, const SizeOf& size_of, const Fill& fill,
   for (int32_t i = 0; i < ntensors; ++i) {
     const int64_t n = size_of(i);
     if (n == 0) continue;
-    const uint64_t nb = (static_cast<uint64_t>(n) + QOPT_BLOCK - 1) / QOPT_BLOCK;
+    const uint64_t nb = (static_cast<uint64_t>(n) + Chunk::kElements - 1) / Chunk::kElements;
     if (nb > 0xFFFFFFFFull) return QOPT_EINVAL;  // block index of one tensor is 32-bit
     total += nb;
     ++pieces;
@@ -1485,10 +1522,10 @@ struct StepSize {
   int64_t operator()(int32_t i) const { return t[i].n; }
 };
 
-struct Step32Fill {
+template <int kN> struct Step32Fill {
   const qopt_tensor32* t;
   size_t psize, gsize;
-  bool operator()(Step32Chunk& c, uint32_t slot, int32_t i) const {
+  bool operator()(Step32Chunk<kN>& c, uint32_t slot, int32_t i) const {
     const qopt_tensor32& x = t[i];
     c.param[slot] = x.param;
     c.grad[slot] = x.grad;
@@ -1546,11 +1583,20 @@ int launch_step_chunks(const qopt_tensor* tensors, int32_t ntensors, size_t psiz
   return launch_step_mode<PT, GT, kNoScreen>(tensors, ntensors, psize, gsize, k, cbm, cbv, stream);
 }
 
+// Large steps take blocks of 4 slices with one workgroup per CU, small ones blocks of 1 on as many
+// workgroups as fit (see adamw32_kernel).  Measured (us, small against large): 2^20 elements 5.6 and
+// 6.4, 2^22 19.4 and 19.7, 2^23 39.7 and 36.9, 2^26 336 and 288.
+constexpr int64_t kLargeStep32 = 5 << 20;
+
 template <typename PT, typename GT>
-int launch_step32(const qopt_tensor32* tensors, int32_t ntensors, const AdamWScalars& k,
-                  hipStream_t stream) {
-  return launch_planned<Step32Chunk>(adamw32_kernel<PT, GT>, 0, 1, ntensors, Step32Size{tensors},
-                                     Step32Fill{tensors, sizeof(PT), sizeof(GT)}, stream, k);
+int launch_step32(const qopt_tensor32* tensors, int32_t ntensors, const AdamWScalars& k, hipStream_t stream) {
+  int64_t n = 0;
+  for (int32_t i = 0; i < ntensors && n < kLargeStep32; ++i) n += tensors[i].n < kLargeStep32 ? tensors[i].n : kLargeStep32;
+  if (n < kLargeStep32)
+    return launch_planned<Step32Chunk<1>>(adamw32_kernel<PT, GT, 1>, 0, 1, ntensors, Step32Size{tensors},
+                                          Step32Fill<1>{tensors, sizeof(PT), sizeof(GT)}, stream, k);
+  return launch_planned<Step32Chunk<4>>(adamw32_kernel<PT, GT, 4>, 1, 1, ntensors, Step32Size{tensors},
+                                        Step32Fill<4>{tensors, sizeof(PT), sizeof(GT)}, stream, k);
 }
 
 int check_step32_tensors(const qopt_tensor32* tensors, int32_t ntensors, int param_dtype,
