@@ -522,25 +522,29 @@ struct GemmArgs {
   void* out;
   int64_t ldo;
   uint32_t wide;                // rows of out allow 16-byte stores
-  uint32_t tiles_m, tiles_n, splits;
+  uint32_t tiles_m, tiles_n;
+  uint32_t whole;               // big tiles that are taken whole; the others in halves
+  uint32_t splits;
   int64_t split_stride;         // elements between the outputs of two splits
 };
 
-// The tile of a workgroup.  Consecutive workgroups go to the 8 XCDs in turn, each with its own L2:
-// every XCD takes one contiguous run of the tiles, in an order that walks kGroup tiles down before
-// the next one across, so that the tiles it has in work share rows of both operands.  Measured on
-// 8192 x 11008 x 4096: against one run over all XCDs 6 % faster, groups of 8 against 4 another 3-5 %.
+// Consecutive workgroups go to the 8 XCDs in turn, each with its own L2: with this order of `all`
+// pieces of work every XCD takes one contiguous run of them ...
+__device__ __forceinline__ uint32_t xcd_order(uint32_t wg, uint32_t all) {
+  const uint32_t xcd = wg % 8, each = all / 8, more = all % 8;
+  return xcd * each + (xcd < more ? xcd : more) + wg / 8;
+}
+// ... and the tiles are counted kGroup of them down before the next one across, so that those that an
+// XCD has in work share rows of both operands.  Measured on 8192 x 11008 x 4096: against one run over
+// all XCDs 6 % faster, groups of 8 against 4 another 3 %, 16 against 8 2 % slower.
 constexpr uint32_t kGroup = 8;
 struct TileAt {
-  uint32_t m, n, split;
+  uint32_t m, n;
 };
-__device__ __forceinline__ TileAt tile_at(uint32_t wg, uint32_t tiles_m, uint32_t tiles_n, uint32_t splits) {
-  const uint32_t tiles = tiles_m * tiles_n, all = tiles * splits;
-  const uint32_t xcd = wg % 8, each = all / 8, more = all % 8;
-  const uint32_t i = xcd * each + (xcd < more ? xcd : more) + wg / 8;
-  const uint32_t t = i % tiles, group = t / (kGroup * tiles_n), left = tiles_m - group * kGroup;
+__device__ __forceinline__ TileAt tile_at(uint32_t t, uint32_t tiles_m, uint32_t tiles_n) {
+  const uint32_t group = t / (kGroup * tiles_n), left = tiles_m - group * kGroup;
   const uint32_t rows = left < kGroup ? left : kGroup, in = t % (kGroup * tiles_n);
-  return {group * kGroup + in % rows, in / rows, i / tiles};
+  return {group * kGroup + in % rows, in / rows};
 }
 
 // The code rows of one tile: at most `most` of them, 2^31 bytes or less.
@@ -558,7 +562,8 @@ __device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src,
   else return __builtin_amdgcn_raw_buffer_load_b8(src, at, 0, 0);
 }
 
-// One workgroup per tile of kM x kN outputs (and split of k), one step per block of 128 along k.
+// One tile of kM x kN outputs from row m0 and column n0 on, by one workgroup; one step per block of 128
+// along k, steps `first` to `last`.
 //
 // A step's kM + kN rows of 128 codes are loaded from memory straight into one of two LDS buffers
 // (no registers), two steps ahead; its fragments are read from LDS half a step ahead, into one of
@@ -582,7 +587,8 @@ __device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src,
 // operands lie in the last-level cache); three and four steps of 64 in flight were no faster, and
 // tiles of 4 waves of 128 x 128 6 % slower.
 template <int kM, int kN, int kWavesM, int kWavesN, bool kExact, bool kTilesB, typename OT>
-__global__ void __launch_bounds__(kWavesM* kWavesN* kWave) gemm_kernel(GemmArgs g) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64_t m0, int64_t n0, int first, int last,
+                                          OT* out) {
   constexpr int kWaves = kWavesM * kWavesN;
   constexpr int kWm = kM / kWavesM, kWn = kN / kWavesN;  // a wave's part of the tile
   constexpr int kFm = kWm / 32, kFn = kWn / 32;          // fragments of 32 per wave
@@ -595,16 +601,9 @@ __global__ void __launch_bounds__(kWavesM* kWavesN* kWave) gemm_kernel(GemmArgs 
   // the places that a lane's loads fill must not depend on the load: rows 8 * kWaves apart differ by
   // a multiple of 8 in row / kF
   static_assert((8 * kWaves >> kShiftM) % 8 == 0 && (8 * kWaves >> kShiftN) % 8 == 0, "places");
-  __shared__ __align__(16) uint8_t lds[2 * kRows * kBlock];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const TileAt tile = tile_at(blockIdx.x, g.tiles_m, g.tiles_n, g.splits);
-  const int64_t m0 = static_cast<int64_t>(tile.m) * kM, n0 = static_cast<int64_t>(tile.n) * kN;
-  // this split's steps
-  const int first = static_cast<int>(static_cast<int64_t>(g.kb) * tile.split / g.splits);
-  const int last = static_cast<int>(static_cast<int64_t>(g.kb) * (tile.split + 1) / g.splits) - 1;
-
   const __amdgpu_buffer_rsrc_t ra = rows_buffer(g.a, m0, g.m, kM, g.kp);
   const __amdgpu_buffer_rsrc_t rb = rows_buffer(g.b, n0, g.n, kN, g.kp);
   const uint32_t row8 = wave * 8 + (lane >> 3);
@@ -745,7 +744,6 @@ __global__ void __launch_bounds__(kWavesM* kWavesN* kWave) gemm_kernel(GemmArgs 
 
   // Lane (r, h) holds row kFm r + i; its columns kFn (8 q + 4 h + e) + j for e = 0 .. 3 and all j are
   // consecutive.
-  OT* out = static_cast<OT*>(g.out) + tile.split * g.split_stride;
 #pragma unroll
   for (int i = 0; i < kFm; ++i) {
     const int64_t row = m0 + wm * kWm + kFm * (lane & 31) + i;
@@ -779,6 +777,35 @@ __global__ void __launch_bounds__(kWavesM* kWavesN* kWave) gemm_kernel(GemmArgs 
         }
       }
     }
+  }
+}
+
+// One workgroup per tile of 128 x 128 and split of k.
+template <bool kExact, bool kTilesB, typename OT>
+__global__ void __launch_bounds__(256) gemm_kernel(GemmArgs g) {
+  __shared__ __align__(16) uint8_t lds[2 * 256 * kBlock];
+  const uint32_t tiles = g.tiles_m * g.tiles_n, i = xcd_order(blockIdx.x, tiles * g.splits), split = i / tiles;
+  const TileAt tile = tile_at(i % tiles, g.tiles_m, g.tiles_n);
+  const int first = static_cast<int>(static_cast<int64_t>(g.kb) * split / g.splits);
+  const int last = static_cast<int>(static_cast<int64_t>(g.kb) * (split + 1) / g.splits) - 1;
+  gemm_tile<128, 128, 2, 2, kExact, kTilesB, OT>(g, lds, tile.m * int64_t{128}, tile.n * int64_t{128}, first, last,
+                                                 static_cast<OT*>(g.out) + split * g.split_stride);
+}
+
+// One workgroup per tile of 256 x 256, and two for each of those of the last round that would leave
+// half of the CUs or more without work.
+template <bool kTilesB, typename OT> __global__ void __launch_bounds__(512) gemm_big_kernel(GemmArgs g) {
+  __shared__ __align__(16) uint8_t lds[2 * 512 * kBlock];
+  OT* out = static_cast<OT*>(g.out);
+  if (blockIdx.x < g.whole) {
+    const TileAt tile = tile_at(xcd_order(blockIdx.x, g.whole), g.tiles_m, g.tiles_n);
+    gemm_tile<256, 256, 2, 4, false, kTilesB, OT>(g, lds, tile.m * int64_t{256}, tile.n * int64_t{256}, 0, g.kb - 1, out);
+  } else {
+    const uint32_t i = xcd_order(blockIdx.x - g.whole, gridDim.x - g.whole);
+    const TileAt tile = tile_at(g.whole + i / 2, g.tiles_m, g.tiles_n);
+    const int64_t m0 = tile.m * int64_t{256} + (i % 2) * 128;
+    if (m0 < g.m)
+      gemm_tile<128, 256, 2, 4, false, kTilesB, OT>(g, lds, m0, tile.n * int64_t{256}, 0, g.kb - 1, out);
   }
 }
 
@@ -859,25 +886,26 @@ template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t
   }
 }
 
-// How a product is cut up: tiles of 256 x 256 or 128 x 128, and the splits of k.
+// How a product is cut up: tiles of 256 x 256, `whole` of them whole and the others in halves, or (whole
+// and halves 0) tiles of 128 x 128 with k in so many splits.
 struct Plan {
-  bool big;
+  int64_t whole, halves;
   int splits;
 };
 
 // The plan of least time by this model, in microseconds on 256 CUs.  A step (128 along k) takes a CU
-//   1.70 for one tile of 256 x 256 (2.52 PFLOP/s with all CUs busy),
+//   1.70 for one tile of 256 x 256 (2.52 PFLOP/s with all CUs busy), 1.1 for half of one,
 //   1.06 for two tiles of 128 x 128 side by side (2.03), 0.70 for one;
 //   the exact path 1.67 and 0.96.
-// Small tiles cost a quarter more per product but fill the chip at a quarter of the size: 2048 x 11008
-// x 4096 takes 100 us with them (3 rounds of 1376 tiles) and 109 us with the big ones (2 rounds of
-// 344), 8192 x 4096 x 11008 363 us and 293 us.  Splitting k, for products of too few tiles, adds a
-// launch that joins the partial results (4) and their way to memory and back (4 TB/s).
+// Small tiles cost a quarter more per product but fill the chip at a quarter of the size: 1024 x 4096 x
+// 4096 takes 25.5 us with them and 55 us with 64 whole tiles, 8192 x 4096 x 11008 363 us and 293 us.
+// Splitting k, for products of too few tiles, adds a launch that joins the partial results (4) and
+// their way to memory and back (4 TB/s).
 Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
   const int64_t kb = ceil_div(k, kBlock);
   const int64_t small = ceil_div(m, 128) * ceil_div(n, 128), large = ceil_div(m, 256) * ceil_div(n, 256);
   const double two = exact ? 1.67 : 1.06, one = exact ? 0.96 : 0.70;
-  Plan best = {false, 1};
+  Plan best = {0, 0, 1};
   double least = 0;
   for (int splits = 1; splits <= 16 && splits <= kb; splits *= 2) {
     const int64_t wgs = small * splits, steps = ceil_div(kb, splits);
@@ -890,23 +918,33 @@ Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
     }
     if (wgs > 512) break;
   }
-  if (!exact && static_cast<double>(kb) * ceil_div(large, 256) * 1.70 <= least) best = {true, 1};
+  if (exact) return best;
+  const int64_t rest = large % 256, halved = rest <= 128 ? rest : 0;
+  const double us = static_cast<double>(kb) * (ceil_div(large - halved, 256) * 1.70 + (halved ? 1.1 : 0.0));
+  if (us <= least) best = {large - halved, 2 * halved, 1};
   return best;
 }
 
 int64_t partial_stride(int64_t n) { return ceil_div(n, 4) * 4; }
 
-template <int kM, int kN, int kWavesM, int kWavesN, bool kExact, typename OT>
-int launch_gemm(GemmArgs g, bool b_tiles, hipStream_t s) {
-  g.tiles_m = static_cast<uint32_t>(ceil_div(g.m, kM));
-  g.tiles_n = static_cast<uint32_t>(ceil_div(g.n, kN));
+template <bool kExact, typename OT> int launch_gemm(GemmArgs g, bool b_tiles, hipStream_t s) {
+  g.tiles_m = static_cast<uint32_t>(ceil_div(g.m, 128));
+  g.tiles_n = static_cast<uint32_t>(ceil_div(g.n, 128));
   const int64_t wgs = static_cast<int64_t>(g.tiles_m) * g.tiles_n * g.splits;
   if (wgs > kMaxGrid) return QOPT_EINVAL;
-  const dim3 grid(static_cast<unsigned>(wgs)), block(kWavesM * kWavesN * kWave);
-  if (b_tiles)
-    hipLaunchKernelGGL((gemm_kernel<kM, kN, kWavesM, kWavesN, kExact, true, OT>), grid, block, 0, s, g);
-  else
-    hipLaunchKernelGGL((gemm_kernel<kM, kN, kWavesM, kWavesN, kExact, false, OT>), grid, block, 0, s, g);
+  const dim3 grid(static_cast<unsigned>(wgs));
+  if (b_tiles) hipLaunchKernelGGL((gemm_kernel<kExact, true, OT>), grid, dim3(256), 0, s, g);
+  else hipLaunchKernelGGL((gemm_kernel<kExact, false, OT>), grid, dim3(256), 0, s, g);
+  return launch_status();
+}
+
+int launch_gemm_big(GemmArgs g, const Plan& plan, bool b_tiles, hipStream_t s) {
+  g.tiles_m = static_cast<uint32_t>(ceil_div(g.m, 256));
+  g.tiles_n = static_cast<uint32_t>(ceil_div(g.n, 256));
+  g.whole = static_cast<uint32_t>(plan.whole);
+  const dim3 grid(static_cast<unsigned>(plan.whole + plan.halves));  // at most kMaxGrid tiles of 128 x 128
+  if (b_tiles) hipLaunchKernelGGL((gemm_big_kernel<true, uint16_t>), grid, dim3(512), 0, s, g);
+  else hipLaunchKernelGGL((gemm_big_kernel<false, uint16_t>), grid, dim3(512), 0, s, g);
   return launch_status();
 }
 
@@ -1007,8 +1045,7 @@ extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scal
     g.ldo = partial_stride(n);
     g.split_stride = m * g.ldo;
     g.wide = 1;
-    rc = exact ? launch_gemm<128, 128, 2, 2, true, float>(g, tiles, s)
-               : launch_gemm<128, 128, 2, 2, false, float>(g, tiles, s);
+    rc = exact ? launch_gemm<true, float>(g, tiles, s) : launch_gemm<false, float>(g, tiles, s);
     if (rc != QOPT_OK) return rc;
     const int64_t wgs = ceil_div(m * (g.ldo / 4), 256);
     const dim3 grid(static_cast<unsigned>(wgs < 4096 ? wgs : 4096));
@@ -1024,9 +1061,9 @@ extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scal
   g.out = out_dev;
   g.ldo = ldo;
   g.wide = aligned(out_dev, 16) && (ldo * osize) % 16 == 0 ? 1u : 0u;
-  if (exact) return launch_gemm<128, 128, 2, 2, true, float>(g, tiles, s);
-  return plan.big ? launch_gemm<256, 256, 2, 4, false, uint16_t>(g, tiles, s)
-                  : launch_gemm<128, 128, 2, 2, false, uint16_t>(g, tiles, s);
+  if (exact) return launch_gemm<true, float>(g, tiles, s);
+  if (plan.whole + plan.halves > 0) return launch_gemm_big(g, plan, tiles, s);
+  return launch_gemm<false, uint16_t>(g, tiles, s);
 }
 
 namespace {

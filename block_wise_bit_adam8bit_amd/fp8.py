@@ -42,44 +42,51 @@ def _check_dtype(dtype, what):
     return _DT[dtype]
 
 
-def _same_gpu(*ts):
-    dev = ts[0].device
-    for t in ts:
+def _same_gpu(first, *others):
+    index = first.get_device() if first.is_cuda else -1
+    if index < 0:
+        raise ValueError("all tensors must be on a GPU")
+    for t in others:
         if not t.is_cuda:
             raise ValueError("all tensors must be on a GPU")
-        if t.device != dev:
+        if t.get_device() != index:
             raise ValueError("all tensors must be on the same GPU")
-    return dev
+    return first.device
 
 
 def _row_stride(t, what):
     """Elements between the rows of a 2-D tensor whose rows are contiguous."""
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return cols
+    far, near = t.stride()
+    if cols > 1 and near != 1:
         raise ValueError(f"the rows of {what} must be contiguous")
     if rows <= 1:
         return cols
-    if t.stride(0) < cols:
+    if far < cols:
         raise ValueError(f"the rows of {what} must not overlap")
-    return t.stride(0)
+    return far
 
 
 def _quantized(codes, scales, what):
     """Checks a (codes, scales) pair; returns its form."""
-    if codes.dtype != CODE_DTYPE or scales.dtype != torch.uint8:
+    if codes.dtype is not CODE_DTYPE or scales.dtype is not torch.uint8:
         raise TypeError(f"{what}: codes must be float8_e4m3fn and scales uint8")
     if codes.dim() != 2 or codes.shape[1] % QOPT_FP8_BLOCK:
         raise ValueError(f"{what}: codes must be 2-D with a multiple of {QOPT_FP8_BLOCK} columns")
-    rows, kb = codes.shape[0], codes.shape[1] // QOPT_FP8_BLOCK
-    by_rows, by_tiles = (kb, -(-rows // 16) * 16), (_blocks(rows), kb)
-    if tuple(scales.shape) not in (by_rows, by_tiles):
-        raise ValueError(f"{what}: scales must be {by_rows} or {by_tiles}, not "
-                         f"{tuple(scales.shape)}")
+    rows, kb = codes.shape
+    kb //= QOPT_FP8_BLOCK
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{what}: codes and scales must be contiguous")
     # the two shapes differ for every matrix with elements: rows <= 16 has 16 columns in the
     # first and one row in the second, more rows have fewer than rows / 16 tiles
-    return QOPT_FP8_ROWS if tuple(scales.shape) == by_rows else QOPT_FP8_TILES
+    shape, by_rows, by_tiles = scales.shape, (kb, -(-rows // 16) * 16), (-(-rows // QOPT_FP8_BLOCK), kb)
+    if shape == by_rows:
+        return QOPT_FP8_ROWS
+    if shape == by_tiles:
+        return QOPT_FP8_TILES
+    raise ValueError(f"{what}: scales must be {by_rows} or {by_tiles}, not {tuple(shape)}")
 
 
 def _empty_matrix(rows, cols, tiles, device):
@@ -152,6 +159,7 @@ def _output(out, shape, dtype, dev):
     """The output tensor and the distance of its rows."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev), shape[-1]
+    shape = torch.Size(shape)
     if out.shape != shape or out.dtype != dtype:
         raise ValueError(f"out must have shape {tuple(shape)} and dtype {dtype}")
     if out.device != dev:
@@ -173,7 +181,7 @@ def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat
     if b_codes.shape[1] != a_codes.shape[1]:
         raise ValueError("a and b must have the same number of columns")
     dev = _same_gpu(a_codes, a_scales, b_codes, b_scales)
-    out, ldo = _output(out, torch.Size((a_codes.shape[0], b_codes.shape[0])), out_dtype, dev)
+    out, ldo = _output(out, (a_codes.shape[0], b_codes.shape[0]), out_dtype, dev)
     return _matmul(Fp8Matrix(a_codes, a_scales), Fp8Matrix(b_codes, b_scales), fb, out, dt, ldo)
 
 
@@ -200,7 +208,7 @@ def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
     m = x.shape[0] if x.dim() == 2 else x.shape[:-1].numel()
     if m <= QOPT_FP8_FEW_ROWS and ldx > QOPT_FP8_MAX_DIM:  # further apart than one launch reaches
         x, ldx = x.contiguous(), k
-    out, ldo = _output(out, torch.Size((*x.shape[:-1], n)), out_dtype, dev)
+    out, ldo = _output(out, (*x.shape[:-1], n), out_dtype, dev)
     return _linear(x, dx, m, k, ldx, Fp8Matrix(w_codes, w_scales), form, out, do, ldo)
 
 
