@@ -721,24 +721,46 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
   __builtin_amdgcn_sched_barrier(0);
   step_barrier();
   load_step(1, upto_last(first + 1));
-  Frags f0, f1;
-  read_half(f0, 0, 0);
-  for (int t = first; t <= last; ++t) {
-    // past the last step the last one is loaded again: no branch, which would keep the compiler from
-    // spreading the loads
-    const int buf = (t - first) & 1, ahead = upto_last(t + 2);
-    read_half(f1, buf, 1);
-    multiply(f0, c0);
-    spread(false);
-    step_barrier();
-    asm volatile("" : "+v"(c1.a), "+v"(c1.b));  // not used before the wait that it landed with
-    read_half(f0, buf ^ 1, 0);
-    const Scales c2 = load_scales(ahead);
-    load_step(buf, ahead);
-    multiply(f1, c0);
-    spread(true);
-    c0 = c1;
-    c1 = c2;
+  if constexpr (kExact && kFm * kFn > 4) {
+    // One register set: widened operands take the room of the second, and the other wave of the SIMD
+    // works meanwhile.  8192 x 4096 x 11008 in 550 us, 1.34 PFLOP/s (594 us with tiles of 128 x 128; 570 us
+    // with the widening spread between the matrix instructions).
+    for (int t = first; t <= last; ++t) {
+      const int buf = (t - first) & 1, ahead = upto_last(t + 2);
+      Frags f;
+      read_half(f, buf, 0);
+      multiply(f, c0);
+      __builtin_amdgcn_sched_barrier(0);
+      read_half(f, buf, 1);
+      multiply(f, c0);
+      __builtin_amdgcn_sched_barrier(0);
+      step_barrier();
+      asm volatile("" : "+v"(c1.a), "+v"(c1.b));
+      const Scales c2 = load_scales(ahead);
+      load_step(buf, ahead);
+      c0 = c1;
+      c1 = c2;
+    }
+  } else {
+    Frags f0, f1;
+    read_half(f0, 0, 0);
+    for (int t = first; t <= last; ++t) {
+      // past the last step the last one is loaded again: no branch, which would keep the compiler from
+      // spreading the loads
+      const int buf = (t - first) & 1, ahead = upto_last(t + 2);
+      read_half(f1, buf, 1);
+      multiply(f0, c0);
+      spread(false);
+      step_barrier();
+      asm volatile("" : "+v"(c1.a), "+v"(c1.b));  // not used before the wait that it landed with
+      read_half(f0, buf ^ 1, 0);
+      const Scales c2 = load_scales(ahead);
+      load_step(buf, ahead);
+      multiply(f1, c0);
+      spread(true);
+      c0 = c1;
+      c1 = c2;
+    }
   }
   __builtin_amdgcn_s_waitcnt(0x0070);  // no load is on its way into LDS when the workgroup ends
 
@@ -794,18 +816,19 @@ __global__ void __launch_bounds__(256) gemm_kernel(GemmArgs g) {
 
 // One workgroup per tile of 256 x 256, and two for each of those of the last round that would leave
 // half of the CUs or more without work.
-template <bool kTilesB, typename OT> __global__ void __launch_bounds__(512) gemm_big_kernel(GemmArgs g) {
+template <bool kExact, bool kTilesB, typename OT>
+__global__ void __launch_bounds__(512) gemm_big_kernel(GemmArgs g) {
   __shared__ __align__(16) uint8_t lds[2 * 512 * kBlock];
   OT* out = static_cast<OT*>(g.out);
   if (blockIdx.x < g.whole) {
     const TileAt tile = tile_at(xcd_order(blockIdx.x, g.whole), g.tiles_m, g.tiles_n);
-    gemm_tile<256, 256, 2, 4, false, kTilesB, OT>(g, lds, tile.m * int64_t{256}, tile.n * int64_t{256}, 0, g.kb - 1, out);
+    gemm_tile<256, 256, 2, 4, kExact, kTilesB, OT>(g, lds, tile.m * int64_t{256}, tile.n * int64_t{256}, 0, g.kb - 1, out);
   } else {
     const uint32_t i = xcd_order(blockIdx.x - g.whole, gridDim.x - g.whole);
     const TileAt tile = tile_at(g.whole + i / 2, g.tiles_m, g.tiles_n);
     const int64_t m0 = tile.m * int64_t{256} + (i % 2) * 128;
     if (m0 < g.m)
-      gemm_tile<128, 256, 2, 4, false, kTilesB, OT>(g, lds, m0, tile.n * int64_t{256}, 0, g.kb - 1, out);
+      gemm_tile<128, 256, 2, 4, kExact, kTilesB, OT>(g, lds, m0, tile.n * int64_t{256}, 0, g.kb - 1, out);
   }
 }
 
@@ -896,7 +919,7 @@ struct Plan {
 // The plan of least time by this model, in microseconds on 256 CUs.  A step (128 along k) takes a CU
 //   1.70 for one tile of 256 x 256 (2.52 PFLOP/s with all CUs busy), 1.1 for half of one,
 //   1.06 for two tiles of 128 x 128 side by side (2.03), 0.70 for one;
-//   the exact path 1.67 and 0.96.
+//   the exact path 3.2, 2.1, 1.67 and 0.96.
 // Small tiles cost a quarter more per product but fill the chip at a quarter of the size: 1024 x 4096 x
 // 4096 takes 25.5 us with them and 55 us with 64 whole tiles, 8192 x 4096 x 11008 363 us and 293 us.
 // Splitting k, for products of too few tiles, adds a launch that joins the partial results (4) and
@@ -918,9 +941,9 @@ Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
     }
     if (wgs > 512) break;
   }
-  if (exact) return best;
   const int64_t rest = large % 256, halved = rest <= 128 ? rest : 0;
-  const double us = static_cast<double>(kb) * (ceil_div(large - halved, 256) * 1.70 + (halved ? 1.1 : 0.0));
+  const double us = static_cast<double>(kb) * (ceil_div(large - halved, 256) * (exact ? 3.2 : 1.70) +
+                                              (halved ? (exact ? 2.1 : 1.1) : 0.0));
   if (us <= least) best = {large - halved, 2 * halved, 1};
   return best;
 }
@@ -938,13 +961,13 @@ template <bool kExact, typename OT> int launch_gemm(GemmArgs g, bool b_tiles, hi
   return launch_status();
 }
 
-int launch_gemm_big(GemmArgs g, const Plan& plan, bool b_tiles, hipStream_t s) {
+template <bool kExact, typename OT> int launch_gemm_big(GemmArgs g, const Plan& plan, bool b_tiles, hipStream_t s) {
   g.tiles_m = static_cast<uint32_t>(ceil_div(g.m, 256));
   g.tiles_n = static_cast<uint32_t>(ceil_div(g.n, 256));
   g.whole = static_cast<uint32_t>(plan.whole);
   const dim3 grid(static_cast<unsigned>(plan.whole + plan.halves));  // at most kMaxGrid tiles of 128 x 128
-  if (b_tiles) hipLaunchKernelGGL((gemm_big_kernel<true, uint16_t>), grid, dim3(512), 0, s, g);
-  else hipLaunchKernelGGL((gemm_big_kernel<false, uint16_t>), grid, dim3(512), 0, s, g);
+  if (b_tiles) hipLaunchKernelGGL((gemm_big_kernel<kExact, true, OT>), grid, dim3(512), 0, s, g);
+  else hipLaunchKernelGGL((gemm_big_kernel<kExact, false, OT>), grid, dim3(512), 0, s, g);
   return launch_status();
 }
 
@@ -1061,9 +1084,9 @@ extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scal
   g.out = out_dev;
   g.ldo = ldo;
   g.wide = aligned(out_dev, 16) && (ldo * osize) % 16 == 0 ? 1u : 0u;
-  if (exact) return launch_gemm<true, float>(g, tiles, s);
-  if (plan.whole + plan.halves > 0) return launch_gemm_big(g, plan, tiles, s);
-  return launch_gemm<false, uint16_t>(g, tiles, s);
+  if (plan.whole + plan.halves > 0)
+    return exact ? launch_gemm_big<true, float>(g, plan, tiles, s) : launch_gemm_big<false, uint16_t>(g, plan, tiles, s);
+  return exact ? launch_gemm<true, float>(g, tiles, s) : launch_gemm<false, uint16_t>(g, tiles, s);
 }
 
 namespace {
