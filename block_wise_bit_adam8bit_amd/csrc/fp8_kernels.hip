@@ -110,29 +110,23 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
   return __builtin_bit_cast(uint32_t, w);
 }
 
-// kCount (a multiple of 8) consecutive elements of a row; those from `left` on are 0.
-template <typename XT, int kCount>
-__device__ __forceinline__ void load_row(const XT* p, bool wide, int64_t left,
-                                         typename Elements<XT>::Reg (&x)[kCount / Elements<XT>::kPer]) {
-  if (wide && left >= kCount) {
-    constexpr int kWide = 16 / sizeof(XT) / Elements<XT>::kPer;  // registers per 16 bytes: 4
+// Eight consecutive elements of a row, from an address of any element (the hardware reads 16 bytes
+// at any alignment).
+template <typename XT> __device__ __forceinline__ void load8(const XT* p, typename Elements<XT>::Reg (&x)[8 / Elements<XT>::kPer]) {
+  __builtin_memcpy(x, p, sizeof(x));
+}
+// The same near a row's end, `left` elements on (any number): those from there on are 0.  No branch: the
+// loads past the end read the row's last element instead.
+template <typename XT>
+__device__ __forceinline__ void load8_upto(const XT* p, int64_t left, typename Elements<XT>::Reg (&x)[8 / Elements<XT>::kPer]) {
+  auto one = [&](int j) {
+    const XT v = p[j < left ? j : left - 1];
+    return j < left ? v : XT(0);
+  };
 #pragma unroll
-    for (int i = 0; i < kCount / Elements<XT>::kPer / kWide; ++i) {
-      typedef typename Elements<XT>::Reg Quad __attribute__((ext_vector_type(4)));
-      const Quad q = reinterpret_cast<const Quad*>(p)[i];
-#pragma unroll
-      for (int j = 0; j < kWide; ++j) x[kWide * i + j] = q[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kCount / Elements<XT>::kPer; ++j) {
-      if constexpr (sizeof(XT) == 4) {
-        x[j] = j < left ? p[j] : 0.0f;
-      } else {
-        const uint32_t lo = 2 * j < left ? p[2 * j] : 0u, hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
-        x[j] = lo | hi << 16;
-      }
-    }
+  for (int j = 0; j < 8 / Elements<XT>::kPer; ++j) {
+    if constexpr (sizeof(XT) == 4) x[j] = one(j);
+    else x[j] = static_cast<uint32_t>(one(2 * j)) | static_cast<uint32_t>(one(2 * j + 1)) << 16;
   }
 }
 
@@ -144,7 +138,6 @@ struct QuantArgs {
   uint8_t *codes, *scales, *codes_t, *scales_t;
   int64_t kp, kpt;  // bytes per row of codes and codes_t
   int64_t sr, srt;  // bytes per block row of scales and scales_t
-  uint32_t wide;    // rows of x allow 16-byte loads
   uint32_t tiles;   // tiles along a row
 };
 
@@ -169,10 +162,24 @@ __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
   const int64_t col = col0 + 8 * c;
   const XT* x = static_cast<const XT*>(q.x);
   typename E::Reg v[8][kRegs];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  // rows past the last one: that one's values at first
+  auto row_at = [&](int i) {
     const int64_t row = row0 + 8 * r + i;
-    load_row<XT, 8>(x + (row < q.rows ? row : 0) * q.ldx + col, q.wide != 0, row < q.rows ? q.cols - col : 0, v[i]);
+    return x + (row < q.rows ? row : q.rows - 1) * q.ldx + col;
+  };
+  if (col0 + kBlock <= q.cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load8<XT>(row_at(i), v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load8_upto<XT>(row_at(i), q.cols - col, v[i]);
+  }
+  if (row0 + kBlock > q.rows) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < kRegs; ++j)
+        if (row0 + 8 * r + i >= q.rows) v[i][j] = typename E::Reg(0);
   }
   uint32_t rmax[8], cmax[kRegs];  // cmax: of a pair of columns for bf16
   auto maxima = [&](auto magnitude) {
@@ -323,23 +330,22 @@ template <typename OT> __device__ __forceinline__ void store1(OT* p, float x) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00027000);
 }
-constexpr uint32_t kPastEnd = 0x80000000u;  // past the end of every buffer that it is used with (2^31 bytes or less)
 
 struct FewArgs {
   const void* x;
   int64_t m, k, ldx;
   const uint8_t *w, *ws;
   int64_t n;
-  uint32_t kp, x_bytes, ws_bytes;
+  uint32_t kp, ws_bytes;
   uint32_t ws_row, ws_block;  // distances between the scales of rows (>> w_shift) and of blocks
   int32_t kb, w_shift;
   void* out;
   int64_t ldo;
 };
 
-// Waves per workgroup by the runs of 16 weight rows that it takes: measured 4 against 8, 1 row of
-// 4096 x 4096 (one run) 7.6 and 6.7 us, 24 rows of 11008 x 4096 (three) 16.0 and 17.2 us.
-constexpr int few_waves(int runs) { return runs == 1 ? 8 : 4; }
+// Waves per workgroup: 8, but 4 where each holds most registers (measured, 4 and 8: 32 rows of
+// 50257 x 2048 34.5 and 38.8 us, 1 row of 11008 x 4096 11.6 and 9.9 us).
+constexpr int few_waves(int frags, int runs) { return frags == 2 && runs == 4 ? 4 : 8; }
 
 // x w^T for at most 16 * kFrags rows of x: the time of reading the weights.  A workgroup owns
 // 16 * kRuns rows of w; its waves take turns at the blocks of 128 along k, and their sums are added
@@ -348,17 +354,19 @@ constexpr int few_waves(int runs) { return runs == 1 ? 8 : 4; }
 // lanes), so there is no launch before this one.
 // The weights' bytes bound it at the rate of memory; what a workgroup adds to that is reading x from
 // the L2 and quantizing it anew.  Measured (bf16, repeated in a graph, 2.3 us of it the launch): 1 row
-// of 4096 x 4096 6.7 us, 1 of 11008 x 4096 10.8 us (4.2 TB/s), 24 of it 16.0 us, 7 of 50257 x 2048
-// 26.9 us (3.8 TB/s).
-// Nothing in the loop branches: what lies past k, past the last block or past the last row is read
-// past the end of a buffer, as 0, and a lane without a row of x takes the last one's values, which
-// no result uses.  (With branches around the loads the compiler waited for each before the next.)
-// kWide: rows of x are read in pieces of 16 bytes, of which k is a multiple.
-template <typename XT, typename OT, int kFrags, int kRuns, bool kWide>
-__global__ void __launch_bounds__(few_waves(kRuns) * kWave) few_rows_kernel(FewArgs g) {
+// of 4096 x 4096 5.8 us, 1 of 11008 x 4096 9.9 us (4.6 TB/s), 24 of it 15.1 us, 7 of 50257 x 2048 22.3 us
+// (4.6 TB/s).
+// Nothing around the loads branches (the compiler would wait for each before the next): weights past
+// the last row are read past the end of a buffer, as 0, and a lane without a row of x takes the last
+// one's values, which no result uses.  What k has beyond whole blocks comes after the loop.
+// The loads of one block per wave are on their way at a time: two or four register sets in turn cost
+// more waves per SIMD than they hid (1 row of 4096 x 4096 6.4 us, 6.5 with two, 7.9 with four; 16 rows
+// 8.4 and 9.0; 1 row of 11008 x 4096 9.5 and 11.2).
+template <typename XT, typename OT, int kFrags, int kRuns>
+__global__ void __launch_bounds__(few_waves(kFrags, kRuns) * kWave) few_rows_kernel(FewArgs g) {
   typedef Elements<XT> E;
   typedef typename E::Reg Reg;
-  constexpr int kFewWaves = few_waves(kRuns);
+  constexpr int kFewWaves = few_waves(kFrags, kRuns);
   constexpr int kRegs = 32 / E::kPer;
   constexpr bool kExact = sizeof(OT) == 4;
   __shared__ f32x4 sums[kFewWaves][kFrags * kRuns][kWave];
@@ -366,65 +374,40 @@ __global__ void __launch_bounds__(few_waves(kRuns) * kWave) few_rows_kernel(FewA
   const int r = lane & 15, h = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * kRuns);
   const int64_t rows = g.n - n0 < 16 * kRuns ? g.n - n0 : 16 * kRuns;
-  const __amdgpu_buffer_rsrc_t bx = buffer(g.x, g.x_bytes), bs = buffer(g.ws, g.ws_bytes);
+  const __amdgpu_buffer_rsrc_t bs = buffer(g.ws, g.ws_bytes);
   const __amdgpu_buffer_rsrc_t bw = buffer(g.w + n0 * g.kp, static_cast<uint32_t>(rows * g.kp));
-  const uint32_t k = static_cast<uint32_t>(g.k);
-  uint32_t ws[kRuns], xs[kFrags];
+  const int whole = static_cast<int>(g.k / kBlock);  // blocks
+  uint32_t ws[kRuns];
+  const XT* xs[kFrags];
 #pragma unroll
   for (int i = 0; i < kRuns; ++i) ws[i] = (static_cast<uint32_t>(n0 + 16 * i + r) >> g.w_shift) * g.ws_row;
 #pragma unroll
   for (int f = 0; f < kFrags; ++f)
-    xs[f] = static_cast<uint32_t>((f * 16 + r < g.m ? f * 16 + r : g.m - 1) * g.ldx * static_cast<int64_t>(sizeof(XT)));
+    xs[f] = static_cast<const XT*>(g.x) + (f * 16 + r < g.m ? f * 16 + r : g.m - 1) * g.ldx + h * 32;
   f32x4 acc[kFrags][kRuns];
 #pragma unroll
   for (int f = 0; f < kFrags; ++f)
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) acc[f][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // A wave's blocks go through kAhead register sets in turn: a set is loaded again as soon as its
-  // block is multiplied, so that the loads of kAhead blocks are on their way at the start and
-  // kAhead - 1 all along.
   struct Block {
     Reg x[kFrags][kRegs];
     i32x4 c[kRuns][2];
     uint32_t s[kRuns];
   };
-  constexpr int kAhead = 2;  // 4 measured 7.9 us against 6.7 (1 row of 4096 x 4096)
-  auto load = [&](Block& v, int b) {
-    const uint32_t col = static_cast<uint32_t>(b) * kBlock + h * 32;
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f) {
-      if constexpr (kWide) {
-        constexpr int kPiece = 16 / sizeof(XT);  // elements
-        typedef Reg Quad __attribute__((ext_vector_type(4)));
-#pragma unroll
-        for (int i = 0; i < 32 / kPiece; ++i) {
-          const uint32_t at = col + i * kPiece;
-          const Quad q = __builtin_bit_cast(Quad, __builtin_amdgcn_raw_buffer_load_b128(
-                                                      bx, at < k ? xs[f] + at * sizeof(XT) : kPastEnd, 0, 0));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v.x[f][4 * i + j] = q[j];
-        }
-      } else {
-        auto one = [&](uint32_t at) { return at < k ? xs[f] + at * static_cast<uint32_t>(sizeof(XT)) : kPastEnd; };
-#pragma unroll
-        for (int j = 0; j < kRegs; ++j) {
-          if constexpr (E::kPer == 2) {
-            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(bx, one(col + 2 * j), 0, 0);
-            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(bx, one(col + 2 * j + 1), 0, 0);
-            v.x[f][j] = (lo & 0xFFFFu) | hi << 16;
-          } else {
-            v.x[f][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bx, one(col + j), 0, 0));
-          }
-        }
-      }
-    }
+  auto load_weights = [&](Block& v, int b) {
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) {
-      const uint32_t at = b < g.kb ? (16 * i + r) * g.kp + col : kPastEnd;
+      const uint32_t at = (16 * i + r) * g.kp + static_cast<uint32_t>(b) * kBlock + h * 32;
       v.c[i][0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bw, at, 0, 0));
       v.c[i][1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(bw, at, 16, 0));
       v.s[i] = __builtin_amdgcn_raw_buffer_load_b8(bs, ws[i] + static_cast<uint32_t>(b) * g.ws_block, 0, 0);
     }
+  };
+  auto load = [&](Block& v, int b) {
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+      __builtin_memcpy(v.x[f], xs[f] + static_cast<int64_t>(b) * kBlock, sizeof(v.x[f]));
+    load_weights(v, b);
   };
   auto multiply = [&](const Block& v) {
 #pragma unroll
@@ -472,15 +455,25 @@ __global__ void __launch_bounds__(few_waves(kRuns) * kWave) few_rows_kernel(FewA
       }
     }
   };
-  Block set[kAhead];
+  Block set;
+  for (int b = wave; b < whole; b += kFewWaves) {
+    load(set, b);
+    multiply(set);
+  }
+  if (whole < g.kb && wave == whole % kFewWaves) {
+    const int64_t col = static_cast<int64_t>(whole) * kBlock;
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d) load(set[d], wave + d * kFewWaves);
-  for (int b0 = wave; b0 < g.kb; b0 += kAhead * kFewWaves) {
+    for (int f = 0; f < kFrags; ++f)
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      multiply(set[d]);  // of a block past the last one: zeros
-      load(set[d], b0 + (kAhead + d) * kFewWaves);
-    }
+      for (int i = 0; i < 4; ++i) {
+        Reg part[8 / E::kPer];
+        load8_upto<XT>(xs[f] + col + 8 * i, g.k - col - h * 32 - 8 * i, part);
+#pragma unroll
+        for (int j = 0; j < 8 / E::kPer; ++j) set.x[f][8 / E::kPer * i + j] = part[j];
+        __builtin_amdgcn_sched_barrier(0);  // eight at a time: all of them would cost the loop its registers
+      }
+    load_weights(set, whole);
+    multiply(set);
   }
 #pragma unroll
   for (int f = 0; f < kFrags; ++f)
@@ -521,7 +514,6 @@ struct GemmArgs {
   uint32_t as_bytes, bs_bytes;  // bytes of scales
   void* out;
   int64_t ldo;
-  uint32_t wide;                // rows of out allow 16-byte stores
   uint32_t tiles_m, tiles_n;
   uint32_t whole;               // big tiles that are taken whole; the others in halves
   uint32_t splits;
@@ -779,18 +771,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int j = 0; j < kFn; ++j) v[e * kFn + j] = acc[i][j][4 * q + e];
-        if (g.wide && col + 4 * kFn <= g.n) {
+        if (col + 4 * kFn <= g.n) {  // 16 bytes at a time, at any alignment
           if constexpr (sizeof(OT) == 4) {
-#pragma unroll
-            for (int e = 0; e < kFn; ++e)
-              reinterpret_cast<f32x4*>(po + col)[e] = f32x4{v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]};
+            __builtin_memcpy(po + col, v, sizeof(v));
           } else {
-            static_assert(sizeof(OT) == 4 || kFn >= 2, "8 bf16 values per store");
+            uint32_t w[2 * kFn];
 #pragma unroll
-            for (int e = 0; e < 4 * kFn; e += 8)
-              *reinterpret_cast<u32x4*>(po + col + e) =
-                  u32x4{pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
-                        pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7])};
+            for (int e = 0; e < 2 * kFn; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            __builtin_memcpy(po + col, w, sizeof(w));
           }
         } else {
 #pragma unroll
@@ -842,9 +830,17 @@ __global__ void __launch_bounds__(256) join_kernel(const float* part, int64_t m,
     const float* p = part + row * ldp + col;
     f32x4 v = *reinterpret_cast<const f32x4*>(p);
     for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(p + s * m * ldp);
+    OT* po = out + row * ldo + col;
+    if (col + 4 <= n) {
+      OT w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < n) store1(out + row * ldo + col + e, v[e]);
+      for (int e = 0; e < 4; ++e) store1(w + e, v[e]);
+      __builtin_memcpy(po, w, sizeof(w));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < n) store1(po + e, v[e]);
+    }
   }
 }
 
@@ -878,20 +874,19 @@ template <typename XT, bool kTiles> int launch_quantize(const QuantArgs& q, hipS
   return launch_status();
 }
 
-template <typename XT, typename OT, int kRuns, bool kWide> int launch_few_runs(const FewArgs& g, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(g.n, 16 * kRuns))), block(few_waves(kRuns) * kWave);
-  if (g.m <= 16) hipLaunchKernelGGL((few_rows_kernel<XT, OT, 1, kRuns, kWide>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((few_rows_kernel<XT, OT, 2, kRuns, kWide>), grid, block, 0, s, g);
+template <typename XT, typename OT, int kRuns> int launch_few_runs(const FewArgs& g, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(g.n, 16 * kRuns))), block(few_waves(g.m <= 16 ? 1 : 2, kRuns) * kWave);
+  if (g.m <= 16) hipLaunchKernelGGL((few_rows_kernel<XT, OT, 1, kRuns>), grid, block, 0, s, g);
+  else hipLaunchKernelGGL((few_rows_kernel<XT, OT, 2, kRuns>), grid, block, 0, s, g);
   return launch_status();
 }
 
 // More weight rows per workgroup let more of them share one reading of x, fewer fill the chip more
 // evenly.  The time goes by what a CU has to read, per column of k: its rounds of workgroups times
-// their rows of weights and of x.  Measured for 24 rows of 11008 x 4096, 1 to 4 runs of 16: 31.9, 23.4,
-// 16.0 and 17.5 us; for 1 row of 4096 x 4096 6.7, 8.3, 9.9 and 11.7 us; the rule takes the least of each.
+// their rows of weights and of x.  Measured, in an earlier form of the kernel, for 24 rows of 11008 x
+// 4096, 1 to 4 runs of 16: 31.9, 23.4, 16.0 and 17.5 us; for 1 row of 4096 x 4096 6.7, 8.3, 9.9 and
+// 11.7 us; the rule takes the least of each.
 template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t s) {
-  const bool wide = aligned(g.x, 16) && (g.ldx * sizeof(XT)) % 16 == 0 && (g.k * sizeof(XT)) % 16 == 0;
-  if (!wide) return launch_few_runs<XT, OT, 2, false>(g, s);  // bound by loads of single elements
   int runs = 1;
   int64_t least = 0;
   for (int r = 1; r <= 4; ++r) {
@@ -902,10 +897,10 @@ template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t
     }
   }
   switch (runs) {
-    case 1: return launch_few_runs<XT, OT, 1, true>(g, s);
-    case 2: return launch_few_runs<XT, OT, 2, true>(g, s);
-    case 3: return launch_few_runs<XT, OT, 3, true>(g, s);
-    default: return launch_few_runs<XT, OT, 4, true>(g, s);
+    case 1: return launch_few_runs<XT, OT, 1>(g, s);
+    case 2: return launch_few_runs<XT, OT, 2>(g, s);
+    case 3: return launch_few_runs<XT, OT, 3>(g, s);
+    default: return launch_few_runs<XT, OT, 4>(g, s);
   }
 }
 
@@ -1008,7 +1003,6 @@ extern "C" int qopt_fp8_quantize(const void* x_dev, int dtype, int64_t rows, int
                        padded(cols), padded(rows),
                        form == QOPT_FP8_TILES ? ceil_div(cols, kBlock) : scale_stride(rows),
                        form == QOPT_FP8_TILES ? ceil_div(rows, kBlock) : scale_stride(cols),
-                       aligned(x_dev, 16) && (ldx * size) % 16 == 0 ? 1u : 0u,
                        static_cast<uint32_t>(ceil_div(cols, kBlock))};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == QOPT_F32)
@@ -1047,7 +1041,6 @@ extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scal
   if (need > 0 && (!workspace_dev || workspace_bytes < need)) return QOPT_EINVAL;
   const bool exact = out_dtype == QOPT_F32, tiles = b_form == QOPT_FP8_TILES;
   const Plan plan = plan_for(m, n, k, exact);
-  const size_t osize = exact ? 4 : 2;
   const int64_t kb = ceil_div(k, kBlock);
   GemmArgs g = {};
   g.a = a_codes_dev;
@@ -1067,7 +1060,6 @@ extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scal
     g.out = workspace_dev;
     g.ldo = partial_stride(n);
     g.split_stride = m * g.ldo;
-    g.wide = 1;
     rc = exact ? launch_gemm<true, float>(g, tiles, s) : launch_gemm<false, float>(g, tiles, s);
     if (rc != QOPT_OK) return rc;
     const int64_t wgs = ceil_div(m * (g.ldo / 4), 256);
@@ -1083,7 +1075,6 @@ extern "C" int qopt_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scal
   }
   g.out = out_dev;
   g.ldo = ldo;
-  g.wide = aligned(out_dev, 16) && (ldo * osize) % 16 == 0 ? 1u : 0u;
   if (plan.whole + plan.halves > 0)
     return exact ? launch_gemm_big<true, float>(g, plan, tiles, s) : launch_gemm_big<false, uint16_t>(g, plan, tiles, s);
   return exact ? launch_gemm<true, float>(g, tiles, s) : launch_gemm<false, uint16_t>(g, tiles, s);
@@ -1122,8 +1113,6 @@ extern "C" int qopt_fp8_linear(const void* x_dev, int dtype, int64_t m, int64_t 
     return QOPT_EALIGN;
   if (need > 0 && (!workspace_dev || workspace_bytes < need)) return QOPT_EINVAL;
   const bool tiles = w_form == QOPT_FP8_TILES;
-  // the few rows' kernel addresses x by 31-bit offsets
-  if (m <= QOPT_FP8_FEW_ROWS && ldx > QOPT_FP8_MAX_DIM) return QOPT_EINVAL;
   if (m > QOPT_FP8_FEW_ROWS) {
     uint8_t* codes = static_cast<uint8_t*>(workspace_dev);
     uint8_t* scales = codes + linear_codes_bytes(m, k);
@@ -1135,7 +1124,6 @@ extern "C" int qopt_fp8_linear(const void* x_dev, int dtype, int64_t m, int64_t 
   }
   const int64_t kb = ceil_div(k, kBlock);
   const FewArgs g = {x_dev, m, k, ldx, w_codes_dev, w_scales_dev, n, static_cast<uint32_t>(padded(k)),
-                     static_cast<uint32_t>(((m - 1) * ldx + k) * static_cast<int64_t>(size)),
                      static_cast<uint32_t>(tiles ? ceil_div(n, kBlock) * kb : rows_scale_bytes(n, k)),
                      static_cast<uint32_t>(tiles ? kb : 1), static_cast<uint32_t>(tiles ? 1 : scale_stride(n)),
                      static_cast<int32_t>(kb), tiles ? 7 : 0, out_dev, ldo};

@@ -15,8 +15,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._lib import (LIB, QOPT_BF16, QOPT_F32, QOPT_FP8_BLOCK, QOPT_FP8_FEW_ROWS,
-                   QOPT_FP8_MAX_DIM, QOPT_FP8_ROWS, QOPT_FP8_TILES)
+from ._lib import (LIB, QOPT_BF16, QOPT_F32, QOPT_FP8_BLOCK, QOPT_FP8_FEW_ROWS, QOPT_FP8_ROWS,
+                   QOPT_FP8_TILES)
 from .embedding import qopt_embedding_xavier_init
 
 _DT = {torch.float32: QOPT_F32, torch.bfloat16: QOPT_BF16}
@@ -206,8 +206,6 @@ def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
         raise ValueError("x must be 2-D with contiguous rows, or contiguous")
     dev = _same_gpu(x, w_codes, w_scales)
     m = x.shape[0] if x.dim() == 2 else x.shape[:-1].numel()
-    if m <= QOPT_FP8_FEW_ROWS and ldx > QOPT_FP8_MAX_DIM:  # further apart than one launch reaches
-        x, ldx = x.contiguous(), k
     out, ldo = _output(out, (*x.shape[:-1], n), out_dtype, dev)
     return _linear(x, dx, m, k, ldx, Fp8Matrix(w_codes, w_scales), form, out, do, ldo)
 

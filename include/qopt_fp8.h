@@ -95,8 +95,7 @@ int qopt_fp8_matmul_workspace(int64_t m, int64_t n, int64_t k, int out_dtype, si
  * out = x w^T for x_dev [m, k] as it is and a quantized w [n, k]: x is quantized in rows
  * as qopt_fp8_quantize does, then multiplied.  Up to QOPT_FP8_FEW_ROWS rows that is one
  * launch, in which the weights are read once; above, the result is that of the two calls.
- * Instructions and precision by out_dtype are those of qopt_fp8_matmul.  (ldx up to
- * QOPT_FP8_MAX_DIM in the first case: QOPT_EINVAL beyond.)
+ * Instructions and precision by out_dtype are those of qopt_fp8_matmul.
  * workspace_dev as above, of qopt_fp8_linear_workspace bytes.
  */
 int qopt_fp8_linear(const void* x_dev, int dtype, int64_t m, int64_t k, int64_t ldx,

@@ -58,8 +58,7 @@ def test_linear_checks():
 
     assert call(m=0) == OK and call(n=0, ldo=0) == OK
     for bad in (dict(m=-1), dict(n=-1), dict(k=-1), dict(ldx=255), dict(ldo=7), dict(x=None),
-                dict(w=None), dict(sw=None), dict(out=None), dict(m=33), dict(m=33, ws=P, nws=16),
-                dict(ldx=_lib.QOPT_FP8_MAX_DIM + 1)):
+                dict(w=None), dict(sw=None), dict(out=None), dict(m=33), dict(m=33, ws=P, nws=16)):
         assert call(**bad) == EINVAL, bad
     for bad in (dict(dt=3), dict(odt=3), dict(f=2)):
         assert call(**bad) == EUNSUPPORTED, bad
