@@ -169,6 +169,46 @@ def test_without_decay_the_8bit_step_is_adam8bits(q, pdt, gdt):
             assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("scale", [None, 0.37])
+@pytest.mark.parametrize("eps", [1e-8, 0.0])
+@pytest.mark.parametrize("pdt,gdt", PAIRS)
+def test_large_and_small_8bit_steps_agree(q, pdt, gdt, eps, scale):
+    """A step of many blocks leaves the bits that steps of its tensors one by one leave, which
+    another kernel takes: odd lengths and offsets, zero, subnormal and non-finite blocks."""
+    rng = np.random.default_rng(21)
+    sizes = SIZES + [1400 * BLOCK] * 3 + [5 * BLOCK + 3]
+    sets = []
+    for i, n in enumerate(sizes):
+        p, g = draws(n, pdt, rng, 0.02), draws(n, gdt, rng, 1e-3)
+        m, v = rng.integers(0, 256, n).astype(np.uint8), rng.integers(0, 256, n).astype(np.uint8)
+        am, av = (np.abs(rng.normal(0, s, -(-n // BLOCK))).astype(np.float32) for s in (1e-3, 1e-6))
+        if n == 17 * BLOCK:
+            gf = g if gdt == "f32" else oracle.bf16_to_f32(g)
+            gf = gf.copy()
+            gf[5], gf[3 * BLOCK], gf[4 * BLOCK + 9] = np.inf, np.nan, 1e30
+            gf[6 * BLOCK:8 * BLOCK] = 0
+            g = oracle.f32_to_bf16_rne(gf) if gdt == "bf16" else gf
+            am[6], av[6], am[9], av[9] = 0, 0, 1e-40, 1e-42
+        sets.append([to_dev(p, pdt), to_dev(g, gdt), to_dev(m), to_dev(v), to_dev(am), to_dev(av)])
+    # the last tensor one element into its buffers
+    for k in range(4):
+        buf = torch.empty(sizes[-1] + 1, dtype=sets[-1][k].dtype, device="cuda")
+        buf[1:] = sets[-1][k]
+        sets[-1][k] = buf[1:]
+    other = [[t.clone() for t in s] for s in sets]
+    gs = None if scale is None else torch.full((1,), scale, device="cuda")
+    hp = dict(HP, eps=eps)
+    for step in (1, 2, 3):
+        q.qopt_adamw8bit_step([tuple(s) for s in sets], step=step, grad_scale=gs, **hp)
+        for s in other:
+            q.qopt_adamw8bit_step([tuple(s)], step=step, grad_scale=gs, **hp)
+        for n, x, y in zip(sizes, sets, other):
+            for k, (a, b) in enumerate(zip(x, y)):
+                if a.is_floating_point():  # a NaN's sign and payload included
+                    a, b = (t.view(torch.int32 if t.dtype == torch.float32 else torch.int16) for t in (a, b))
+                assert torch.equal(a, b), (step, n, k)
+
+
 @pytest.mark.parametrize("nbits", [8, 32])
 def test_non_finite_gradients(q, nbits):
     """NaN and infinities stay within their block (8-bit state: it is stored as zeros) or
@@ -202,7 +242,7 @@ def test_steps_a_captured_graph_replays(q, nbits):
     and the clipping factor changed on the device: every replay is the eager step.  The
     bf16 call has more than one launch, which outside a capture use a second stream."""
     rng = np.random.default_rng(2)
-    sizes = [2048 * 40] * 50 + [2049] * 20
+    sizes = [2048 * 60] * 50 + [2049] * 20
     p = [to_dev(draws(n, "bf16", rng, 0.02), "bf16") for n in sizes]
     st = [[to_dev(x) for x in zero_state(n, nbits)] for n in sizes]
     g = [to_dev(draws(n, "bf16", rng, 1e-3), "bf16") for n in sizes]
