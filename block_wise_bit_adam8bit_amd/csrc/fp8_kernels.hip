@@ -557,12 +557,12 @@ __device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src,
 // One tile of kM x kN outputs from row m0 and column n0 on, by one workgroup; one step per block of 128
 // along k, steps `first` to `last`.
 //
-// A step's kM + kN rows of 128 codes are loaded from memory straight into one of two LDS buffers
-// (no registers), two steps ahead; its fragments are read from LDS half a step ahead, into one of
+// A step's kM + kN rows of 128 codes are loaded from memory straight into one of kBufs LDS buffers
+// (no registers), up to kBufs steps ahead; its fragments are read from LDS half a step ahead, into one of
 // two register sets:
 //     multiply half 0 of step t   | read half 1 of step t
 //     wait: step t + 1 has landed, every wave has read all of step t (one barrier per step)
-//     multiply half 1 of step t   | read half 0 of step t + 1, start loading step t + 2
+//     multiply half 1 of step t   | read half 0 of step t + 1, start loading step t + kBufs
 // with the LDS reads and loads spread between the matrix instructions, which take 64 cycles each
 // (reads issued ahead of them in one go kept the matrix units waiting: 4 % slower).
 //
@@ -578,7 +578,7 @@ __device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src,
 // which the matrix instructions alone take 206 us and the loads alone 280 us (193 us where the
 // operands lie in the last-level cache); three and four steps of 64 in flight were no faster, and
 // tiles of 4 waves of 128 x 128 6 % slower.
-template <int kM, int kN, int kWavesM, int kWavesN, bool kExact, bool kTilesB, typename OT>
+template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, bool kExact, bool kTilesB, typename OT>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64_t m0, int64_t n0, int first, int last,
                                           OT* out) {
   constexpr int kWaves = kWavesM * kWavesN;
@@ -700,58 +700,101 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto step_barrier = [&] {  // this wave's loads have landed and its reads are done; then all waves'
-    __builtin_amdgcn_s_waitcnt(0x0070);
+  // All but the last kLater of this wave's loads have landed and its reads are done; then all waves'.
+  constexpr int kLater = (kBufs - 2) * (kLoads + 2);
+  constexpr int kFirst = kLater + kLoads;
+  static_assert(kFirst < 64, "counts of loads under way");
+  auto step_barrier = [&] {
+    __builtin_amdgcn_s_waitcnt(0x0070 | (kLater & 15) | (kLater >> 4) << 14);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
 
   auto upto_last = [&](int t) { return t < last ? t : last; };
-  Scales c0 = load_scales(first), c1 = load_scales(upto_last(first + 1));
-  load_step(0, first);
-  __builtin_amdgcn_sched_barrier(0);
-  step_barrier();
-  load_step(1, upto_last(first + 1));
-  if constexpr (kExact && kFm * kFn > 4) {
-    // One register set: widened operands take the room of the second, and the other wave of the SIMD
-    // works meanwhile.  8192 x 4096 x 11008 in 550 us, 1.34 PFLOP/s (594 us with tiles of 128 x 128; 570 us
-    // with the widening spread between the matrix instructions).
-    for (int t = first; t <= last; ++t) {
-      const int buf = (t - first) & 1, ahead = upto_last(t + 2);
-      Frags f;
-      read_half(f, buf, 0);
-      multiply(f, c0);
+  if constexpr (kBufs > 2) {
+    // For tiles that have a CU to themselves and would wait for memory in every step: step t's loads are
+    // issued kBufs - 1/2 steps ahead, its scales' kBufs - 1.  1024 x 2048 x 4096 (128 x 128, 128 CUs) takes
+    // 17.2 us with three buffers, 23.8 with two and 17.2 with four; 4096 x 2048 x 8192 (128 x 256) 59.4 and
+    // 67.8.  The exact path, which widens its operands meanwhile, gains nothing (30.0 and 30.1) and keeps
+    // two.  Turns of kBufs steps, so that the registers of the scales have fixed places.
+    Scales c[kBufs];
+#pragma unroll
+    for (int u = 0; u < kBufs; ++u) {
+      if (u < kBufs - 1) c[u] = load_scales(upto_last(first + u));
+      load_step(u, upto_last(first + u));
       __builtin_amdgcn_sched_barrier(0);
-      read_half(f, buf, 1);
-      multiply(f, c0);
-      __builtin_amdgcn_sched_barrier(0);
-      step_barrier();
-      asm volatile("" : "+v"(c1.a), "+v"(c1.b));
-      const Scales c2 = load_scales(ahead);
-      load_step(buf, ahead);
-      c0 = c1;
-      c1 = c2;
     }
-  } else {
+    // of the loads behind step `first` one set of scales is not under way yet
+    __builtin_amdgcn_s_waitcnt(0x0070 | (kFirst & 15) | (kFirst >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     Frags f0, f1;
     read_half(f0, 0, 0);
-    for (int t = first; t <= last; ++t) {
-      // past the last step the last one is loaded again: no branch, which would keep the compiler from
-      // spreading the loads
-      const int buf = (t - first) & 1, ahead = upto_last(t + 2);
-      read_half(f1, buf, 1);
-      multiply(f0, c0);
-      spread(false);
-      step_barrier();
-      asm volatile("" : "+v"(c1.a), "+v"(c1.b));  // not used before the wait that it landed with
-      read_half(f0, buf ^ 1, 0);
-      const Scales c2 = load_scales(ahead);
-      load_step(buf, ahead);
-      multiply(f1, c0);
-      spread(true);
-      c0 = c1;
-      c1 = c2;
+    for (int t = first; t <= last;) {
+#pragma unroll
+      for (int u = 0; u < kBufs; ++u) {
+        constexpr int kLast = kBufs - 1;
+        c[(u + kLast) % kBufs] = load_scales(upto_last(t + kLast));
+        read_half(f1, u, 1);
+        multiply(f0, c[u]);
+        spread(false);
+        step_barrier();
+        asm volatile("" : "+v"(c[(u + 1) % kBufs].a), "+v"(c[(u + 1) % kBufs].b));
+        read_half(f0, (u + 1) % kBufs, 0);
+        load_step(u, upto_last(t + kBufs));
+        multiply(f1, c[u]);
+        spread(true);
+        if (++t > last) break;
+      }
+    }
+  } else {
+    Scales c0 = load_scales(first), c1 = load_scales(upto_last(first + 1));
+    load_step(0, first);
+    __builtin_amdgcn_sched_barrier(0);
+    step_barrier();
+    load_step(1, upto_last(first + 1));
+    if constexpr (kExact && kFm * kFn > 4) {
+      // One register set: widened operands take the room of the second, and the other wave of the SIMD
+      // works meanwhile.  8192 x 4096 x 11008 in 550 us, 1.34 PFLOP/s (594 us with tiles of 128 x 128; 570 us
+      // with the widening spread between the matrix instructions).
+      for (int t = first; t <= last; ++t) {
+        const int buf = (t - first) & 1, ahead = upto_last(t + 2);
+        Frags f;
+        read_half(f, buf, 0);
+        multiply(f, c0);
+        __builtin_amdgcn_sched_barrier(0);
+        read_half(f, buf, 1);
+        multiply(f, c0);
+        __builtin_amdgcn_sched_barrier(0);
+        step_barrier();
+        asm volatile("" : "+v"(c1.a), "+v"(c1.b));
+        const Scales c2 = load_scales(ahead);
+        load_step(buf, ahead);
+        c0 = c1;
+        c1 = c2;
+      }
+    } else {
+      Frags f0, f1;
+      read_half(f0, 0, 0);
+      for (int t = first; t <= last; ++t) {
+        // past the last step the last one is loaded again: no branch, which would keep the compiler from
+        // spreading the loads
+        const int buf = (t - first) & 1, ahead = upto_last(t + 2);
+        read_half(f1, buf, 1);
+        multiply(f0, c0);
+        spread(false);
+        step_barrier();
+        asm volatile("" : "+v"(c1.a), "+v"(c1.b));  // not used before the wait that it landed with
+        read_half(f0, buf ^ 1, 0);
+        const Scales c2 = load_scales(ahead);
+        load_step(buf, ahead);
+        multiply(f1, c0);
+        spread(true);
+        c0 = c1;
+        c1 = c2;
+      }
     }
   }
   __builtin_amdgcn_s_waitcnt(0x0070);  // no load is on its way into LDS when the workgroup ends
@@ -791,14 +834,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
 }
 
 // One workgroup per tile of 128 x 128 and split of k.
-template <bool kExact, bool kTilesB, typename OT>
+template <int kBufs, bool kExact, bool kTilesB, typename OT>
 __global__ void __launch_bounds__(256) gemm_kernel(GemmArgs g) {
-  __shared__ __align__(16) uint8_t lds[2 * 256 * kBlock];
+  __shared__ __align__(16) uint8_t lds[kBufs * 256 * kBlock];
   const uint32_t tiles = g.tiles_m * g.tiles_n, i = xcd_order(blockIdx.x, tiles * g.splits), split = i / tiles;
   const TileAt tile = tile_at(i % tiles, g.tiles_m, g.tiles_n);
   const int first = static_cast<int>(static_cast<int64_t>(g.kb) * split / g.splits);
   const int last = static_cast<int>(static_cast<int64_t>(g.kb) * (split + 1) / g.splits) - 1;
-  gemm_tile<128, 128, 2, 2, kExact, kTilesB, OT>(g, lds, tile.m * int64_t{128}, tile.n * int64_t{128}, first, last,
+  gemm_tile<128, 128, 2, 2, kBufs, kExact, kTilesB, OT>(g, lds, tile.m * int64_t{128}, tile.n * int64_t{128}, first, last,
                                                  static_cast<OT*>(g.out) + split * g.split_stride);
 }
 
@@ -806,17 +849,19 @@ __global__ void __launch_bounds__(256) gemm_kernel(GemmArgs g) {
 // half of the CUs or more without work.
 template <bool kExact, bool kTilesB, typename OT>
 __global__ void __launch_bounds__(512) gemm_big_kernel(GemmArgs g) {
-  __shared__ __align__(16) uint8_t lds[2 * 512 * kBlock];
+  constexpr int kHalfBufs = kExact ? 2 : 3;
+  constexpr int kLds = 2 * 512 > kHalfBufs * 384 ? 2 * 512 : kHalfBufs * 384;
+  __shared__ __align__(16) uint8_t lds[kLds * kBlock];
   OT* out = static_cast<OT*>(g.out);
   if (blockIdx.x < g.whole) {
     const TileAt tile = tile_at(xcd_order(blockIdx.x, g.whole), g.tiles_m, g.tiles_n);
-    gemm_tile<256, 256, 2, 4, kExact, kTilesB, OT>(g, lds, tile.m * int64_t{256}, tile.n * int64_t{256}, 0, g.kb - 1, out);
+    gemm_tile<256, 256, 2, 4, 2, kExact, kTilesB, OT>(g, lds, tile.m * int64_t{256}, tile.n * int64_t{256}, 0, g.kb - 1, out);
   } else {
     const uint32_t i = xcd_order(blockIdx.x - g.whole, gridDim.x - g.whole);
     const TileAt tile = tile_at(g.whole + i / 2, g.tiles_m, g.tiles_n);
     const int64_t m0 = tile.m * int64_t{256} + (i % 2) * 128;
     if (m0 < g.m)
-      gemm_tile<128, 256, 2, 4, kExact, kTilesB, OT>(g, lds, m0, tile.n * int64_t{256}, 0, g.kb - 1, out);
+      gemm_tile<128, 256, 2, 4, kHalfBufs, kExact, kTilesB, OT>(g, lds, m0, tile.n * int64_t{256}, 0, g.kb - 1, out);
   }
 }
 
@@ -912,23 +957,23 @@ struct Plan {
 };
 
 // The plan of least time by this model, in microseconds on 256 CUs.  A step (128 along k) takes a CU
-//   1.70 for one tile of 256 x 256 (2.52 PFLOP/s with all CUs busy), 1.1 for half of one,
-//   1.06 for two tiles of 128 x 128 side by side (2.03), 0.70 for one;
-//   the exact path 3.2, 2.1, 1.67 and 0.96.
+//   1.70 for one tile of 256 x 256 (2.52 PFLOP/s with all CUs busy), 0.92 for half of one,
+//   1.06 for two tiles of 128 x 128 side by side (2.03), 0.70 for one, and 0.50 with three buffers, where
+//   no CU has more than one; the exact path 3.2, 2.1, 1.67 and 0.96.
 // Small tiles cost a quarter more per product but fill the chip at a quarter of the size: 1024 x 4096 x
-// 4096 takes 25.5 us with them and 55 us with 64 whole tiles, 8192 x 4096 x 11008 363 us and 293 us.
+// 4096 takes 18 us with them and 55 us with 64 whole tiles, 8192 x 4096 x 11008 363 us and 293 us.
 // Splitting k, for products of too few tiles, adds a launch that joins the partial results (4) and
 // their way to memory and back (4 TB/s).
 Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
   const int64_t kb = ceil_div(k, kBlock);
   const int64_t small = ceil_div(m, 128) * ceil_div(n, 128), large = ceil_div(m, 256) * ceil_div(n, 256);
-  const double two = exact ? 1.67 : 1.06, one = exact ? 0.96 : 0.70;
+  const double two = exact ? 1.67 : 1.06, one = exact ? 0.96 : 0.70, alone = exact ? 0.96 : 0.50;
   Plan best = {0, 0, 1};
   double least = 0;
   for (int splits = 1; splits <= 16 && splits <= kb; splits *= 2) {
     const int64_t wgs = small * splits, steps = ceil_div(kb, splits);
     const int64_t rounds = wgs / 512, rest = wgs % 512;
-    double us = static_cast<double>(steps) * (rounds * two + (rest == 0 ? 0.0 : rest <= 256 ? one : two));
+    double us = static_cast<double>(steps) * (rounds * two + (rest == 0 ? 0.0 : rest > 256 ? two : rounds > 0 ? one : alone));
     if (splits > 1) us += 4.0 + static_cast<double>(splits) * m * n * 8 / 4e6;
     if (splits == 1 || us < least) {
       least = us;
@@ -938,7 +983,7 @@ Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
   }
   const int64_t rest = large % 256, halved = rest <= 128 ? rest : 0;
   const double us = static_cast<double>(kb) * (ceil_div(large - halved, 256) * (exact ? 3.2 : 1.70) +
-                                              (halved ? (exact ? 2.1 : 1.1) : 0.0));
+                                              (halved ? (exact ? 2.1 : 0.92) : 0.0));
   if (us <= least) best = {large - halved, 2 * halved, 1};
   return best;
 }
@@ -951,8 +996,15 @@ template <bool kExact, typename OT> int launch_gemm(GemmArgs g, bool b_tiles, hi
   const int64_t wgs = static_cast<int64_t>(g.tiles_m) * g.tiles_n * g.splits;
   if (wgs > kMaxGrid) return QOPT_EINVAL;
   const dim3 grid(static_cast<unsigned>(wgs));
-  if (b_tiles) hipLaunchKernelGGL((gemm_kernel<kExact, true, OT>), grid, dim3(256), 0, s, g);
-  else hipLaunchKernelGGL((gemm_kernel<kExact, false, OT>), grid, dim3(256), 0, s, g);
+  if constexpr (!kExact) {
+    if (wgs <= 256) {
+      if (b_tiles) hipLaunchKernelGGL((gemm_kernel<3, kExact, true, OT>), grid, dim3(256), 0, s, g);
+      else hipLaunchKernelGGL((gemm_kernel<3, kExact, false, OT>), grid, dim3(256), 0, s, g);
+      return launch_status();
+    }
+  }
+  if (b_tiles) hipLaunchKernelGGL((gemm_kernel<2, kExact, true, OT>), grid, dim3(256), 0, s, g);
+  else hipLaunchKernelGGL((gemm_kernel<2, kExact, false, OT>), grid, dim3(256), 0, s, g);
   return launch_status();
 }
 
