@@ -180,6 +180,22 @@ def test_matmul(q, m, n, k, dtype, tiles):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n", [(130, 200), (2048, 4096), (3000, 3100)])
+def test_every_number_of_blocks(q, m, n, dtype):
+    """One to nine blocks along the sum: fewer, as many and more than the steps that a kernel
+    has under way, in tiles of each size."""
+    for kb in range(1, 10):
+        rng = np.random.default_rng(kb)
+        k = kb * 128 - (kb % 3)
+        x, w = integers(rng, m, k, F32), integers(rng, n, k, F32)
+        want = (x.double() @ w.double().T).to(dtype)
+        a = q.qopt_fp8_quantize(x)
+        for tiles in (False, True):
+            got = q.qopt_fp8_matmul(*a, *q.qopt_fp8_quantize(w, tiles=tiles), dtype)
+            assert torch.equal(got, want), (k, tiles)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_matmul_into_strided_rows(q, dtype):
     """Rows of the result apart and at odd offsets; what lies between them stays."""
     rng = np.random.default_rng(9)
