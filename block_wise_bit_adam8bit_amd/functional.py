@@ -231,33 +231,41 @@ def qopt_adam8bit_step(tensors, *, lr, beta1, beta2, eps, step, _prepared=None):
 
 class AdamWPlan:
     """The launch descriptors of an AdamW step over one list of tensors, made by
-    qopt_adamw8bit_plan or qopt_adamw32bit_plan and stepped any number of times.  It holds
-    references to the tensors, whose storage must stay where it is."""
+    qopt_adamw8bit_plan or qopt_adamw32bit_plan and stepped any number of times.  It keeps
+    the memory that the tensors had when it was made and steps that memory: a tensor that
+    is given other memory later (``p.data = ...``) needs a new plan."""
 
-    __slots__ = ("bits", "tensors", "array", "pdtype", "gdtype", "device")
+    __slots__ = ("bits", "tensors", "storages", "array", "pdtype", "gdtype", "device")
 
     def __init__(self, bits, tensors, array, pdtype, gdtype, device):
         self.bits, self.tensors, self.array = bits, tensors, array
         self.pdtype, self.gdtype, self.device = pdtype, gdtype, device
+        self.storages = [x.untyped_storage() for t in tensors for x in t]
+
+
+def _check_spans(spans):
+    """Refuse lists in which a tensor that the step writes shares memory with another: its
+    blocks would be updated by two waves at once.  ``spans``: (first byte, end, written)."""
+    spans.sort()
+    end = end_written = 0  # furthest end of all spans so far, and of the written ones
+    for lo, hi, written in spans:
+        if lo < (end if written else end_written):
+            raise ValueError("the tensors of one step must not overlap (a parameter listed twice?)")
+        if hi > end:
+            end = hi
+        if written and hi > end_written:
+            end_written = hi
 
 
 def _check_disjoint(tensors):
-    """Refuse lists in which a tensor that the step writes shares memory with another:
-    its blocks would be updated by two waves at once."""
+    """_check_spans of tuples of tensors of which a step writes all but the second."""
     spans = []
     for t in tensors:
         for i, x in enumerate(t):
             n = x.numel() * x.element_size()
             if n:
                 spans.append((x.data_ptr(), x.data_ptr() + n, i != 1))
-    spans.sort()
-    end, end_written = 0, 0  # furthest end of all spans so far, and of the written ones
-    for lo, hi, written in spans:
-        if lo < (end if written else end_written):
-            raise ValueError("the tensors of one step must not overlap (a parameter listed twice?)")
-        end = max(end, hi)
-        if written:
-            end_written = max(end_written, hi)
+    _check_spans(spans)
 
 
 def qopt_adamw8bit_plan(tensors):
@@ -274,15 +282,17 @@ def qopt_adamw32bit_plan(tensors):
     (fp32 or bf16 params and grads, fp32 moments); none may overlap another."""
     tensors = [tuple(t) for t in tensors]
     arr = (_lib.qopt_tensor32 * len(tensors))()
-    pdt = gdt = dev = None
+    dev = pair = None
+    spans = []
     for i, (p, g, m, v) in enumerate(tensors):
         n = p.numel()
-        if p.dtype not in _DTYPES or g.dtype not in _DTYPES:
-            raise TypeError("params and grads must be float32 or bfloat16")
-        if pdt is None:
-            pdt, gdt = _DTYPES[p.dtype], _DTYPES[g.dtype]
-        elif (_DTYPES[p.dtype], _DTYPES[g.dtype]) != (pdt, gdt):
-            raise TypeError("one call takes one (param dtype, grad dtype) pair")
+        if (p.dtype, g.dtype) != pair:
+            if p.dtype not in _DTYPES or g.dtype not in _DTYPES:
+                raise TypeError("params and grads must be float32 or bfloat16")
+            if pair is not None:
+                raise TypeError("one call takes one (param dtype, grad dtype) pair")
+            pair = p.dtype, g.dtype
+            psize, gsize = p.element_size(), g.element_size()
         if m.dtype != torch.float32 or v.dtype != torch.float32:
             raise TypeError("moments must be float32")
         if g.numel() != n or m.numel() != n or v.numel() != n:
@@ -292,10 +302,14 @@ def qopt_adamw32bit_plan(tensors):
             dev = d
         elif d != dev:
             raise ValueError("all tensors of one call must be on the same GPU")
-        arr[i] = _lib.qopt_tensor32(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), n)
-    _check_disjoint(tensors)
-    return AdamWPlan(32, tensors, arr, QOPT_F32 if pdt is None else pdt,
-                     QOPT_F32 if gdt is None else gdt, dev)
+        pp, gp, mp, vp = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
+        arr[i] = (pp, gp, mp, vp, n)
+        if n:
+            spans += ((pp, pp + psize * n, True), (gp, gp + gsize * n, False), (mp, mp + 4 * n, True),
+                      (vp, vp + 4 * n, True))
+    _check_spans(spans)
+    pdt, gdt = (QOPT_F32, QOPT_F32) if pair is None else (_DTYPES[pair[0]], _DTYPES[pair[1]])
+    return AdamWPlan(32, tensors, arr, pdt, gdt, dev)
 
 
 def _adamw_args(plan, bits, lr, beta1, beta2, eps, weight_decay, step, grad_scale):

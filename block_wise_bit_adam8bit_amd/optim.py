@@ -26,8 +26,7 @@ from collections import defaultdict
 import torch
 
 from .checkpoint import compress_moments_multi, decompress_moments_multi
-from .functional import (make_tensor_array, nblocks, qopt_adam8bit_step, qopt_adamw8bit_plan,
-                         qopt_adamw8bit_step, qopt_adamw32bit_plan, qopt_adamw32bit_step)
+from .functional import make_tensor_array, nblocks, qopt_adam8bit_step, qopt_adamw8bit_step, qopt_adamw32bit_step
 
 _STATE_KEYS = ("m_codes", "v_codes", "m_absmax", "v_absmax")
 _CODE_ALIGN = 256  # bytes between the starts of consecutive parameters' codes
@@ -261,7 +260,6 @@ class AdamW(torch.optim.Optimizer):
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
                                       weight_decay=weight_decay, state_bits=state_bits,
                                       min_8bit_size=min_8bit_size))
-        self._plans = {}
 
     def add_param_group(self, param_group):
         g = {**self.defaults, **param_group}
@@ -306,8 +304,13 @@ class AdamW(torch.optim.Optimizer):
                     raise RuntimeError("AdamW does not take sparse gradients")
                 if not p.is_contiguous() or not p.grad.is_contiguous():
                     raise RuntimeError("AdamW needs contiguous parameters and gradients")
-        plans = {}
-        for gi, group in enumerate(self.param_groups):
+                if not p.is_cuda or p.grad.device != p.device:
+                    raise ValueError("AdamW needs parameters and gradients on a GPU")
+                if not {p.dtype, p.grad.dtype} <= {torch.float32, torch.bfloat16}:
+                    raise TypeError("AdamW needs float32 or bfloat16 parameters and gradients")
+                if grad_scale is not None and grad_scale.device != p.device:
+                    raise ValueError("grad_scale must be on the parameters' GPU")
+        for group in self.param_groups:
             live = [p for p in group["params"] if p.grad is not None]
             self._init_states(group, [p for p in live if not self.state[p]])
             batches = {}
@@ -318,25 +321,13 @@ class AdamW(torch.optim.Optimizer):
                 batches.setdefault(key, []).append((p, p.grad, *(st[k] for k in keys)))
             b1, b2 = group["betas"]
             for key, items in batches.items():
-                # a batch's plan is kept while its tensors stay where they are; plans that
-                # this step does not use are dropped with what they hold
-                ident = (gi, key[:4], tuple(x.data_ptr() for t in items for x in t))
                 coded = key[3] == len(_STATE_KEYS)
-                plan = self._plans.get(ident)
-                if plan is None:
-                    plan = (qopt_adamw8bit_plan if coded else qopt_adamw32bit_plan)(items)
-                plans[ident] = plan
                 run = qopt_adamw8bit_step if coded else qopt_adamw32bit_step
-                run(plan, lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
+                run(items, lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
                     weight_decay=group["weight_decay"], step=key[4], grad_scale=grad_scale)
                 for t in items:
                     self.state[t[0]]["step"] = key[4]
-        self._plans = plans
         return loss
-
-    def __setstate__(self, state):
-        super().__setstate__(state)
-        self._plans = {}
 
     _params_by_saved_id = Adam8bit._params_by_saved_id
 
@@ -357,7 +348,6 @@ class AdamW(torch.optim.Optimizer):
             for k in (saved if keys is None else keys):
                 if k != "params":
                     group[k] = saved[k]
-        self._plans = {}
 
     def load_state_dict(self, state_dict):
         """Load a state dict of ``AdamW`` or ``Adam8bit``; each parameter keeps the kind of

@@ -449,7 +449,7 @@ def test_optimizer_resumes_and_converts(q, tmp_path):
         opt.step(), again.step()
     for a, b in zip(params, twin):
         assert torch.equal(a, b)
-    assert third.state and third._plans == {}
+    assert third.state
     # to torch.optim.AdamW and back: fp32 moments travel unchanged, coded ones as their values
     sd = opt.fp32_adam_state_dict()
     ref = torch.optim.AdamW([torch.nn.Parameter(p.detach().clone()) for p in params])
@@ -489,7 +489,6 @@ def test_optimizer_moves_with_its_tensors(q):
         opt.step(), ropt.step()
     for a, b in zip(params, ref):
         assert torch.equal(a, b)
-    assert len(opt._plans) == 2  # one per kind
 
 
 def test_optimizer_refuses(q):
@@ -509,3 +508,37 @@ def test_optimizer_refuses(q):
     src = torch.optim.AdamW([torch.nn.Parameter(torch.zeros(64, 64))], amsgrad=True)
     with pytest.raises(ValueError):
         opt.load_fp32_adam_state(src.state_dict())
+
+
+def test_optimizer_refuses_before_any_state(q):
+    """Every group is looked over first: nothing has moved when one of them is refused."""
+    good = torch.nn.Parameter(torch.ones(64, 64, device="cuda"))
+    half = torch.nn.Parameter(torch.ones(64, 64, device="cuda", dtype=torch.float16))
+    for p in (good, half):
+        p.grad = torch.ones_like(p)
+    opt = q.AdamW([dict(params=[good]), dict(params=[half])])
+    with pytest.raises(TypeError):
+        opt.step()
+    assert not any(opt.state.values()) and bool((good == 1).all())
+    opt = q.AdamW([good])
+    with pytest.raises(ValueError):
+        opt.step(grad_scale=torch.ones(1))
+    assert not any(opt.state.values()) and bool((good == 1).all())
+
+
+@pytest.mark.parametrize("nbits", [8, 32])
+def test_a_plan_steps_the_memory_it_was_made_of(q, nbits):
+    """A parameter given other memory leaves its plan with the old, which the plan keeps."""
+    n = 5 * BLOCK + 3
+    p = torch.nn.Parameter(torch.ones(n, device="cuda"))
+    g = torch.ones(n, device="cuda")
+    state = [to_dev(s) for s in zero_state(n, nbits)]
+    plan = (q.qopt_adamw8bit_plan if nbits == 8 else q.qopt_adamw32bit_plan)([(p, g, *state)])
+    old = p.data
+    p.data = torch.full((n,), 3.0, device="cuda")
+    own_step(q, nbits)(plan, step=1, **HP)
+    assert bool((p == 3).all()) and bool((old < 1).all())
+    del old
+    other = [torch.full((n,), 5.0, device="cuda") for _ in range(20)]  # would take freed memory
+    own_step(q, nbits)(plan, step=2, **HP)
+    assert all(bool((o == 5).all()) for o in other) and bool((p == 3).all())

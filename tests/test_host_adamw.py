@@ -4,6 +4,7 @@ the plan's check that tensors do not overlap."""
 import ctypes
 
 import pytest
+import torch
 
 qopt = pytest.importorskip("block_wise_bit_adam8bit_amd")
 from block_wise_bit_adam8bit_amd import _lib, functional  # noqa: E402
@@ -85,3 +86,12 @@ def test_overlap_check():
                 [(a, b, c, d), (a[99:], b[:1], torch.zeros(1), torch.zeros(1))]):
         with pytest.raises(ValueError):
             check(bad)
+
+
+def test_optimizer_refuses_cpu_parameters():
+    p = torch.nn.Parameter(torch.ones(8192))
+    p.grad = torch.ones(8192)
+    opt = qopt.AdamW([p])
+    with pytest.raises(ValueError):
+        opt.step()
+    assert not any(opt.state.values())
