@@ -155,7 +155,15 @@ def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
     return (a, b) if normal and transposed else a if normal else b
 
 
-def _output(out, shape, dtype, dev):
+def _span(t):
+    """First byte and end of the memory that a tensor's elements lie in."""
+    at = t.data_ptr()
+    if not t.numel():
+        return at, at
+    return at, at + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _output(out, shape, dtype, dev, *operands):
     """The output tensor and the distance of its rows."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev), shape[-1]
@@ -164,6 +172,11 @@ def _output(out, shape, dtype, dev):
         raise ValueError(f"out must have shape {tuple(shape)} and dtype {dtype}")
     if out.device != dev:
         raise ValueError("all tensors must be on the same GPU")
+    lo, hi = _span(out)
+    for t in operands:
+        first, end = _span(t)
+        if first < hi and lo < end:
+            raise ValueError("out must not overlap an operand")
     if out.dim() == 2:
         return out, _row_stride(out, "out")
     if not out.is_contiguous():
@@ -181,7 +194,8 @@ def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat
     if b_codes.shape[1] != a_codes.shape[1]:
         raise ValueError("a and b must have the same number of columns")
     dev = _same_gpu(a_codes, a_scales, b_codes, b_scales)
-    out, ldo = _output(out, (a_codes.shape[0], b_codes.shape[0]), out_dtype, dev)
+    out, ldo = _output(out, (a_codes.shape[0], b_codes.shape[0]), out_dtype, dev,
+                       a_codes, a_scales, b_codes, b_scales)
     return _matmul(Fp8Matrix(a_codes, a_scales), Fp8Matrix(b_codes, b_scales), fb, out, dt, ldo)
 
 
@@ -206,7 +220,7 @@ def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
         raise ValueError("x must be 2-D with contiguous rows, or contiguous")
     dev = _same_gpu(x, w_codes, w_scales)
     m = x.shape[0] if x.dim() == 2 else x.shape[:-1].numel()
-    out, ldo = _output(out, (*x.shape[:-1], n), out_dtype, dev)
+    out, ldo = _output(out, (*x.shape[:-1], n), out_dtype, dev, x, w_codes, w_scales)
     return _linear(x, dx, m, k, ldx, Fp8Matrix(w_codes, w_scales), form, out, do, ldo)
 
 
@@ -257,13 +271,21 @@ class Fp8LinearFunction(torch.autograd.Function):
 def fp8_linear(x, w):
     """x w^T with gradients: x [..., k] and w [n, k] in float32 or bfloat16.  The result and
     x's gradient have x's type, w's gradient has w's.  The weight is quantized anew in every
-    call; a server quantizes it once and calls ``qopt_fp8_linear``."""
+    call; a server quantizes it once and calls ``qopt_fp8_linear``.  A forward and backward
+    pass may be captured into a graph as any of torch's: with no other result of the same
+    leaves alive whose backward ran, or will run, outside of it."""
     _check_dtype(x.dtype, "x")
     _check_dtype(w.dtype, "w")
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError("x must be [..., k] and w [n, k]")
     _same_gpu(x, w)
-    return Fp8LinearFunction.apply(x, w)
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+        return Fp8LinearFunction.apply(x, w)
+    wq = _quantize(w.detach().contiguous(), _DT[w.dtype], w.shape[1], True, True, False)[0]
+    x = x.detach()
+    if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < x.shape[1]:
+        x = x.contiguous()
+    return qopt_fp8_linear(x, *wq)
 
 
 class Fp8Linear(torch.nn.Module):

@@ -79,7 +79,8 @@ int qopt_fp8_quantize(const void* x_dev, int dtype, int64_t rows, int64_t cols, 
  *     bf16 matrix instructions, whose products and sums are binary32.  Element values
  *     under 2^-126 may count as 0 here.
  * A NaN element makes its whole row (of A) or column (of B) of the result NaN.
- * out_dev: rows ldo >= n elements apart; elements between n and ldo are left as they are.
+ * out_dev: rows ldo >= n elements apart; elements between n and ldo are left as they are.  It
+ * must not overlap an operand.
  * workspace_dev: at least qopt_fp8_matmul_workspace(m, n, k, ...) bytes, 16-byte aligned
  * (NULL if that is 0); scratch whose contents need no preparation, for one call at a time.
  * m or n 0: nothing is written; k 0: out is all 0.

@@ -223,6 +223,61 @@ def test_nan_stays_in_its_row_and_column(q, dtype):
     assert np.array_equal(np.isnan(few), want[:10])
 
 
+@pytest.mark.parametrize("m", [5, 150])
+@pytest.mark.parametrize("x_size,w_size", [(1e37, 1e-37), (1e-36, 1e36), (1e-38, 1e38), (1e-41, 1e38),
+                                           (1e38, 1e-38), (1e-20, 1e-18), (1e-19, 1e-25)])
+def test_sizes_at_the_ends_of_the_range(q, x_size, w_size, m):
+    """Scales near both ends: as everywhere, but that binary32 results may take element values
+    under 2^-126 as 0, and that a subnormal result is off by half a step of its own (2^-150 and
+    2^-134) besides, and each binary32 sum before it by 2^-150."""
+    rng = np.random.default_rng(1)
+    x = torch.from_numpy(np.clip(rng.normal(0, 1, (m, 260)), -2.5, 2.5) * x_size).float().cuda()
+    w = torch.from_numpy(np.clip(rng.normal(0, 1, (70, 260)), -2.5, 2.5) * w_size).float().cuda()
+    a, b = q.qopt_fp8_quantize(x), q.qopt_fp8_quantize(w, tiles=True)
+    for dtype in (F32, BF16):
+        want, tol = bound(pair(a), pair(b), dtype, dtype == F32)
+        tol += (2.0 ** -134 if dtype == BF16 else 0) + 400 * 2.0 ** -150
+        if dtype == F32:
+            va, vb = (np.abs(fp8.dequantize(*pair(t))) for t in (a, b))
+            tol += np.where(va < 2.0 ** -126, va, 0) @ vb.T + va @ np.where(vb < 2.0 ** -126, vb, 0).T
+        for got in (q.qopt_fp8_matmul(*a, *b, dtype), q.qopt_fp8_linear(x, *b, dtype)):
+            err = np.abs(host(got) - want)
+            assert np.all(err <= tol), (dtype, err.max(), (err / tol).max())
+
+
+def test_out_that_overlaps_is_refused(q):
+    x = torch.ones(40, 128, device="cuda")
+    w = q.qopt_fp8_quantize(torch.ones(128, 128, device="cuda"), tiles=True)
+    with pytest.raises(ValueError):
+        q.qopt_fp8_linear(x, *w, out=x)
+    a = q.qopt_fp8_quantize(x)
+    room = torch.empty(40 * 128 * 4, dtype=torch.uint8, device="cuda")
+    codes = room[100 * 16:100 * 16 + 40 * 128].view(torch.float8_e4m3fn).view(40, 128)
+    codes.copy_(a.codes)
+    with pytest.raises(ValueError):
+        q.qopt_fp8_matmul(codes, a.scales, *w, F32, out=room.view(F32).view(40, 128))
+    got = q.qopt_fp8_matmul(codes, a.scales, *w, F32, out=torch.empty(40, 128, device="cuda"))
+    assert bool((got == 128).all())
+
+
+@pytest.mark.parametrize("m", [3, 80])
+def test_without_gradients(q, m):
+    """No gradient wanted: the result of the quantized weight, whatever the leaves ask for."""
+    x = torch.randn(m, 300, device="cuda", dtype=BF16, requires_grad=True)
+    w = torch.randn(70, 300, device="cuda", requires_grad=True)
+    want = q.qopt_fp8_linear(x.detach(), *q.qopt_fp8_quantize(w.detach(), tiles=True))
+    with torch.no_grad():
+        y = q.fp8_linear(x, w)
+    assert not y.requires_grad and torch.equal(y, want)
+    assert torch.equal(q.fp8_linear(x.detach().view(1, m, 300), w.detach())[0], want)
+    wide = torch.zeros(m, 310, device="cuda", dtype=BF16)
+    wide[:, 5:305] = x.detach()
+    assert torch.equal(q.fp8_linear(wide[:, 5:305], w.detach()), want)
+    assert torch.equal(q.fp8_linear(x.detach().t().contiguous().t(), w.detach()), want)
+    same = q.fp8_linear(x.detach()[:1].expand(m, 300), w.detach())
+    assert torch.equal(same, want[:1].expand(m, 70))
+
+
 def test_empty_products(q):
     z = lambda r, k: q.Fp8Matrix(torch.empty(r, k, dtype=torch.float8_e4m3fn, device="cuda"),  # noqa: E731
                                  torch.empty(k // 128, -(-r // 16) * 16, dtype=torch.uint8, device="cuda"))
