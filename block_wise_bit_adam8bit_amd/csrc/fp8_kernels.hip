@@ -571,11 +571,14 @@ __device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src,
 // picks its byte.  (A byte load per fragment from scales laid out row by row touched 32 cache lines
 // each and cost a third of the time: 8192 x 4096 x 11008 at 1.7 PFLOP/s instead of 2.3.)  It also
 // leaves each lane with kFn * 4 consecutive columns of the result.
-// The 16-byte piece c of a row lies at place c ^ (row / kF % 8): 8 lanes that read one piece of
-// their rows touch all banks once.
+// In LDS a fragment's 32 rows follow each other, and the 16-byte piece c of row r lies at place
+// c ^ (r / 2 % 8): 16 lanes that read one piece of their rows touch all 64 banks once.  (Rows in the
+// operand's order leave half of the banks to any one read: 1024 x 2048 x 4096 17.0 us instead of 16.4, 4096^3
+// 56.3 and 54.7, 11008 x 4096 x 8192 312 and 308; but 8192 x 4096 x 11008, where rows 4 apart lie in few
+// channels of the L2, 300 and 308.)
 //
-// Measured (8-bit, 256 x 256 tiles of 8 waves): 8192 x 4096 x 11008 in 293 us, 2.52 PFLOP/s, of
-// which the matrix instructions alone take 206 us and the loads alone 280 us (193 us where the
+// Measured (8-bit, 256 x 256 tiles of 8 waves): 8192 x 4096 x 11008 in 293 to 308 us, 2.4 to 2.5 PFLOP/s,
+// of which the matrix instructions alone take 206 us and the loads alone 280 us (193 us where the
 // operands lie in the last-level cache); three and four steps of 64 in flight were no faster, and
 // tiles of 4 waves of 128 x 128 6 % slower.
 template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, bool kExact, bool kTilesB, typename OT>
@@ -584,31 +587,31 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
   constexpr int kWaves = kWavesM * kWavesN;
   constexpr int kWm = kM / kWavesM, kWn = kN / kWavesN;  // a wave's part of the tile
   constexpr int kFm = kWm / 32, kFn = kWn / 32;          // fragments of 32 per wave
-  constexpr int kShiftM = kFm == 4 ? 2 : kFm - 1, kShiftN = kFn == 4 ? 2 : kFn - 1;
   constexpr int kRows = kM + kN;
   constexpr int kLoads = kRows / 8 / kWaves;             // 8 rows per wave and load
   static_assert(kM % (8 * kWaves) == 0 && kN % (8 * kWaves) == 0, "whole loads per operand");
   static_assert((kFm == 1 || kFm == 2 || kFm == 4) && (kFn == 1 || kFn == 2 || kFn == 4), "scale loads");
   static_assert(kBlock % kWn == 0 || !kTilesB, "a wave's columns lie in one tile of scales");
-  // the places that a lane's loads fill must not depend on the load: rows 8 * kWaves apart differ by
-  // a multiple of 8 in row / kF
-  static_assert((8 * kWaves >> kShiftM) % 8 == 0 && (8 * kWaves >> kShiftN) % 8 == 0, "places");
+  static_assert(kWaves % (2 * kFm) == 0 && kWaves % (2 * kFn) == 0, "a wave's loads fill the same eight rows of 16");
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / kWavesN, wn = wave % kWavesN;
   const __amdgpu_buffer_rsrc_t ra = rows_buffer(g.a, m0, g.m, kM, g.kp);
   const __amdgpu_buffer_rsrc_t rb = rows_buffer(g.b, n0, g.n, kN, g.kp);
-  const uint32_t row8 = wave * 8 + (lane >> 3);
-  const uint32_t piece_a = ((lane & 7) ^ ((row8 >> kShiftM) & 7)) * 16;
-  const uint32_t piece_b = ((lane & 7) ^ ((row8 >> kShiftN) & 7)) * 16;
-  // Lane l of a wave fills bytes 16 l .. 16 l + 15 of its 8 rows in LDS.  A row past the operand's
-  // last one lies past its buffer's end and reads as 0.
+  // Lane l of a wave fills bytes 16 l .. 16 l + 15 of 8 rows in LDS, which are kF apart in the operand;
+  // kF waves together read 8 kF rows that follow each other.  A row past the operand's last one lies past its buffer's
+  // end and reads as 0.
+  const uint32_t piece_a = ((lane & 7) ^ ((wave / kFm & 1) * 4 + (lane >> 4))) * 16;
+  const uint32_t piece_b = ((lane & 7) ^ ((wave / kFn & 1) * 4 + (lane >> 4))) * 16;
   auto load_step = [&](int buf, int t) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int row = (i * kWaves + wave) * 8;  // first of this load's 8 rows
       const bool is_a = i * kWaves * 8 < kM;
-      const uint32_t from = static_cast<uint32_t>((is_a ? row : row - kM) + (lane >> 3)) * g.kp;
+      const int part = is_a ? kWm : kWn, frags = is_a ? kFm : kFn;
+      const int at = (i * kWaves + wave) * 8 - (is_a ? 0 : kM);  // rows of the operand before this run's
+      const int frag = at / 8 % frags, eight = at % part / (8 * frags);
+      const int row = (is_a ? 0 : kM) + at / part * part + frag * 32 + eight * 8;  // its first row in LDS
+      const uint32_t from = static_cast<uint32_t>(at / (8 * frags) * (8 * frags) + frag + frags * (lane >> 3)) * g.kp;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_void*)(lds + (buf * kRows + row) * kBlock), 16,
                                                from + (is_a ? piece_a : piece_b), t * kBlock, 0, 0);
     }
@@ -627,9 +630,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
   };
 
   const int h = lane >> 5;
-  const uint32_t at = ((2 * h) ^ (lane & 7)) << 4;
-  uint32_t oa = (wm * kWm + (lane & 31) * kFm) * kBlock + at;
-  uint32_t ob = (kM + wn * kWn + (lane & 31) * kFn) * kBlock + at;
+  const uint32_t at = ((2 * h) ^ ((lane >> 1) & 7)) << 4;
+  uint32_t oa = (wm * kWm + (lane & 31)) * kBlock + at;
+  uint32_t ob = (kM + wn * kWn + (lane & 31)) * kBlock + at;
   struct Frags {
     i32x4 a[kFm][2], b[kFn][2];
   };
@@ -638,13 +641,13 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, uint8_t* lds, int64
     const uint32_t a0 = (oa ^ (half * 64)) + buf * (kRows * kBlock), b0 = (ob ^ (half * 64)) + buf * (kRows * kBlock);
 #pragma unroll
     for (int j = 0; j < kFn; ++j) {
-      f.b[j][0] = *reinterpret_cast<const i32x4*>(lds + b0 + j * kBlock);
-      f.b[j][1] = *reinterpret_cast<const i32x4*>(lds + (b0 ^ 16) + j * kBlock);
+      f.b[j][0] = *reinterpret_cast<const i32x4*>(lds + b0 + j * (32 * kBlock));
+      f.b[j][1] = *reinterpret_cast<const i32x4*>(lds + (b0 ^ 16) + j * (32 * kBlock));
     }
 #pragma unroll
     for (int i = 0; i < kFm; ++i) {
-      f.a[i][0] = *reinterpret_cast<const i32x4*>(lds + a0 + i * kBlock);
-      f.a[i][1] = *reinterpret_cast<const i32x4*>(lds + (a0 ^ 16) + i * kBlock);
+      f.a[i][0] = *reinterpret_cast<const i32x4*>(lds + a0 + i * (32 * kBlock));
+      f.a[i][1] = *reinterpret_cast<const i32x4*>(lds + (a0 ^ 16) + i * (32 * kBlock));
     }
   };
 
