@@ -577,8 +577,8 @@ __device__ __forceinline__ uint32_t load_scale_bytes(__amdgpu_buffer_rsrc_t src,
 // In LDS a fragment's 32 rows follow each other, and the 16-byte piece c of row r lies at place
 // c ^ (r / 2 % 8): 16 lanes that read one piece of their rows touch all 64 banks once.  (Rows in the
 // operand's order leave half of the banks to any one read: 1024 x 2048 x 4096 17.0 us instead of 16.4, 4096^3
-// 56.3 and 54.7, 11008 x 4096 x 8192 312 and 308; but 8192 x 4096 x 11008, where rows 4 apart lie in few
-// channels of the L2, 300 and 308.)
+// 56.3 and 54.7, 11008 x 4096 x 8192 312 and 308; but 8192 x 4096 x 11008 300 and 308, also with another
+// conflict-free layout whose loads read 8 rows that follow each other.)
 //
 // Measured (8-bit, 256 x 256 tiles of 8 waves): 8192 x 4096 x 11008 in 293 to 308 us, 2.4 to 2.5 PFLOP/s,
 // of which the matrix instructions alone take 206 us and the loads alone 280 us (193 us where the
