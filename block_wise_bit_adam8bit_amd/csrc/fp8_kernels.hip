@@ -967,7 +967,7 @@ struct Plan {
 //   1.06 for two tiles of 128 x 128 side by side (2.03), 0.70 for one, and 0.50 with three buffers, where
 //   no CU has more than one; the exact path 3.2, 2.1, 1.67 and 0.96.
 // Small tiles cost a quarter more per product but fill the chip at a quarter of the size: 1024 x 4096 x
-// 4096 takes 18 us with them and 55 us with 64 whole tiles, 8192 x 4096 x 11008 363 us and 293 us.
+// 4096 takes 18 us with them and 55 us with 64 whole tiles, 8192 x 4096 x 11008 363 us and 300 us.
 // Splitting k, for products of too few tiles, adds a launch that joins the partial results (4) and
 // their way to memory and back (4 TB/s).
 Plan plan_for(int64_t m, int64_t n, int64_t k, bool exact) {
