@@ -240,7 +240,12 @@ class AdamWPlan:
     def __init__(self, bits, tensors, array, pdtype, gdtype, device):
         self.bits, self.tensors, self.array = bits, tensors, array
         self.pdtype, self.gdtype, self.device = pdtype, gdtype, device
-        self.storages = [x.untyped_storage() for t in tensors for x in t]
+        self.storages = ()
+
+    def keep(self):
+        """Hold the tensors' memory too, for a plan that is stepped more than once."""
+        self.storages = [x.untyped_storage() for t in self.tensors for x in t]
+        return self
 
 
 def _check_spans(spans):
@@ -257,34 +262,18 @@ def _check_spans(spans):
             end_written = hi
 
 
-def _check_disjoint(tensors):
-    """_check_spans of tuples of tensors of which a step writes all but the second."""
-    spans = []
-    for t in tensors:
-        for i, x in enumerate(t):
-            n = x.numel() * x.element_size()
-            if n:
-                spans.append((x.data_ptr(), x.data_ptr() + n, i != 1))
-    _check_spans(spans)
-
-
-def qopt_adamw8bit_plan(tensors):
-    """Plan of an 8-bit AdamW step over a list of (param, grad, m_codes, v_codes, m_absmax,
-    v_absmax) tuples, checked as for qopt_adam8bit_step; none may overlap another."""
+def _adamw_plan(tensors, bits):
+    """Checks the tuples of an AdamW step and makes its launch descriptors."""
     tensors = [tuple(t) for t in tensors]
-    arr, pdt, gdt, dev = make_tensor_array(tensors)
-    _check_disjoint(tensors)
-    return AdamWPlan(8, tensors, arr, pdt, gdt, dev)
-
-
-def qopt_adamw32bit_plan(tensors):
-    """Plan of an AdamW step with 32-bit moments over a list of (param, grad, m, v) tuples
-    (fp32 or bf16 params and grads, fp32 moments); none may overlap another."""
-    tensors = [tuple(t) for t in tensors]
-    arr = (_lib.qopt_tensor32 * len(tensors))()
-    dev = pair = None
+    coded = bits == 8
+    arr = ((_lib.qopt_tensor if coded else _lib.qopt_tensor32) * len(tensors))()
+    index = pair = None
     spans = []
-    for i, (p, g, m, v) in enumerate(tensors):
+    for i, t in enumerate(tensors):
+        if coded:
+            p, g, m, v, am, av = t
+        else:
+            p, g, m, v = t
         n = p.numel()
         if (p.dtype, g.dtype) != pair:
             if p.dtype not in _DTYPES or g.dtype not in _DTYPES:
@@ -293,23 +282,52 @@ def qopt_adamw32bit_plan(tensors):
                 raise TypeError("one call takes one (param dtype, grad dtype) pair")
             pair = p.dtype, g.dtype
             psize, gsize = p.element_size(), g.element_size()
-        if m.dtype != torch.float32 or v.dtype != torch.float32:
-            raise TypeError("moments must be float32")
         if g.numel() != n or m.numel() != n or v.numel() != n:
             raise ValueError("param, grad and moments must have the same size")
-        d = _check_cuda(p, g, m, v)
-        if dev is None:
-            dev = d
-        elif d != dev:
+        at = p.get_device()
+        for x in t:
+            if x.get_device() != at or at < 0 or not x.is_contiguous():
+                _check_cuda(*t)
+        if index is None:
+            index = at
+        elif at != index:
             raise ValueError("all tensors of one call must be on the same GPU")
         pp, gp, mp, vp = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
-        arr[i] = (pp, gp, mp, vp, n)
-        if n:
-            spans += ((pp, pp + psize * n, True), (gp, gp + gsize * n, False), (mp, mp + 4 * n, True),
-                      (vp, vp + 4 * n, True))
+        if coded:
+            nb = nblocks(n)
+            if m.dtype != torch.uint8 or v.dtype != torch.uint8:
+                raise TypeError("codes must be uint8")
+            if am.dtype != torch.float32 or av.dtype != torch.float32:
+                raise TypeError("absmax must be float32")
+            if am.numel() != nb or av.numel() != nb:
+                raise ValueError("absmax must hold ceil(n / 2048) elements")
+            ap, bp = am.data_ptr(), av.data_ptr()
+            arr[i] = (pp, gp, mp, vp, ap, bp, n)
+            if n:
+                spans += ((pp, pp + psize * n, True), (gp, gp + gsize * n, False), (mp, mp + n, True),
+                          (vp, vp + n, True), (ap, ap + 4 * nb, True), (bp, bp + 4 * nb, True))
+        else:
+            if m.dtype != torch.float32 or v.dtype != torch.float32:
+                raise TypeError("moments must be float32")
+            arr[i] = (pp, gp, mp, vp, n)
+            if n:
+                spans += ((pp, pp + psize * n, True), (gp, gp + gsize * n, False),
+                          (mp, mp + 4 * n, True), (vp, vp + 4 * n, True))
     _check_spans(spans)
     pdt, gdt = (QOPT_F32, QOPT_F32) if pair is None else (_DTYPES[pair[0]], _DTYPES[pair[1]])
-    return AdamWPlan(32, tensors, arr, pdt, gdt, dev)
+    return AdamWPlan(bits, tensors, arr, pdt, gdt, None if index is None else tensors[0][0].device)
+
+
+def qopt_adamw8bit_plan(tensors):
+    """Plan of an 8-bit AdamW step over a list of (param, grad, m_codes, v_codes, m_absmax,
+    v_absmax) tuples, checked as for qopt_adam8bit_step; none may overlap another."""
+    return _adamw_plan(tensors, 8).keep()
+
+
+def qopt_adamw32bit_plan(tensors):
+    """Plan of an AdamW step with 32-bit moments over a list of (param, grad, m, v) tuples
+    (fp32 or bf16 params and grads, fp32 moments); none may overlap another."""
+    return _adamw_plan(tensors, 32).keep()
 
 
 def _adamw_args(plan, bits, lr, beta1, beta2, eps, weight_decay, step, grad_scale):
@@ -330,7 +348,7 @@ def qopt_adamw8bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, g
     v_absmax) tuples, or a plan of it, updated in place on torch's current stream.
     ``grad_scale``: a float32 GPU tensor of one value that every gradient is multiplied
     with, read when the step runs (a clipping factor, for instance)."""
-    plan = tensors if isinstance(tensors, AdamWPlan) else qopt_adamw8bit_plan(tensors)
+    plan = tensors if isinstance(tensors, AdamWPlan) else _adamw_plan(tensors, 8)
     hp, gs = _adamw_args(plan, 8, lr, beta1, beta2, eps, weight_decay, step, grad_scale)
     dev = plan.device
     if dev is None:
@@ -343,7 +361,7 @@ def qopt_adamw32bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, 
     """One AdamW step with 32-bit moments over a list of (param, grad, m, v) tuples, or a
     plan of it, updated in place on torch's current stream; ``grad_scale`` as for
     qopt_adamw8bit_step."""
-    plan = tensors if isinstance(tensors, AdamWPlan) else qopt_adamw32bit_plan(tensors)
+    plan = tensors if isinstance(tensors, AdamWPlan) else _adamw_plan(tensors, 32)
     hp, gs = _adamw_args(plan, 32, lr, beta1, beta2, eps, weight_decay, step, grad_scale)
     dev = plan.device
     if dev is None:

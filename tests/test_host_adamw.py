@@ -78,7 +78,10 @@ def test_null_and_misaligned_state():
 def test_overlap_check():
     import torch
     a, b, c, d = (torch.zeros(100) for _ in range(4))
-    check = functional._check_disjoint
+    def check(tensors):
+        functional._check_spans([(x.data_ptr(), x.data_ptr() + x.numel() * x.element_size(), i != 1)
+                                 for t in tensors for i, x in enumerate(t) if x.numel()])
+
     check([(a, b, c, d)])
     check([(a[:50], b, c[:50], d[:50]), (a[50:], b, c[50:], d[50:])])  # a gradient serves two
     check([(a[:0], a[:0], a[:0], a[:0]), (a, b, c, d)])
