@@ -336,7 +336,8 @@ def fp8_linear(x, w):
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError("x must be [..., k] and w [n, k]")
     _same_gpu(x, w)
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+    # a trace records the function as one operation, but of the calls below only their empty outputs
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or torch.jit.is_tracing():
         return Fp8LinearFunction.apply(x, w)
     wq = _quantize(w.detach().contiguous(), _DT[w.dtype], w.shape[1], True, True, False)[0]
     x = x.detach()

@@ -1,0 +1,62 @@
+"""CPU tests of the 8-bit linear layer's Python side: what reaches the library and what torch
+records of it.  The library's calls are replaced by a stand-in that fills the results."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+qopt = pytest.importorskip("block_wise_bit_adam8bit_amd")
+from block_wise_bit_adam8bit_amd import _lib, fp8  # noqa: E402
+
+VALUE = 7.0
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Names of the library's entry points as they are called; results are float32 VALUEs."""
+    names = []
+
+    def call(name, device, *args):
+        names.append(name)
+        if name == "qopt_fp8_matmul":
+            out, m, n = args[8], args[5], args[6]
+        elif name == "qopt_fp8_linear":
+            out, m, n = args[9], args[2], args[8]
+        else:
+            return
+        np.ctypeslib.as_array((ctypes.c_float * (m * n)).from_address(out))[:] = VALUE
+
+    monkeypatch.setattr(_lib, "call", call)
+    monkeypatch.setattr(fp8, "_same_gpu", lambda first, *others: first.device)
+    return names
+
+
+class Layer(torch.nn.Module):
+    def __init__(self, requires_grad):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.randn(24, 200), requires_grad=requires_grad)
+
+    def forward(self, x):
+        return qopt.fp8_linear(x, self.weight)
+
+
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("requires_grad", [False, True])
+@pytest.mark.parametrize("grad_mode", [False, True])
+def test_a_traced_layer_calls_the_library(calls, grad_mode, requires_grad, m):
+    """A trace holds the products themselves, whatever gradients were wanted while it was made."""
+    layer = Layer(requires_grad)
+    with torch.set_grad_enabled(grad_mode):
+        traced = torch.jit.trace(layer, (torch.randn(m, 200),))
+        del calls[:]
+        y = traced(torch.randn(m, 200))
+    assert calls and calls[-1] in ("qopt_fp8_linear", "qopt_fp8_matmul")
+    assert y.shape == (m, 24) and bool((y == VALUE).all())
+    # gradients are those of the mode it runs in, not of the one it was traced in
+    y = traced(torch.randn(m + 30, 200))
+    assert y.shape == (m + 30, 24)
+    assert y.requires_grad == requires_grad and bool((y == VALUE).all())
+    if requires_grad:
+        assert torch.autograd.grad(y.sum(), list(traced.parameters()))[0].shape == (24, 200)
