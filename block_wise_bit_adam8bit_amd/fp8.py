@@ -12,6 +12,7 @@ import ctypes
 from typing import NamedTuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib
@@ -325,10 +326,15 @@ class Fp8LinearFunction(torch.autograd.Function):
         return dx, dw
 
 
+def _has_tangent(t):
+    return forward_ad.unpack_dual(t).tangent is not None
+
+
 def fp8_linear(x, w):
     """x w^T with gradients: x [..., k] and w [n, k] in float32 or bfloat16.  The result and
     x's gradient have x's type, w's gradient has w's.  The weight is quantized anew in every
-    call; a server quantizes it once and calls ``qopt_fp8_linear``.  A forward and backward
+    call; a server quantizes it once and calls ``qopt_fp8_linear``.  Forward-mode derivatives
+    are refused (NotImplementedError).  A forward and backward
     pass may be captured into a graph as any of torch's: with no other result of the same
     leaves alive whose backward ran, or will run, outside of it."""
     _check_dtype(x.dtype, "x")
@@ -336,8 +342,10 @@ def fp8_linear(x, w):
     if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
         raise ValueError("x must be [..., k] and w [n, k]")
     _same_gpu(x, w)
-    # a trace records the function as one operation, but of the calls below only their empty outputs
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or torch.jit.is_tracing():
+    # a trace records the function as one operation, but of the calls below only their empty outputs;
+    # of a tangent the function says that it has no derivative, where they would drop it
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or torch.jit.is_tracing() \
+            or _has_tangent(x) or _has_tangent(w):
         return Fp8LinearFunction.apply(x, w)
     wq = _quantize(w.detach().contiguous(), _DT[w.dtype], w.shape[1], True, True, False)[0]
     x = x.detach()

@@ -60,3 +60,21 @@ def test_a_traced_layer_calls_the_library(calls, grad_mode, requires_grad, m):
     assert y.requires_grad == requires_grad and bool((y == VALUE).all())
     if requires_grad:
         assert torch.autograd.grad(y.sum(), list(traced.parameters()))[0].shape == (24, 200)
+
+
+@pytest.mark.parametrize("requires_grad", [False, True])
+@pytest.mark.parametrize("grad_mode", [False, True])
+@pytest.mark.parametrize("which", ["x", "w"])
+def test_forward_mode_is_refused(calls, which, grad_mode, requires_grad):
+    """A tangent is not dropped, whether or not gradients are wanted beside it."""
+    x, w = torch.randn(5, 200), torch.randn(24, 200)
+    with torch.autograd.forward_ad.dual_level(), torch.set_grad_enabled(grad_mode):
+        t = x if which == "x" else w
+        dual = torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))
+        x, w = (dual, w.requires_grad_(requires_grad)) if which == "x" else (x.requires_grad_(requires_grad), dual)
+        with pytest.raises(NotImplementedError):
+            qopt.fp8_linear(x, w)
+        # without a tangent the level itself is no reason to refuse
+        assert bool((qopt.fp8_linear(torch.randn(5, 200), torch.randn(24, 200)) == VALUE).all())
+    with pytest.raises(RuntimeError):  # functorch's duals hide in wrappers
+        torch.func.jvp(lambda a: qopt.fp8_linear(a, torch.randn(24, 200)), (torch.randn(5, 200),), (torch.ones(5, 200),))
