@@ -157,10 +157,19 @@ def _linear(x, dx, m, k, ldx, w, form, out, do, ldo):
     return out
 
 
+# Each of these is one call of the library, without derivatives: torch records nothing of it.  In a
+# trace only the empty results would remain, so a trace is refused.
+
+def _not_traced():
+    if torch.jit.is_tracing():
+        raise RuntimeError("a library call cannot be traced; fp8_linear can")
+
+
 def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
     """Quantize a 2-D float32 or bfloat16 tensor in blocks of 128 along its rows, or in
     tiles of 128 x 128 (``tiles``).  Returns the Fp8Matrix of x (``normal``), of its transpose
     (``transposed``), or the pair of both."""
+    _not_traced()
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     if not normal and not transposed:
@@ -203,6 +212,7 @@ def _output(out, shape, dtype, dev, *operands):
 def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, *, out=None):
     """a b^T of two quantized matrices [m, k] (scales by rows) and [n, k] (by rows or tiles):
     [m, n] in ``out_dtype`` (bfloat16 or float32), into ``out`` if given."""
+    _not_traced()
     fa, fb = _quantized(a_codes, a_scales, "a"), _quantized(b_codes, b_scales, "b")
     dt = _check_dtype(out_dtype, "out_dtype")
     if fa != QOPT_FP8_ROWS:
@@ -217,8 +227,9 @@ def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat
 
 def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
     """x w^T for x [..., k] in float32 or bfloat16, quantized on the way, and a quantized
-    weight [n, k]: [..., n] in ``out_dtype`` (default: x's).  One launch for up to
-    QOPT_FP8_FEW_ROWS rows of x."""
+    weight [n, k]: [..., n] in ``out_dtype`` (default: x's), without derivatives.  One launch for
+    up to QOPT_FP8_FEW_ROWS rows of x."""
+    _not_traced()
     form = _quantized(w_codes, w_scales, "w")
     dx = _check_dtype(x.dtype, "x")
     out_dtype = x.dtype if out_dtype is None else out_dtype

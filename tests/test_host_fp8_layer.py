@@ -78,3 +78,16 @@ def test_forward_mode_is_refused(calls, which, grad_mode, requires_grad):
         assert bool((qopt.fp8_linear(torch.randn(5, 200), torch.randn(24, 200)) == VALUE).all())
     with pytest.raises(RuntimeError):  # functorch's duals hide in wrappers
         torch.func.jvp(lambda a: qopt.fp8_linear(a, torch.randn(24, 200)), (torch.randn(5, 200),), (torch.ones(5, 200),))
+
+
+def test_the_library_calls_themselves_are_not_traced(calls):
+    """Their results would be empty tensors in a trace: refused, instead of wrong."""
+    x, codes = torch.randn(5, 256), torch.zeros(24, 256, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    tiles, rows = torch.zeros(1, 2, dtype=torch.uint8), torch.zeros(2, 32, dtype=torch.uint8)
+    for f in (lambda a: qopt.qopt_fp8_linear(a, codes, tiles),
+              lambda a: qopt.qopt_fp8_matmul(codes, rows, codes, tiles, torch.float32) + a.sum(),
+              lambda a: qopt.qopt_fp8_quantize(a)[0]):
+        f(x)
+        with pytest.raises(RuntimeError, match="trace"):
+            torch.jit.trace(f, (x,))
+    assert len(calls) == 3
