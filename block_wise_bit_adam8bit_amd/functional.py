@@ -42,7 +42,7 @@ def codebook_bytes(kind):
 def codebook(kind, device=None):
     """Device copy of the codebook of ``kind`` on ``device`` (built and uploaded once
     per process and device; 16-byte aligned)."""
-    if isinstance(device, torch.device):
+    if isinstance(device, torch.device) and device.type == "cuda":
         t = _cb_cache.get((kind, device.index))
         if t is not None:
             return t
