@@ -368,14 +368,15 @@ def fp8_linear(x, w):
 class Fp8Linear(torch.nn.Module):
     """Linear layer without bias whose products, forward and backward, run in 8-bit
     floating point (``fp8_linear``).  The weight itself stays in ``dtype`` (float32 or
-    bfloat16), Xavier-uniform from ``seed`` as the Stable Embedding's table."""
+    bfloat16), Xavier-uniform from ``seed`` as the Stable Embedding's table; without one the seed
+    is drawn from torch's generator, so that layers of one shape start apart."""
 
-    def __init__(self, in_features, out_features, *, device=None, dtype=torch.float32, seed=0):
+    def __init__(self, in_features, out_features, *, device=None, dtype=torch.float32, seed=None):
         super().__init__()
         device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
         self.in_features, self.out_features = int(in_features), int(out_features)
-        self.seed = int(seed)
+        self.seed = int(torch.randint(1 << 62, (), device="cpu")) if seed is None else int(seed)
         self.weight = torch.nn.Parameter(
             torch.empty(self.out_features, self.in_features, dtype=dtype, device=device))
         self.reset_parameters()

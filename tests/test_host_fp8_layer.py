@@ -91,3 +91,21 @@ def test_the_library_calls_themselves_are_not_traced(calls):
         with pytest.raises(RuntimeError, match="trace"):
             torch.jit.trace(f, (x,))
     assert len(calls) == 3
+
+
+def test_layers_start_apart(monkeypatch):
+    """Two layers of one shape do not start with the same weights unless they are told to, and
+    torch's seed settles which ones they get."""
+    seeds = []
+    monkeypatch.setattr(fp8, "qopt_embedding_xavier_init", lambda weight, seed: seeds.append(seed))
+
+    def make(**options):
+        return qopt.Fp8Linear(16, 16, device="cpu", **options).seed
+
+    torch.manual_seed(5)
+    drawn = [make(), make()]
+    assert drawn[0] != drawn[1]
+    torch.manual_seed(5)
+    assert [make(), make()] == drawn
+    assert [make(seed=3), make(seed=3), make(seed=0)] == [3, 3, 0]
+    assert seeds == [*drawn, *drawn, 3, 3, 0]
