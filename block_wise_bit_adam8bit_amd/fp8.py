@@ -9,6 +9,7 @@ outputs and workspaces and supplies the current stream.
 """
 
 import ctypes
+import math
 from typing import NamedTuple
 
 import torch
@@ -262,7 +263,8 @@ class Fp8LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w):
         need_x, need_w = ctx.needs_input_grad
-        (n, k), m = w.shape, x.shape[:-1].numel()
+        lead, (n, k) = [int(d) for d in x.shape[:-1]], (int(d) for d in w.shape)  # tensors, in a trace
+        m = math.prod(lead)
         x2, w = x.reshape(m, k).contiguous(), w.contiguous()
         dev, dx, kp = x.device, _DT[x.dtype], _blocks(k) * QOPT_FP8_BLOCK
         w_codes, w_all = _sizes(n, k, True)
@@ -275,7 +277,7 @@ class Fp8LinearFunction(torch.autograd.Function):
             ws = _room(LIB.qopt_fp8_linear_workspace, "qopt_fp8_linear_workspace", m, n, k, dx)
         kept = torch.empty(wt_all + xt_all, dtype=torch.uint8, device=dev)
         temp = torch.empty(w_all + x_all + ws, dtype=torch.uint8, device=dev)
-        y = torch.empty(*x.shape[:-1], n, dtype=x.dtype, device=dev)
+        y = torch.empty(*lead, n, dtype=x.dtype, device=dev)
         wq, wt = temp.data_ptr(), kept.data_ptr()
         xq, xt = wq + w_all, wt + wt_all
         work = xq + x_all if ws else None
@@ -291,7 +293,7 @@ class Fp8LinearFunction(torch.autograd.Function):
                           xq, xq + x_codes, xt, xt + xt_codes)
             _lib.call("qopt_fp8_matmul", dev, xq, xq + x_codes, wq, wq + w_codes, QOPT_FP8_TILES, m, n,
                       kp, y.data_ptr(), dx, n, work, ws)
-        ctx.x_shape, ctx.dtypes = x.shape, (x.dtype, w.dtype)
+        ctx.x_shape, ctx.dtypes = torch.Size((*lead, k)), (x.dtype, w.dtype)
         ctx.save_for_backward(kept)
         return y
 
@@ -301,6 +303,7 @@ class Fp8LinearFunction(torch.autograd.Function):
         need_x, need_w = ctx.needs_input_grad
         if not need_x and not need_w:
             return None, None
+        _not_traced()
         (kept,) = ctx.saved_tensors
         m, n, k = ctx.x_shape[:-1].numel(), dy.shape[-1], ctx.x_shape[-1]
         dy = dy.reshape(m, n).contiguous()

@@ -15,11 +15,14 @@ VALUE = 7.0
 
 @pytest.fixture
 def calls(monkeypatch):
-    """Names of the library's entry points as they are called; results are float32 VALUEs."""
+    """Names of the library's entry points as they are called; results are float32 VALUEs.
+    Arguments have to be such as ctypes takes for the entry point."""
     names = []
 
     def call(name, device, *args):
         names.append(name)
+        for kind, arg in zip(_lib._SIGNATURES[name][1], (*args, None), strict=True):
+            kind.from_param(arg) if kind is ctypes.c_void_p else kind(arg)
         if name == "qopt_fp8_matmul":
             out, m, n = args[8], args[5], args[6]
         elif name == "qopt_fp8_linear":
@@ -60,6 +63,16 @@ def test_a_traced_layer_calls_the_library(calls, grad_mode, requires_grad, m):
     assert y.requires_grad == requires_grad and bool((y == VALUE).all())
     if requires_grad:
         assert torch.autograd.grad(y.sum(), list(traced.parameters()))[0].shape == (24, 200)
+
+
+def test_a_backward_pass_is_not_traced(calls):
+    """Its gradients would be empty tensors in a trace: refused, instead of wrong."""
+    w = torch.randn(24, 200)
+    f = lambda a: torch.autograd.grad(qopt.fp8_linear(a, w).sum(), a)[0]  # noqa: E731
+    x = torch.randn(5, 200, requires_grad=True)
+    f(x)
+    with pytest.raises(RuntimeError, match="trace"):
+        torch.jit.trace(f, (x,))
 
 
 @pytest.mark.parametrize("requires_grad", [False, True])
