@@ -189,6 +189,17 @@ def _span(t):
     return at, at + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
+def _side_by_side(a, b):
+    """Whether two 2-D tensors lie in different columns of rows that are equally far apart."""
+    if a.dim() != 2 or b.dim() != 2 or any(t.shape[1] > 1 and t.stride(1) != 1 for t in (a, b)):
+        return False
+    pitch, of_b = (t.stride(0) * t.element_size() for t in (a, b))
+    if pitch != of_b or not pitch:
+        return False
+    off = (b.data_ptr() - a.data_ptr()) % pitch  # from a row of a to the next one of b
+    return a.shape[1] * a.element_size() <= off and off + b.shape[1] * b.element_size() <= pitch
+
+
 def _output(out, shape, dtype, dev, *operands):
     """The output tensor and the distance of its rows."""
     if out is None:
@@ -201,7 +212,7 @@ def _output(out, shape, dtype, dev, *operands):
     lo, hi = _span(out)
     for t in operands:
         first, end = _span(t)
-        if first < hi and lo < end:
+        if first < hi and lo < end and not _side_by_side(out, t):
             raise ValueError("out must not overlap an operand")
     if out.dim() == 2:
         return out, _row_stride(out, "out")

@@ -24,12 +24,13 @@ def calls(monkeypatch):
         for kind, arg in zip(_lib._SIGNATURES[name][1], (*args, None), strict=True):
             kind.from_param(arg) if kind is ctypes.c_void_p else kind(arg)
         if name == "qopt_fp8_matmul":
-            out, m, n = args[8], args[5], args[6]
+            out, m, n, ldo = args[8], args[5], args[6], args[10]
         elif name == "qopt_fp8_linear":
-            out, m, n = args[9], args[2], args[8]
+            out, m, n, ldo = args[9], args[2], args[8], args[11]
         else:
             return
-        np.ctypeslib.as_array((ctypes.c_float * (m * n)).from_address(out))[:] = VALUE
+        for row in range(m):
+            np.ctypeslib.as_array((ctypes.c_float * n).from_address(out + 4 * row * ldo))[:] = VALUE
 
     monkeypatch.setattr(_lib, "call", call)
     monkeypatch.setattr(fp8, "_same_gpu", lambda first, *others: first.device)
@@ -122,3 +123,33 @@ def test_layers_start_apart(monkeypatch):
     assert [make(), make()] == drawn
     assert [make(seed=3), make(seed=3), make(seed=0)] == [3, 3, 0]
     assert seeds == [*drawn, *drawn, 3, 3, 0]
+
+
+def test_out_between_the_rows_of_an_operand(calls):
+    """Rows of one buffer side by side do not overlap, whatever their types; rows that share a byte do."""
+    codes, tiles = torch.zeros(8, 256, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.zeros(1, 2, dtype=torch.uint8)
+    run = lambda x, out: qopt.qopt_fp8_linear(x, codes, tiles, torch.float32, out=out)  # noqa: E731
+    for m in (1, 2, 40):
+        room = torch.zeros(m, 300)
+        for x, out in ((room[:, 8:264], room[:, :8]), (room[:, :256], room[:, 256:264]),
+                       (room[:, 30:286], room[:, 22:30]), (room[:, 30:286], room[:, 286:294])):
+            run(x, out)
+            assert bool((out == VALUE).all()) and bool((x == 0).all())
+            room.zero_()
+        half = room.view(torch.bfloat16)  # rows of 600
+        run(half[:, 17:273], room[:, :8])
+        run(half[:, 16:272], room[:, 136:144])
+        bad = [(room[:, 7:263], room[:, :8]), (room[:, :256], room[:, 255:263]),
+               (room[:, 30:286], room[:, 30:38]), (room[:, 30:286], room[:, 278:286]),
+               (half[:, 15:271], room[:, :8]), (half[:, 17:273], room[:, 136:144])]
+        if m > 1:  # the next row: columns that run over a row's end, and another distance of the rows
+            flat = torch.zeros(m * 300 + 300)
+            bad += [(flat.as_strided((m, 256), (300, 1), 100), flat.as_strided((m, 8), (300, 1), 350)),
+                    (flat.as_strided((m, 256), (300, 1), 0), flat.as_strided((m, 8), (298, 1), 260))]
+        for x, out in bad:
+            with pytest.raises(ValueError, match="overlap"):
+                run(x, out)
+    # an operand that is not rows of a matrix: its whole span counts
+    room = torch.zeros(4, 3, 256)
+    with pytest.raises(ValueError, match="overlap"):
+        run(room, room.view(-1)[:96].view(4, 3, 8))
