@@ -330,14 +330,17 @@ def qopt_adamw32bit_plan(tensors):
     return _adamw_plan(tensors, 32).keep()
 
 
+def _check_grad_scale(grad_scale):
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
+        raise ValueError("grad_scale must be one float32 value")
+
+
 def _adamw_args(plan, bits, lr, beta1, beta2, eps, weight_decay, step, grad_scale):
     if plan.bits != bits:
         raise ValueError(f"the plan is one of a step with {plan.bits}-bit moments")
-    if grad_scale is not None:
-        if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
-            raise ValueError("grad_scale must be one float32 value")
-        if plan.device is not None and grad_scale.device != plan.device:
-            raise ValueError("grad_scale must be on the tensors' GPU")
+    _check_grad_scale(grad_scale)
+    if grad_scale is not None and plan.device is not None and grad_scale.device != plan.device:
+        raise ValueError("grad_scale must be on the tensors' GPU")
     hp = _lib.qopt_adamw_hparams(float(lr), float(beta1), float(beta2), float(eps),
                                  float(weight_decay), int(step))
     return ctypes.byref(hp), None if grad_scale is None else grad_scale.data_ptr()

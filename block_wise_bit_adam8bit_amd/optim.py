@@ -26,7 +26,8 @@ from collections import defaultdict
 import torch
 
 from .checkpoint import compress_moments_multi, decompress_moments_multi
-from .functional import make_tensor_array, nblocks, qopt_adam8bit_step, qopt_adamw8bit_step, qopt_adamw32bit_step
+from .functional import (_check_grad_scale, make_tensor_array, nblocks, qopt_adam8bit_step,
+                         qopt_adamw8bit_step, qopt_adamw32bit_step)
 
 _STATE_KEYS = ("m_codes", "v_codes", "m_absmax", "v_absmax")
 _CODE_ALIGN = 256  # bytes between the starts of consecutive parameters' codes
@@ -296,6 +297,7 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        _check_grad_scale(grad_scale)
         for group in self.param_groups:  # checked before any state changes
             for p in group["params"]:
                 if p.grad is None:

@@ -98,3 +98,14 @@ def test_optimizer_refuses_cpu_parameters():
     with pytest.raises(ValueError):
         opt.step()
     assert not any(opt.state.values())
+
+
+def test_optimizer_looks_at_grad_scale_first():
+    """Before any parameter, and so before any state exists: its type and its size."""
+    p = torch.nn.Parameter(torch.ones(8192))
+    p.grad = torch.ones(8192)
+    opt = qopt.AdamW([p])
+    for bad in (torch.ones(2), torch.ones(0), torch.ones(1, dtype=torch.float64), torch.ones(1, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError, match="grad_scale must be one float32"):
+            opt.step(grad_scale=bad)
+    assert not any(opt.state.values())
