@@ -335,15 +335,25 @@ def _check_grad_scale(grad_scale):
         raise ValueError("grad_scale must be one float32 value")
 
 
+def _settings(lr, beta1, beta2, eps, weight_decay, step):
+    return ctypes.byref(_lib.qopt_adamw_hparams(float(lr), float(beta1), float(beta2), float(eps),
+                                                float(weight_decay), int(step)))
+
+
+def _check_settings(**settings):
+    """Refuse hyper-parameters as the library does: it checks them also for a step of no tensors."""
+    _lib.check("qopt_adamw32bit_step",
+               LIB.qopt_adamw32bit_step(None, 0, QOPT_F32, QOPT_F32, _settings(**settings), None, None))
+
+
 def _adamw_args(plan, bits, lr, beta1, beta2, eps, weight_decay, step, grad_scale):
     if plan.bits != bits:
         raise ValueError(f"the plan is one of a step with {plan.bits}-bit moments")
     _check_grad_scale(grad_scale)
     if grad_scale is not None and plan.device is not None and grad_scale.device != plan.device:
         raise ValueError("grad_scale must be on the tensors' GPU")
-    hp = _lib.qopt_adamw_hparams(float(lr), float(beta1), float(beta2), float(eps),
-                                 float(weight_decay), int(step))
-    return ctypes.byref(hp), None if grad_scale is None else grad_scale.data_ptr()
+    return (_settings(lr, beta1, beta2, eps, weight_decay, step),
+            None if grad_scale is None else grad_scale.data_ptr())
 
 
 def qopt_adamw8bit_step(tensors, *, lr, beta1, beta2, eps, weight_decay, step, grad_scale=None):

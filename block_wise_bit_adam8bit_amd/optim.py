@@ -26,8 +26,8 @@ from collections import defaultdict
 import torch
 
 from .checkpoint import compress_moments_multi, decompress_moments_multi
-from .functional import (_check_grad_scale, make_tensor_array, nblocks, qopt_adam8bit_step,
-                         qopt_adamw8bit_step, qopt_adamw32bit_step)
+from .functional import (_adamw_plan, _check_grad_scale, _check_settings, make_tensor_array,
+                         nblocks, qopt_adam8bit_step, qopt_adamw8bit_step, qopt_adamw32bit_step)
 
 _STATE_KEYS = ("m_codes", "v_codes", "m_absmax", "v_absmax")
 _CODE_ALIGN = 256  # bytes between the starts of consecutive parameters' codes
@@ -312,23 +312,33 @@ class AdamW(torch.optim.Optimizer):
                     raise TypeError("AdamW needs float32 or bfloat16 parameters and gradients")
                 if grad_scale is not None and grad_scale.device != p.device:
                     raise ValueError("grad_scale must be on the parameters' GPU")
-        for group in self.param_groups:
-            live = [p for p in group["params"] if p.grad is not None]
-            self._init_states(group, [p for p in live if not self.state[p]])
-            batches = {}
-            for p in live:
-                st = self.state[p]
-                keys = _STATE_KEYS if "m_codes" in st else _MOMENT_KEYS
-                key = (p.device, p.dtype, p.grad.dtype, len(keys), st["step"] + 1)
-                batches.setdefault(key, []).append((p, p.grad, *(st[k] for k in keys)))
-            b1, b2 = group["betas"]
-            for key, items in batches.items():
-                coded = key[3] == len(_STATE_KEYS)
-                run = qopt_adamw8bit_step if coded else qopt_adamw32bit_step
-                run(items, lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
-                    weight_decay=group["weight_decay"], step=key[4], grad_scale=grad_scale)
-                for t in items:
-                    self.state[t[0]]["step"] = key[4]
+        jobs, fresh = [], []
+        try:  # every group's lists and settings, before the first of them moves
+            for group in self.param_groups:
+                live = [p for p in group["params"] if p.grad is not None]
+                new = [p for p in live if not self.state[p]]
+                fresh += new
+                self._init_states(group, new)
+                batches = {}
+                for p in live:
+                    st = self.state[p]
+                    bits, keys = (8, _STATE_KEYS) if "m_codes" in st else (32, _MOMENT_KEYS)
+                    key = (p.device, p.dtype, p.grad.dtype, bits, st["step"] + 1)
+                    batches.setdefault(key, []).append((p, p.grad, *(st[k] for k in keys)))
+                for (*_, bits, step), items in batches.items():
+                    b1, b2 = group["betas"]
+                    settings = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
+                                    weight_decay=group["weight_decay"], step=step)
+                    _check_settings(**settings)
+                    jobs.append((bits, _adamw_plan(items, bits), settings))
+        except Exception:
+            for p in fresh:
+                self.state.pop(p, None)
+            raise
+        for bits, plan, settings in jobs:
+            (qopt_adamw8bit_step if bits == 8 else qopt_adamw32bit_step)(plan, grad_scale=grad_scale, **settings)
+            for t in plan.tensors:
+                self.state[t[0]]["step"] = settings["step"]
         return loss
 
     _params_by_saved_id = Adam8bit._params_by_saved_id
