@@ -542,3 +542,99 @@ def test_a_plan_steps_the_memory_it_was_made_of(q, nbits):
     other = [torch.full((n,), 5.0, device="cuda") for _ in range(20)]  # would take freed memory
     own_step(q, nbits)(plan, step=2, **HP)
     assert all(bool((o == 5).all()) for o in other) and bool((p == 3).all())
+
+
+# ------------------------------------------------------------------ above the few blocks' and small steps' limits
+
+# More blocks than the workgroup-per-block kernel takes (4096), and enough for a wave's whole runs.
+MANY_BLOCKS = 20000
+
+
+def equal_but_for_nans(a, b):
+    if not a.is_floating_point():
+        return torch.equal(a, b)
+    nan = torch.isnan(a)
+    bit = torch.int32 if a.dtype == torch.float32 else torch.int16
+    return torch.equal(nan, torch.isnan(b)) and torch.equal(a.view(bit)[~nan], b.view(bit)[~nan])
+
+
+@pytest.mark.parametrize("pdt,gdt", PAIRS)
+@pytest.mark.parametrize("hp", [dict(HP, beta1=0.0, beta2=0.0, weight_decay=0.0),
+                                dict(HP, lr=5e-2, beta1=0.5, beta2=0.75, eps=1e-6, weight_decay=1.5),
+                                dict(HP, eps=0.0, beta2=0.9999), dict(HP, eps=1e-20),
+                                dict(HP, eps=1e-40), dict(HP, lr=4e6), dict(HP, lr=0.0)])
+def test_hyperparameters_of_many_blocks(q, pdt, gdt, hp):
+    """The wave-per-block kernel with step sizes and epsilons that switch the bf16 short path off or make
+    it look for subnormal second moments, scaled gradients and decay, from nonzero moments: sampled
+    blocks against the oracle, every element against the other kernel, which steps of few blocks take."""
+    say(f"{pdt}/{gdt} {hp}")
+    n = MANY_BLOCKS * BLOCK + 333
+    nb = MANY_BLOCKS + 1
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    normal = lambda k, s: torch.randn(k, device="cuda", generator=gen) * s  # noqa: E731
+    types = {"f32": torch.float32, "bf16": torch.bfloat16}
+    p = normal(n, 0.02).to(types[pdt])
+    codes = [torch.randint(0, 256, (n,), dtype=torch.uint8, device="cuda", generator=gen) for _ in range(2)]
+    maxima = [normal(nb, s).abs() for s in (1e-3, 1e-6)]
+    maxima[1][::7] = 0  # second moments that come from this step's gradients alone
+    one = [p, None, *codes, *maxima]
+    # the same by pieces of at most 2000 blocks, which the other kernel takes
+    other = [None if t is None else t.clone() for t in one]
+    sample = np.unique(np.concatenate([np.arange(9), np.random.default_rng(2).integers(0, MANY_BLOCKS, 60),
+                                       MANY_BLOCKS - 1 - np.arange(4)]))
+    at = torch.from_numpy((sample[:, None] * BLOCK + np.arange(BLOCK)).ravel()).cuda()
+    blocks = torch.from_numpy(sample).cuda()
+    tail = slice(MANY_BLOCKS * BLOCK, n)
+    scale = torch.full((1,), 0.37, device="cuda")
+    for step in (1, 2):
+        g = normal(n, 1e-3)
+        if hp["eps"]:  # down to gradients whose squares underflow (0 / 0 without an epsilon)
+            g[: n // 3] *= 10.0 ** (torch.rand(n // 3, device="cuda", generator=gen) * -25)
+        one[1] = g = g.to(types[gdt])
+        parts = []
+        for whole, b in ((True, blocks), (False, torch.tensor([MANY_BLOCKS], device="cuda"))):
+            i = at if whole else torch.arange(tail.start, tail.stop, device="cuda")
+            host = [to_host(t[i].contiguous()) for t in one[:4]] + [to_host(t[b]) for t in one[4:]]
+            with np.errstate(all="ignore"):
+                parts.append((i, b, oracle.adamw8bit_step(*host, step=step, grad_scale=0.37, param_dtype=pdt,
+                                                          grad_dtype=gdt, **hp)))
+        q.qopt_adamw8bit_step([tuple(one)], step=step, grad_scale=scale, **hp)
+        for lo in range(0, nb, 2000):
+            e, k = slice(lo * BLOCK, min(n, (lo + 2000) * BLOCK)), slice(lo, min(nb, lo + 2000))
+            q.qopt_adamw8bit_step([(other[0][e], g[e], other[2][e], other[3][e], other[4][k], other[5][k])],
+                                  step=step, grad_scale=scale, **hp)
+        torch.cuda.synchronize()
+        for i, b, want in parts:
+            for k, (t, w) in enumerate(zip((one[0], *one[2:]), want)):
+                got = t[b] if k > 2 else t[i]
+                w = to_dev(w, "bf16") if w.dtype == np.uint16 else to_dev(w)
+                assert equal_but_for_nans(got, w), f"oracle, step {step}, output {k}"
+        for k in (0, 2, 3, 4, 5):
+            assert equal_but_for_nans(one[k], other[k]), f"other kernel, step {step}, tensor {k}"
+
+
+@pytest.mark.parametrize("scale", [None, 0.37])
+@pytest.mark.parametrize("pdt,gdt", PAIRS)
+def test_large_32bit_steps(q, pdt, gdt, scale):
+    """Above 5 * 2^20 elements another instance of the kernel runs: tensors of odd lengths beside a large
+    one, more of them than a launch holds, moments that are not zero."""
+    say(f"{pdt}/{gdt} scale {scale}")
+    sizes = [5 * 2 ** 20 + 5, 1025, 1, 0, 70003, *range(1000, 1100)]
+    run_parity(q, 32, sizes, pdt, gdt, 3, 17, scale=scale)
+
+
+@pytest.mark.parametrize("pdt,gdt", PAIRS)
+def test_large_32bit_steps_at_odd_offsets(q, pdt, gdt):
+    """... and one element into their buffers, where wide accesses would be misaligned."""
+    guards = []
+
+    def place(a, dtype):
+        t = to_dev(a, dtype)
+        buf = torch.full((t.numel() + 2,), 77, dtype=t.dtype, device="cuda")
+        buf[1:-1] = t
+        guards.append(buf)
+        return buf[1:-1]
+
+    run_parity(q, 32, [5 * 2 ** 20 + 1025, 1024, 3], pdt, gdt, 2, 18, scale=0.37, place=place)
+    for b in guards:
+        assert float(b[0]) == 77 and float(b[-1]) == 77
