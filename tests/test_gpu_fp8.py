@@ -537,3 +537,105 @@ def test_training_step_in_8_bits(q):
 
     for a, b in zip(run(), run()):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ every instance of the kernels
+
+def blocks_of_integers(gen, rows, cols, tiles=False):
+    """Small integers, times 1, 2 or 4 from block to block of 128 (or tile): their sums of products
+    over up to 2^12 columns are exact in binary32, and scales that are taken from another block show."""
+    kb = -(-cols // 128)
+    x = torch.randint(-4, 5, (rows, kb * 128), device="cuda", generator=gen).float()
+    size = torch.randint(0, 3, (-(-rows // 128) if tiles else rows, kb), device="cuda", generator=gen)
+    if tiles:
+        size = size.repeat_interleave(128, 0)[:rows]
+    return (x.view(rows, kb, 128) * (2.0 ** size).unsqueeze(2)).view(rows, kb * 128)[:, :cols].contiguous()
+
+
+def values(matrix, rows):
+    """What a quantized matrix stands for, in binary64 on the GPU."""
+    v, kb = matrix.codes.double(), matrix.codes.shape[1] // 128
+    e = matrix.scales.double() - 127
+    e = e[:, :rows].t() if e.shape == (kb, -(-rows // 16) * 16) else e.repeat_interleave(128, 0)[:rows]
+    return (v.view(rows, kb, 128) * (2.0 ** e).unsqueeze(2)).view(rows, kb * 128)
+
+
+def within(got, a, b, dtype, exact_sums):
+    """The comparison of ``bound``, on the GPU."""
+    want, half = a @ b.t(), {F32: 2.0 ** -24, BF16: 2.0 ** -8}[dtype]
+    tol = half * want.abs() + (a.shape[1] + 2) * 2.0 ** -24 * (a.abs() @ b.abs().t())
+    if not exact_sums:
+        peak = lambda m: m.abs().view(m.shape[0], -1, 128).amax(2)  # noqa: E731
+        tol += 128 * 2.0 ** -17 * (peak(a) @ peak(b).t())
+    return bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n", [(4093, 4090), (4349, 16891)])
+def test_every_number_of_blocks_in_large_tiles(q, m, n, dtype, tiles):
+    """One to nine blocks along the sum in tiles of 256 x 256: one round of whole tiles, and four rounds
+    with the last one's tiles in halves; ragged on every side, into rows that lie apart."""
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    for kb in range(1, 10):
+        k = kb * 128 - (kb % 3)
+        say(f"{m}x{n}x{k} {dtype} tiles {tiles}")
+        x, w = blocks_of_integers(gen, m, k), blocks_of_integers(gen, n, k, tiles)
+        out = torch.full((m, n + 3), 77, dtype=dtype, device="cuda")
+        q.qopt_fp8_matmul(*q.qopt_fp8_quantize(x), *q.qopt_fp8_quantize(w, tiles=tiles), dtype, out=out[:, 1:n + 1])
+        assert torch.equal(out[:, 1:n + 1], (x.double() @ w.double().t()).to(dtype))
+        assert bool((out[:, 0] == 77).all()) and bool((out[:, n + 1:] == 77).all())
+
+
+def few_rows_runs(n, m, size):
+    """Runs of 16 weight rows that a workgroup takes for few rows of x: the library's rule, restated."""
+    cost = lambda r: -(-(-(-n // (16 * r))) // 256) * (16 * r + m * size)  # noqa: E731
+    return min(range(1, 5), key=cost)
+
+
+FEW_N, FEW_M = (300, 4113, 8209, 12289, 50257), (1, 16, 17, 32)
+
+
+def test_the_few_rows_cases_take_every_instance():
+    for dtype in (4, 2):
+        for ms in ((1, 16), (17, 32)):  # one and two fragments of 16 rows
+            assert {few_rows_runs(n, m, dtype) for n in FEW_N for m in ms} == {1, 2, 3, 4}
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", FEW_N)
+def test_few_rows_of_x(q, n, dtype, out_dtype, tiles):
+    """Every number of runs and fragments, with weight rows, rows of x and columns that end inside a
+    workgroup's; exact sums, and reals within the bounds."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    rng = np.random.default_rng(n)
+    for k in (130, 1156):
+        w = blocks_of_integers(gen, n, k, tiles)
+        wq = q.qopt_fp8_quantize(w, tiles=tiles)
+        r = q.qopt_fp8_quantize(reals(rng, n, k, F32), tiles=tiles)
+        rv = values(r, n)
+        for m in FEW_M:
+            say(f"{m} rows, {n}x{k} {dtype} -> {out_dtype} tiles {tiles}")
+            x = blocks_of_integers(gen, m, k).to(dtype)
+            out = torch.full((m, n + 3), 77, dtype=out_dtype, device="cuda")
+            q.qopt_fp8_linear(x, *wq, out_dtype, out=out[:, 1:n + 1])
+            assert torch.equal(out[:, 1:n + 1], (x.double() @ w.double().t()).to(out_dtype))
+            assert bool((out[:, 0] == 77).all()) and bool((out[:, n + 1:] == 77).all())
+            x = reals(rng, m, k, dtype)
+            got = q.qopt_fp8_linear(x, *r, out_dtype)
+            assert within(got, values(q.qopt_fp8_quantize(x), m), rv, out_dtype, out_dtype == F32)
+
+
+@pytest.mark.parametrize("grad_mode", [False, True])
+@pytest.mark.parametrize("m", [3, 80])
+def test_a_traced_layer(q, m, grad_mode):
+    layer = q.Fp8Linear(300, 70, dtype=BF16, seed=4)
+    x, other = (torch.randn(r, 300, device="cuda", dtype=BF16) for r in (m, m + 40))
+    with torch.set_grad_enabled(grad_mode):
+        traced = torch.jit.trace(layer, (x,))
+        for t in (x, other):
+            assert torch.equal(traced(t), layer(t))
+    got, want = (torch.autograd.grad(f(other).float().square().sum(), layer.weight)[0] for f in (traced, layer))
+    assert torch.equal(got, want)
