@@ -552,21 +552,34 @@ def blocks_of_integers(gen, rows, cols, tiles=False):
     return (x.view(rows, kb, 128) * (2.0 ** size).unsqueeze(2)).view(rows, kb * 128)[:, :cols].contiguous()
 
 
-def values(matrix, rows):
-    """What a quantized matrix stands for, in binary64 on the GPU."""
-    v, kb = matrix.codes.double(), matrix.codes.shape[1] // 128
-    e = matrix.scales.double() - 127
+def by_blocks(v, scales):
+    """[rows, columns] of codes' values times their scales, in binary64 on the GPU."""
+    rows, kb = v.shape[0], v.shape[1] // 128
+    e = scales.double() - 127
     e = e[:, :rows].t() if e.shape == (kb, -(-rows // 16) * 16) else e.repeat_interleave(128, 0)[:rows]
     return (v.view(rows, kb, 128) * (2.0 ** e).unsqueeze(2)).view(rows, kb * 128)
 
 
-def within(got, a, b, dtype, exact_sums):
-    """The comparison of ``bound``, on the GPU."""
-    want, half = a @ b.t(), {F32: 2.0 ** -24, BF16: 2.0 ** -8}[dtype]
-    tol = half * want.abs() + (a.shape[1] + 2) * 2.0 ** -24 * (a.abs() @ b.abs().t())
-    if not exact_sums:
-        peak = lambda m: m.abs().view(m.shape[0], -1, 128).amax(2)  # noqa: E731
-        tol += 128 * 2.0 ** -17 * (peak(a) @ peak(b).t())
+def values(matrix):
+    """What a quantized matrix stands for."""
+    return by_blocks(matrix.codes.double(), matrix.scales)
+
+
+def peaks(matrix):
+    """The largest magnitude of every 8 places of a row, codes under 2^-6 taken as 2^-6."""
+    v = by_blocks(matrix.codes.double().abs().clamp(min=2.0 ** -6), matrix.scales)
+    return v.view(v.shape[0], -1, 8).amax(2)
+
+
+def within(got, a, b, dtype):
+    """Whether a product of quantized matrices is right: one rounding, k + 2 roundings of the sum of
+    magnitudes in binary32, and for bf16, where the 8-bit instructions cut 7 of 8 products at 2^-13 of
+    the largest one's power of two, that of every 8 places."""
+    av, bv = values(a), values(b)
+    want, half = av @ bv.t(), {F32: 2.0 ** -24, BF16: 2.0 ** -8}[dtype]
+    tol = half * want.abs() + (av.shape[1] + 2) * 2.0 ** -24 * (av.abs() @ bv.abs().t())
+    if dtype == BF16:
+        tol += 7 * 2.0 ** -13 * (peaks(a) @ peaks(b).t())
     return bool(((got.double() - want).abs() <= tol).all())
 
 
@@ -615,7 +628,6 @@ def test_few_rows_of_x(q, n, dtype, out_dtype, tiles):
         w = blocks_of_integers(gen, n, k, tiles)
         wq = q.qopt_fp8_quantize(w, tiles=tiles)
         r = q.qopt_fp8_quantize(reals(rng, n, k, F32), tiles=tiles)
-        rv = values(r, n)
         for m in FEW_M:
             say(f"{m} rows, {n}x{k} {dtype} -> {out_dtype} tiles {tiles}")
             x = blocks_of_integers(gen, m, k).to(dtype)
@@ -625,7 +637,7 @@ def test_few_rows_of_x(q, n, dtype, out_dtype, tiles):
             assert bool((out[:, 0] == 77).all()) and bool((out[:, n + 1:] == 77).all())
             x = reals(rng, m, k, dtype)
             got = q.qopt_fp8_linear(x, *r, out_dtype)
-            assert within(got, values(q.qopt_fp8_quantize(x), m), rv, out_dtype, out_dtype == F32)
+            assert within(got, q.qopt_fp8_quantize(x), r, out_dtype)
 
 
 @pytest.mark.parametrize("grad_mode", [False, True])
@@ -639,3 +651,65 @@ def test_a_traced_layer(q, m, grad_mode):
             assert torch.equal(traced(t), layer(t))
     got, want = (torch.autograd.grad(f(other).float().square().sum(), layer.weight)[0] for f in (traced, layer))
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("k", [128, 384])
+def test_products_that_cancel(q, k, m):
+    """Two products of 2^16 that cancel beside k - 2 of 2^-j.  The 8-bit instructions cut what is small
+    next to the largest of 8 products, so bf16 results are bounded by the operands and not by the
+    result; binary32 results are exact while all sums, of at most 2^17 in steps of 2^-j, fit 24 bits."""
+    for j in range(10):
+        x = torch.full((m, k), 2.0 ** -j, device="cuda")
+        w = torch.ones(70, k, device="cuda")
+        x[:, :2], w[:, 0], w[:, 1] = 256, 256, -256
+        wq = q.qopt_fp8_quantize(w, tiles=True)
+        got = {dtype: q.qopt_fp8_linear(x, *wq, dtype) for dtype in (F32, BF16)}
+        xq = q.qopt_fp8_quantize(x)
+        want = values(xq) @ values(wq).t()
+        say(f"2^-{j}: {float(want[0, 0])} as bf16 {float(got[BF16][0, 0])}, as fp32 {float(got[F32][0, 0])}")
+        for dtype, y in got.items():
+            assert within(y, xq, wq, dtype)
+        if j <= 6:
+            assert torch.equal(got[F32].double(), want)
+
+
+@pytest.mark.parametrize("at", [0, 40, 64, 120])
+@pytest.mark.parametrize("least,most", [(0, 127), (0, 20), (100, 127)])
+def test_what_8_bit_products_lose(q, at, least, most):
+    """Eight places of codes of every size, of which two products cancel exactly, so that the other six
+    are all that is left: 200 x 3000 combinations within the bound."""
+    gen = torch.Generator(device="cuda").manual_seed(at + most)
+
+    def matrix(rows):
+        codes = torch.zeros(rows, 128, dtype=torch.uint8, device="cuda")
+        codes[:, at:at + 8] = torch.randint(least, most, (rows, 8), device="cuda", generator=gen) \
+            + 128 * torch.randint(0, 2, (rows, 8), device="cuda", generator=gen)
+        codes[:, at + 1] = codes[:, at]
+        return codes
+
+    a, b = matrix(200), matrix(3000)
+    b[:, at + 1] ^= 128
+    a, b = (q.Fp8Matrix(c.view(torch.float8_e4m3fn),
+                        torch.randint(120, 135, (1, -(-len(c) // 16) * 16), dtype=torch.uint8, device="cuda", generator=gen))
+            for c in (a, b))
+    for dtype in (BF16, F32):
+        assert within(q.qopt_fp8_matmul(*a, *b, dtype), a, b, dtype)
+
+
+@pytest.mark.parametrize("m", [3, 40])
+def test_the_largest_magnitudes(q, m):
+    """From 1.9375 * 2^127 on a value rounds to 2^128, which counts as infinity where the result is
+    binary32 and is multiplied as it is where it is bf16; one under that is ordinary in both."""
+    x = torch.ones(m, 256, device="cuda")
+    x[0], x[1] = 0, 0
+    x[0, 3], x[1, 200] = 3.39e38, 3.28e38  # 2^128 and 240 * 2^120
+    w = torch.full((70, 256), 2.0 ** -20, device="cuda")
+    w[5] = 0
+    wq = q.qopt_fp8_quantize(w, tiles=True)
+    want = values(q.qopt_fp8_quantize(x)) @ values(wq).t()
+    assert float(want[0, 0]) == 2.0 ** 108 and float(want[1, 0]) == 240 * 2.0 ** 100
+    assert torch.equal(q.qopt_fp8_linear(x, *wq, BF16).double(), want)
+    exact = q.qopt_fp8_linear(x, *wq, F32)
+    assert torch.equal(exact[1:].double(), want[1:])
+    assert not bool(torch.isfinite(exact[0]).any())
