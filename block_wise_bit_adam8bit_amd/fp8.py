@@ -23,6 +23,7 @@ from .embedding import qopt_embedding_xavier_init
 
 _DT = {torch.float32: QOPT_F32, torch.bfloat16: QOPT_BF16}
 CODE_DTYPE = torch.float8_e4m3fn
+_is_tracing = torch._C._is_tracing  # torch.jit.is_tracing takes twice as long
 
 
 class Fp8Matrix(NamedTuple):
@@ -162,7 +163,7 @@ def _linear(x, dx, m, k, ldx, w, form, out, do, ldo):
 # trace only the empty results would remain, so a trace is refused.
 
 def _not_traced():
-    if torch.jit.is_tracing():
+    if _is_tracing():
         raise RuntimeError("a library call cannot be traced; fp8_linear can")
 
 
@@ -369,7 +370,7 @@ def fp8_linear(x, w):
     _same_gpu(x, w)
     # a trace records the function as one operation, but of the calls below only their empty outputs;
     # of a tangent the function says that it has no derivative, where they would drop it
-    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or torch.jit.is_tracing() \
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or _is_tracing() \
             or _has_tangent(x) or _has_tangent(w):
         return Fp8LinearFunction.apply(x, w)
     wq = _quantize(w.detach().contiguous(), _DT[w.dtype], w.shape[1], True, True, False)[0]
