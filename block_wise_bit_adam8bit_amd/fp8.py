@@ -264,6 +264,14 @@ def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
     return _linear(x, dx, m, k, ldx, Fp8Matrix(w_codes, w_scales), form, out, do, ldo)
 
 
+def _check_linear(x, w):
+    _check_dtype(x.dtype, "x")
+    _check_dtype(w.dtype, "w")
+    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
+        raise ValueError("x must be [..., k] and w [n, k]")
+    _same_gpu(x, w)
+
+
 class Fp8LinearFunction(torch.autograd.Function):
     """y = x w^T with both gradients, every product over e4m3 codes: x and the upstream
     gradient in blocks of 128 along the axis of each sum, w in tiles of 128 x 128.
@@ -274,6 +282,7 @@ class Fp8LinearFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w):
+        _check_linear(x, w)
         need_x, need_w = ctx.needs_input_grad
         lead, (n, k) = [int(d) for d in x.shape[:-1]], (int(d) for d in w.shape)  # tensors, in a trace
         m = math.prod(lead)
@@ -364,16 +373,12 @@ def fp8_linear(x, w):
     are refused (NotImplementedError).  A forward and backward
     pass may be captured into a graph as any of torch's: with no other result of the same
     leaves alive whose backward ran, or will run, outside of it."""
-    _check_dtype(x.dtype, "x")
-    _check_dtype(w.dtype, "w")
-    if w.dim() != 2 or x.dim() < 1 or x.shape[-1] != w.shape[1]:
-        raise ValueError("x must be [..., k] and w [n, k]")
-    _same_gpu(x, w)
     # a trace records the function as one operation, but of the calls below only their empty outputs;
     # of a tangent the function says that it has no derivative, where they would drop it
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or _is_tracing() \
             or _has_tangent(x, w):
         return Fp8LinearFunction.apply(x, w)
+    _check_linear(x, w)
     wq = _quantize(w.detach().contiguous(), _DT[w.dtype], w.shape[1], True, True, False)[0]
     x = x.detach()
     if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) < x.shape[1]:

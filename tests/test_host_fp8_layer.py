@@ -153,3 +153,19 @@ def test_out_between_the_rows_of_an_operand(calls):
     room = torch.zeros(4, 3, 256)
     with pytest.raises(ValueError, match="overlap"):
         run(room, room.view(-1)[:96].view(4, 3, 8))
+
+
+def test_the_function_itself_checks_its_operands(monkeypatch):
+    """As fp8_linear does: a traced layer, too, may be given something else than it was traced with."""
+    apply, x, w = qopt.Fp8LinearFunction.apply, torch.randn(5, 200), torch.randn(24, 200)
+    with pytest.raises(ValueError, match="on a GPU"):  # before an address on the host goes to the device
+        apply(x, w)
+    with pytest.raises(ValueError, match="on a GPU"):
+        apply(x.requires_grad_(), w)
+    monkeypatch.setattr(fp8, "_same_gpu", lambda first, *others: first.device)
+    monkeypatch.setattr(_lib, "call", lambda *args: pytest.fail("reached the library"))
+    for error, a, b in ((TypeError, x.half(), w), (TypeError, x, w.double()), (ValueError, x, w[:, :199]),
+                        (ValueError, x, w.view(-1)), (ValueError, x.sum(), w), (ValueError, x.view(4, 250), w)):
+        for f in (apply, qopt.fp8_linear):
+            with pytest.raises(error):
+                f(a, b)
