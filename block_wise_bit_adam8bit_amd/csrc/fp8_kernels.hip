@@ -360,9 +360,11 @@ constexpr int few_waves(int frags, int runs) { return frags == 2 && runs == 4 ? 
 // quantizes the same 32 places of row r of x in registers (a block's maximum is a maximum over 4
 // lanes), so there is no launch before this one.
 // The weights' bytes bound it at the rate of memory; what a workgroup adds to that is reading x from
-// the L2 and quantizing it anew.  Measured (bf16, repeated in a graph, 2.3 us of it the launch): 1 row
-// of 4096 x 4096 5.8 us, 1 of 11008 x 4096 9.9 us (4.6 TB/s), 24 of it 15.1 us, 7 of 50257 x 2048 22.3 us
-// (4.6 TB/s).
+// the L2 and quantizing it anew.  Measured in a graph (bf16; 2.3 us of it the launch), one weight again and
+// again, which stays in the last-level cache, and 1 GiB of weights in turn: 1 row of 4096 x 4096 5.2 and
+// 6.5 us, 1 of 11008 x 4096 9.1 and 11.4 us (4.9 and 4.0 TB/s), 1 of 1024 x 8192, on 64 CUs, 7.4 and 9.0 us,
+// 24 of 11008 x 4096 15.0 and 16.3 us, 7 of 50257 x 2048 21.4 and 22.4 us (4.8 and 4.6 TB/s), 32 of it
+// 32.6 and 34.6 us.
 // Nothing around the loads branches (the compiler would wait for each before the next): weights past
 // the last row are read past the end of a buffer, as 0, and a lane without a row of x takes the last
 // one's values, which no result uses.  What k has beyond whole blocks comes after the loop.
@@ -938,9 +940,10 @@ template <typename XT, typename OT, int kRuns> int launch_few_runs(const FewArgs
 
 // More weight rows per workgroup let more of them share one reading of x, fewer fill the chip more
 // evenly.  The time goes by what a CU has to read, per column of k: its rounds of workgroups times
-// their rows of weights and of x.  Measured, in an earlier form of the kernel, for 24 rows of 11008 x
-// 4096, 1 to 4 runs of 16: 31.9, 23.4, 16.0 and 17.5 us; for 1 row of 4096 x 4096 6.7, 8.3, 9.9 and
-// 11.7 us; the rule takes the least of each.
+// their rows of weights and of x.  Measured with 1 to 4 runs of 16, 1 GiB of weights in turn (us): 1 row of
+// 4096 x 4096 6.4, 7.4, 9.1 and 10.7; 1 of 11008 x 4096 12.6, 14.1, 11.6 and 11.9; 24 of it 28.0, 24.7, 16.4 and
+// 20.4; 7 of 50257 x 2048 29.4, 23.5, 22.4 and 23.5; 32 of it 73.2, 51.6, 44.0 and 34.5; the rule takes the
+// least of each, and of the same calls with one weight again and again.
 template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t s) {
   int runs = 1;
   int64_t least = 0;
