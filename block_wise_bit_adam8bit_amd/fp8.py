@@ -224,7 +224,8 @@ def _output(out, shape, dtype, dev, *operands):
 
 def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat16, *, out=None):
     """a b^T of two quantized matrices [m, k] (scales by rows) and [n, k] (by rows or tiles):
-    [m, n] in ``out_dtype`` (bfloat16 or float32), into ``out`` if given."""
+    [m, n] in ``out_dtype`` (bfloat16 or float32), into ``out`` if given, which shares no byte
+    with an operand."""
     _not_traced()
     fa, fb = _quantized(a_codes, a_scales, "a"), _quantized(b_codes, b_scales, "b")
     dt = _check_dtype(out_dtype, "out_dtype")
@@ -241,7 +242,8 @@ def qopt_fp8_matmul(a_codes, a_scales, b_codes, b_scales, out_dtype=torch.bfloat
 def qopt_fp8_linear(x, w_codes, w_scales, out_dtype=None, *, out=None):
     """x w^T for x [..., k] in float32 or bfloat16, quantized on the way, and a quantized
     weight [n, k]: [..., n] in ``out_dtype`` (default: x's), without derivatives.  One launch for
-    up to QOPT_FP8_FEW_ROWS rows of x."""
+    up to QOPT_FP8_FEW_ROWS rows of x.  ``out`` shares no byte with an operand; it may be other
+    columns of the buffer that x's rows lie in."""
     _not_traced()
     form = _quantized(w_codes, w_scales, "w")
     dx = _check_dtype(x.dtype, "x")
@@ -369,10 +371,10 @@ def _has_tangent(*tensors):
 def fp8_linear(x, w):
     """x w^T with gradients: x [..., k] and w [n, k] in float32 or bfloat16.  The result and
     x's gradient have x's type, w's gradient has w's.  The weight is quantized anew in every
-    call; a server quantizes it once and calls ``qopt_fp8_linear``.  Forward-mode derivatives
-    are refused (NotImplementedError).  A forward and backward
-    pass may be captured into a graph as any of torch's: with no other result of the same
-    leaves alive whose backward ran, or will run, outside of it."""
+    call; a server quantizes it once and calls ``qopt_fp8_linear``.  A trace (torch.jit.trace)
+    holds it as one operation; forward-mode derivatives are refused (NotImplementedError).  A
+    forward and backward pass may be captured into a graph as any of torch's: with no other
+    result of the same leaves alive whose backward ran, or will run, outside of it."""
     # a trace records the function as one operation, but of the calls below only their empty outputs;
     # of a tangent the function says that it has no derivative, where they would drop it
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad) or _is_tracing() \
