@@ -342,8 +342,8 @@ def _settings(lr, beta1, beta2, eps, weight_decay, step):
 
 def _check_settings(**settings):
     """Refuse hyper-parameters as the library does: it checks them also for a step of no tensors."""
-    _lib.check("qopt_adamw32bit_step",
-               LIB.qopt_adamw32bit_step(None, 0, QOPT_F32, QOPT_F32, _settings(**settings), None, None))
+    _lib.check("qopt_adamw32bit_step", LIB.qopt_adamw32bit_step(
+        None, 0, QOPT_F32, QOPT_F32, _settings(step=1, **settings), None, None))
 
 
 def _adamw_args(plan, bits, lr, beta1, beta2, eps, weight_decay, step, grad_scale):

@@ -291,6 +291,14 @@ class AdamW(torch.optim.Optimizer):
                 st["step"] = 0
                 st.update(zip(keys, ts))
 
+    def _run(self, jobs):
+        """Run and clear a list of (bits, plan, arguments of the step)."""
+        while jobs:
+            bits, plan, arguments = jobs.pop(0)
+            (qopt_adamw8bit_step if bits == 8 else qopt_adamw32bit_step)(plan, **arguments)
+            for t in plan.tensors:
+                self.state[t[0]]["step"] = arguments["step"]
+
     @torch.no_grad()
     def step(self, closure=None, *, grad_scale=None):
         loss = None
@@ -298,10 +306,10 @@ class AdamW(torch.optim.Optimizer):
             with torch.enable_grad():
                 loss = closure()
         _check_grad_scale(grad_scale)
+        work, fresh = [], []
         for group in self.param_groups:  # checked before any state changes
-            for p in group["params"]:
-                if p.grad is None:
-                    continue
+            live = [p for p in group["params"] if p.grad is not None]
+            for p in live:
                 if p.grad.is_sparse:
                     raise RuntimeError("AdamW does not take sparse gradients")
                 if not p.is_contiguous() or not p.grad.is_contiguous():
@@ -312,12 +320,19 @@ class AdamW(torch.optim.Optimizer):
                     raise TypeError("AdamW needs float32 or bfloat16 parameters and gradients")
                 if grad_scale is not None and grad_scale.device != p.device:
                     raise ValueError("grad_scale must be on the parameters' GPU")
-        jobs, fresh = [], []
-        try:  # every group's lists and settings, before the first of them moves
-            for group in self.param_groups:
-                live = [p for p in group["params"] if p.grad is not None]
-                new = [p for p in live if not self.state[p]]
-                fresh += new
+            b1, b2 = group["betas"]
+            settings = dict(lr=float(group["lr"]), beta1=b1, beta2=b2, eps=group["eps"],
+                            weight_decay=group["weight_decay"])
+            if live:
+                _check_settings(**settings)
+            new = [p for p in live if not self.state[p]]
+            fresh += new
+            work.append((group, live, new, settings))
+        # A step that begins states makes every list, which is where overlaps are found, before it runs
+        # the first; later ones run each while the next is made.
+        jobs = []
+        try:
+            for group, live, new, settings in work:
                 self._init_states(group, new)
                 batches = {}
                 for p in live:
@@ -326,19 +341,14 @@ class AdamW(torch.optim.Optimizer):
                     key = (p.device, p.dtype, p.grad.dtype, bits, st["step"] + 1)
                     batches.setdefault(key, []).append((p, p.grad, *(st[k] for k in keys)))
                 for (*_, bits, step), items in batches.items():
-                    b1, b2 = group["betas"]
-                    settings = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
-                                    weight_decay=group["weight_decay"], step=step)
-                    _check_settings(**settings)
-                    jobs.append((bits, _adamw_plan(items, bits), settings))
+                    jobs.append((bits, _adamw_plan(items, bits), dict(settings, step=step, grad_scale=grad_scale)))
+                    if not fresh:
+                        self._run(jobs)
         except Exception:
             for p in fresh:
                 self.state.pop(p, None)
             raise
-        for bits, plan, settings in jobs:
-            (qopt_adamw8bit_step if bits == 8 else qopt_adamw32bit_step)(plan, grad_scale=grad_scale, **settings)
-            for t in plan.tensors:
-                self.state[t[0]]["step"] = settings["step"]
+        self._run(jobs)
         return loss
 
     _params_by_saved_id = Adam8bit._params_by_saved_id
