@@ -1,9 +1,9 @@
 """block_wise_bit_adam8bit_amd: block-wise dynamic-tree 8-bit Adam for MI355X.
 
 The compute lives in libqopt.so (HIP kernels for gfx950 behind the C ABI of
-include/qopt.h, include/qopt_embedding.h, include/qopt_fp8.h, include/qopt_norm.h); this package is
-its thin Python binding plus torch optimizers, the Stable Embedding module, layer normalisation and a
-linear layer whose products run in 8-bit floating point.
+include/qopt.h, include/qopt_embedding.h, include/qopt_fp8.h, include/qopt_fp4.h, include/qopt_norm.h); this package is
+its thin Python binding plus torch optimizers, the Stable Embedding module, layer normalisation and linear
+layers whose products run in 8-bit or 4-bit floating point.
 Importing it loads the library and fails with ImportError if it is not built.
 """
 
@@ -32,6 +32,10 @@ from .embedding import (  # noqa: F401
 from .fp8 import (  # noqa: F401
     Fp8Linear, Fp8LinearFunction, Fp8Matrix, fp8_linear, qopt_fp8_linear, qopt_fp8_matmul,
     qopt_fp8_quantize,
+)
+from .fp4 import (  # noqa: F401
+    Fp4Linear, Fp4LinearFunction, Fp4Matrix, fp4_linear, qopt_fp4_dequantize, qopt_fp4_linear,
+    qopt_fp4_matmul, qopt_fp4_quantize,
 )
 from .norm import (  # noqa: F401
     LayerNorm, LayerNormFunction, layer_norm, qopt_layer_norm_backward, qopt_layer_norm_forward,

@@ -16,6 +16,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqopt.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt.h")
 FP8_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_fp8.h")
+FP4_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_fp4.h")
 NORM_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_norm.h")
 EMB_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_embedding.h")
 
@@ -31,6 +32,10 @@ QOPT_FP8_ROWS, QOPT_FP8_TILES = 0, 1
 QOPT_FP8_BLOCK = 128
 QOPT_FP8_MAX_DIM = 8388608
 QOPT_FP8_FEW_ROWS = 32
+QOPT_FP4_BLOCK = 32
+QOPT_FP4_PAD = 256
+QOPT_FP4_MAX_DIM = 8388608
+QOPT_FP4_FEW_ROWS = 32
 QOPT_NORM_MAX_DIM = 8388608
 QOPT_NORM_MAX_ROWS = 1099511627776
 QOPT_EMB_VEC_MAX_DIM = 4096
@@ -187,6 +192,26 @@ _SIGNATURES = {
                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "qopt_fp8_linear_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "qopt_fp4_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "qopt_fp4_dequantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+                                           ctypes.c_int64, ctypes.c_void_p]),
+    "qopt_fp4_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
+                                       ctypes.c_void_p]),
+    "qopt_fp4_matmul_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "qopt_fp4_linear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_size_t, ctypes.c_void_p]),
+    "qopt_fp4_linear_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                 ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "qopt_layer_norm_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                                ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                                ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
@@ -226,7 +251,7 @@ def _load():
 LIB = _load()
 
 
-def header_constants(paths=(HEADER, EMB_HEADER, FP8_HEADER, NORM_HEADER)):
+def header_constants(paths=(HEADER, EMB_HEADER, FP8_HEADER, FP4_HEADER, NORM_HEADER)):
     """#define values of include/*.h (used by tests to check this mirror)."""
     out = {}
     for path in paths:
