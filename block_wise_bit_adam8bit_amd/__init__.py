@@ -1,9 +1,10 @@
 """block_wise_bit_adam8bit_amd: block-wise dynamic-tree 8-bit Adam for MI355X.
 
 The compute lives in libqopt.so (HIP kernels for gfx950 behind the C ABI of
-include/qopt.h, include/qopt_embedding.h, include/qopt_fp8.h, include/qopt_fp4.h, include/qopt_norm.h); this package is
-its thin Python binding plus torch optimizers, the Stable Embedding module, layer normalisation and linear
-layers whose products run in 8-bit or 4-bit floating point.
+include/qopt.h, include/qopt_embedding.h, include/qopt_fp8.h, include/qopt_fp4.h,
+include/qopt_muon.h, include/qopt_norm.h); this package is its thin Python binding plus torch
+optimizers, the Stable Embedding module, layer normalisation and linear layers whose products
+run in 8-bit or 4-bit floating point.
 Importing it loads the library and fails with ImportError if it is not built.
 """
 
@@ -36,6 +37,10 @@ from .fp8 import (  # noqa: F401
 from .fp4 import (  # noqa: F401
     Fp4Linear, Fp4LinearFunction, Fp4Matrix, fp4_linear, qopt_fp4_dequantize, qopt_fp4_linear,
     qopt_fp4_matmul, qopt_fp4_quantize,
+)
+from .muon import (  # noqa: F401
+    Muon, MuonPlan, qopt_muon32bit_plan, qopt_muon32bit_step, qopt_muon8bit_plan,
+    qopt_muon8bit_step, qopt_orthogonalize,
 )
 from .norm import (  # noqa: F401
     LayerNorm, LayerNormFunction, layer_norm, qopt_layer_norm_backward, qopt_layer_norm_forward,

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libqopt.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt.h")
 FP8_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_fp8.h")
 FP4_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_fp4.h")
+MUON_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_muon.h")
 NORM_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_norm.h")
 EMB_HEADER = os.path.join(os.path.dirname(_HERE), "include", "qopt_embedding.h")
 
@@ -36,6 +37,9 @@ QOPT_FP4_BLOCK = 32
 QOPT_FP4_PAD = 256
 QOPT_FP4_MAX_DIM = 8388608
 QOPT_FP4_FEW_ROWS = 32
+QOPT_MUON_MAX_DIM = 131072
+QOPT_MUON_MAX_STEPS = 32
+QOPT_MUON_ORIGINAL, QOPT_MUON_MATCH_RMS_ADAMW = 0, 1
 QOPT_NORM_MAX_DIM = 8388608
 QOPT_NORM_MAX_ROWS = 1099511627776
 QOPT_EMB_VEC_MAX_DIM = 4096
@@ -112,6 +116,29 @@ class qopt_adamw_hparams(ctypes.Structure):
         ("eps", ctypes.c_float),
         ("weight_decay", ctypes.c_float),
         ("step", ctypes.c_int64),
+    ]
+
+
+class qopt_muon_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("m_absmax", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+    ]
+
+
+class qopt_muon_hparams(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_float),
+        ("momentum", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("nesterov", ctypes.c_int32),
+        ("adjust", ctypes.c_int32),
+        ("steps", ctypes.c_int32),
     ]
 
 
@@ -212,6 +239,23 @@ _SIGNATURES = {
                                        ctypes.c_size_t, ctypes.c_void_p]),
     "qopt_fp4_linear_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    "qopt_orthogonalize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                          ctypes.c_float, ctypes.c_void_p, ctypes.c_int,
+                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qopt_orthogonalize_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
+                                                    ctypes.c_int64,
+                                                    ctypes.POINTER(ctypes.c_size_t)]),
+    "qopt_muon8bit_step": (ctypes.c_int, [ctypes.POINTER(qopt_muon_tensor), ctypes.c_int32,
+                                          ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                          ctypes.POINTER(qopt_muon_hparams), ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qopt_muon32bit_step": (ctypes.c_int, [ctypes.POINTER(qopt_muon_tensor), ctypes.c_int32,
+                                           ctypes.c_int, ctypes.c_int,
+                                           ctypes.POINTER(qopt_muon_hparams), ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "qopt_muon_workspace": (ctypes.c_int, [ctypes.POINTER(qopt_muon_tensor), ctypes.c_int32,
+                                           ctypes.POINTER(ctypes.c_size_t)]),
     "qopt_layer_norm_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                                ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                                ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
@@ -251,7 +295,8 @@ def _load():
 LIB = _load()
 
 
-def header_constants(paths=(HEADER, EMB_HEADER, FP8_HEADER, FP4_HEADER, NORM_HEADER)):
+def header_constants(paths=(HEADER, EMB_HEADER, FP8_HEADER, FP4_HEADER, MUON_HEADER,
+                            NORM_HEADER)):
     """#define values of include/*.h (used by tests to check this mirror)."""
     out = {}
     for path in paths:

@@ -1,0 +1,914 @@
+// Newton-Schulz orthogonalisation and the Muon step for gfx950: the kernels of include/qopt_muon.h.
+//
+// With A = X X^T (m x m, m the shorter side) the iteration X = (a I + b A + c A^2) X is a polynomial of A
+// times X, and so is what several iterations make: their polynomials commute and are symmetric.  A group of
+// iterations is therefore carried out on m x m matrices alone,
+//     P = a I + b A + c A^2,  Q = P Q,  A = P A P,
+// and Q is applied to X at its end; every product but that one is symmetric, so that only the tiles on and
+// below the diagonal are computed, each stored with its mirror image.  For n / m = r a group of L iterations
+// takes (in products of m x m matrices) r / 2 + L / 2 + (L - 1) / 2 + (L - 1) + r, where the iterations by
+// themselves take L (3 r / 2 + 1 / 2): for five iterations as 3 + 2, 3 r + 7 against 7.5 r + 2.5, the same
+// for square matrices and less than half for r = 8.
+// Groups are at most three long, because a singular value s of X stands in A as s^2: what rounding adds to a
+// small one grows by a^2 = 11.9 per iteration on A, a fresh A = X X^T brings it back.  (With rounding to 22
+// bits: three and two iterations are as exact as one at a time on every matrix tried, 4e-7 for normal
+// entries, 5e-6 with eight directions 170 times the rest; four in one group end in infinities there.)
+//
+// Numbers.  A value is kept as hi + lo, two binary16 numbers, times a power of two that keeps the largest
+// possible value (|X| <= 1.203, A <= 1.45, P <= 3.4445, Q <= 3.4445^3) under 65504; hi hi + hi lo + lo hi
+// with binary32 sums leaves out 2^-22 of a product.  Single binary16 numbers, where the destination is
+// bfloat16 and at most two iterations are left, are a third of the instructions.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <vector>
+
+#include "blockwise_code.h"
+#include "product_tile.h"
+#include "qopt_muon.h"
+
+namespace {
+
+using namespace product;
+using blockwise::BlockScale;
+using blockwise::Encoder;
+
+constexpr float kA = 3.4445f, kB = -4.775f, kC = 2.0315f;
+constexpr int kExp = 12, kExpQ = 10;  // powers of two of X, A, P and P A, and of a product Q
+constexpr int kGroupSteps = 3;        // iterations on A before it is made anew
+constexpr int kMaxJobs = 32;          // of one launch (its arguments are 4 KB at most)
+constexpr int kMaxParts = 512;        // partial sums of squares per matrix
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// A matrix as an operand: rows of `pad` values (a multiple of 64).  Split: for every 8 values 16 bytes of hi
+// and 16 bytes of lo; single: 2 bytes per value.
+constexpr int64_t kPad = 64;
+__host__ __device__ constexpr int64_t padded(int64_t d) { return ceil_div(d, kPad) * kPad; }
+__host__ __device__ constexpr int64_t row_bytes(int64_t cols, bool split) { return padded(cols) * (split ? 4 : 2); }
+
+// ------------------------------------------------------------------ momentum and norms
+
+struct SourceJob {
+  const void* g;  // gradient, or the matrix itself
+  void* m;
+  float* absmax;
+  float* u;       // where the update goes
+  double* parts;  // partial sums of squares
+  int64_t n;
+  uint32_t groups;
+};
+struct SourceArgs {
+  SourceJob jobs[kMaxJobs];
+  const qopt_codebook* cb;
+  const float* grad_scale;
+  float mu, omu;
+  int nesterov;
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+
+// Elements i to i + 7 of n, 0 behind the end.
+template <typename T> __device__ __forceinline__ void load8(const T* p, int64_t i, int64_t n, float (&v)[8]) {
+  T w[8];
+  if (i + 8 <= n) {
+    __builtin_memcpy(w, p + i, sizeof(w));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = to_f32(w[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = i + e < n ? to_f32(p[i + e]) : 0.0f;
+  }
+}
+
+// Sum over the 4 waves of a workgroup, in a fixed order, for thread 0.
+__device__ __forceinline__ double group_sum(double s, double (&slots)[4]) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x / kWave] = s;
+  __syncthreads();
+  return slots[0] + slots[1] + slots[2] + slots[3];
+}
+
+enum Source : int { kPlain = 0, kMomentum32 = 1, kMomentum8 = 2 };
+
+// Blocks of 2048 of one matrix (blockIdx.y), every groups-th by a workgroup: the new momentum, the update u
+// and its sum of squares (binary64: squares of any binary32 numbers neither overflow nor vanish).
+template <typename GT, int kSource> __global__ void __launch_bounds__(256) source_kernel(SourceArgs a) {
+  __shared__ __align__(16) qopt_codebook cb;  // kMomentum8
+  __shared__ double slots[4];
+  __shared__ uint32_t maxima[2][4];
+  const SourceJob& job = a.jobs[blockIdx.y];
+  if (blockIdx.x >= job.groups) return;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  if constexpr (kSource == kMomentum8) {
+    for (uint32_t i = threadIdx.x; i < sizeof(qopt_codebook) / 16; i += 256)
+      reinterpret_cast<uint4*>(&cb)[i] = reinterpret_cast<const uint4*>(a.cb)[i];
+    __syncthreads();
+  }
+  const int64_t n = job.n;
+  double sum = 0.0;
+  int turn = 0;
+  for (int64_t b = blockIdx.x; b * QOPT_BLOCK < n; b += job.groups, turn ^= 1) {
+    const int64_t i = b * QOPT_BLOCK + 8 * threadIdx.x;
+    float g[8];
+    load8(static_cast<const GT*>(job.g), i, n, g);
+    if constexpr (kSource != kPlain) {
+      float m[8];
+      if constexpr (kSource == kMomentum32) {
+        load8(static_cast<const float*>(job.m), i, n, m);
+      } else {
+        const uint8_t* codes = static_cast<const uint8_t*>(job.m);
+        const float amax = job.absmax[b];
+        uint8_t c[8];
+        if (i + 8 <= n) {
+          __builtin_memcpy(c, codes + i, 8);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c[e] = i + e < n ? codes[i + e] : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = i + e < n ? cb.decode[c[e]] * amax : 0.0f;
+      }
+      float most = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (a.grad_scale) g[e] = g[e] * gs;
+        const float t = g[e] * a.omu;
+        m[e] = m[e] * a.mu + t;
+        g[e] = a.nesterov ? m[e] * a.mu + t : m[e];
+        if (i + e >= n) m[e] = g[e] = 0.0f;  // behind the end a factor may be infinite
+        most = __builtin_elementwise_maximum(most, fabsf(m[e]));
+      }
+      if constexpr (kSource == kMomentum32) {
+        float* to = static_cast<float*>(job.m) + i;
+        if (i + 8 <= n) {
+          __builtin_memcpy(to, m, sizeof(m));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i + e < n) to[e] = m[e];
+        }
+      } else {
+        uint32_t bits = __float_as_uint(most);
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+          const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(bits), d));
+          bits = bits > o ? bits : o;
+        }
+        if ((threadIdx.x & 63) == 0) maxima[turn][threadIdx.x / kWave] = bits;
+        __syncthreads();
+        bits = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) bits = bits > maxima[turn][w] ? bits : maxima[turn][w];
+        const BlockScale s = blockwise::block_scale(__uint_as_float(bits), cb.sign_mask);
+        const Encoder enc = blockwise::make_encoder(&cb);
+        uint8_t c[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = s.zero ? 0 : static_cast<uint8_t>(blockwise::encode_signed(enc, s, m[e]));
+        uint8_t* to = static_cast<uint8_t*>(job.m) + i;
+        if (i + 8 <= n) {
+          __builtin_memcpy(to, c, 8);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i + e < n) to[e] = c[e];
+        }
+        if (threadIdx.x == 0) job.absmax[b] = s.absmax;
+      }
+      float* u = job.u + i;
+      if (i + 8 <= n) {
+        __builtin_memcpy(u, g, sizeof(g));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i + e < n) u[e] = g[e];
+      }
+    }
+    double part = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part += static_cast<double>(g[e]) * static_cast<double>(g[e]);
+    sum += part;
+  }
+  const double s = group_sum(sum, slots);
+  if (threadIdx.x == 0) job.parts[blockIdx.x] = s;
+}
+
+// ------------------------------------------------------------------ operands from the update
+
+// Eight values as an operand holds them: at `col` (a multiple of 8) of a row.
+template <bool kSplit> __device__ __forceinline__ void write8(uint8_t* row, int64_t col, const float (&v)[8]) {
+  f16x8 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = static_cast<_Float16>(v[e]);
+    lo[e] = static_cast<_Float16>(v[e] - static_cast<float>(hi[e]));
+  }
+  if constexpr (kSplit) {
+    *reinterpret_cast<f16x8*>(row + col * 4) = hi;
+    *reinterpret_cast<f16x8*>(row + col * 4 + 16) = lo;
+  } else {
+    *reinterpret_cast<f16x8*>(row + col * 2) = hi;
+  }
+}
+
+struct PackJob {
+  const void* src;        // [rows, cols]
+  uint8_t *same, *other;  // as operands: its rows, and its transpose's
+  const double* parts;
+  int64_t rows, cols;
+  uint32_t groups, first, across;
+};
+struct PackArgs {
+  PackJob jobs[kMaxJobs];
+  int njobs;
+  double eps;
+};
+
+// X = U 2^kExp / max(|U|, eps) and its transpose, split.  A wave takes 64 x 64 values, a lane 8 x 8 of them:
+// it reads 8 runs of 8, writes them as 8 places of the operand's rows, and of the transpose's; the lanes next
+// to each other make runs of 256 bytes either way.
+template <typename ST> __global__ void __launch_bounds__(256) pack_kernel(PackArgs a) {
+  __shared__ double slots[4];
+  int j = 0;
+  while (j + 1 < a.njobs && blockIdx.x >= a.jobs[j + 1].first) ++j;
+  const PackJob& job = a.jobs[j];
+  double s = 0.0;
+  for (uint32_t i = threadIdx.x; i < job.groups; i += 256) s += job.parts[i];
+  const double norm = sqrt(group_sum(s, slots));
+  const double scale = static_cast<double>(1 << kExp) / (norm < a.eps ? a.eps : norm);  // a NaN stays one
+  const uint32_t at = blockIdx.x - job.first;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / kWave;
+  const int64_t r0 = static_cast<int64_t>(at / job.across) * 64 + 8 * (lane >> 3);
+  const int64_t c0 = (static_cast<int64_t>(at % job.across) * 4 + wave) * 64 + 8 * (lane & 7);
+  if (c0 >= padded(job.cols)) return;  // r0 lies within the padded rows always
+  float v[8][8];
+  const ST* src = static_cast<const ST*>(job.src);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (r0 + i < job.rows) {
+      load8(src + (r0 + i) * job.cols, c0, job.cols, v[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = c0 + e < job.cols ? static_cast<float>(static_cast<double>(v[i][e]) * scale) : 0.0f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (r0 + i < job.rows) write8<true>(job.same + (r0 + i) * row_bytes(job.cols, true), c0, v[i]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i][e];
+    if (c0 + e < job.cols) write8<true>(job.other + (c0 + e) * row_bytes(job.rows, true), r0, t);
+  }
+}
+
+// ------------------------------------------------------------------ products
+
+// One product out = l r^T, with what its epilogue needs.
+struct Job {
+  const uint8_t *l, *r;   // operands: rows of k_bytes
+  const uint8_t* add;     // the polynomial's A
+  uint8_t *out, *out_t;   // the result as an operand, and its transpose
+  void* dst;              // the last product's destination, [lrows, rrows]
+  int32_t lrows, rrows;
+  uint32_t k_bytes, out_bytes, out_t_bytes;  // bytes per row
+  uint32_t first, tiles_m, tiles_n;
+  float factor, rate;
+};
+struct ProductArgs {
+  Job jobs[kMaxJobs];
+  int njobs;
+  float decay;
+};
+static_assert(sizeof(ProductArgs) <= 4096, "kernel arguments");
+
+enum Epilogue : int {
+  kSymmetric,   // out = factor l r^T, which is symmetric
+  kPolynomial,  // out = a I + b add + c l r^T likewise
+  kApply,       // out and out_t, in the layout of the group that comes next
+  kResult,      // dst = factor l r^T
+  kUpdate       // dst = dst * decay - factor l r^T * rate
+};
+
+template <bool kSplit> struct HalfOp {
+  struct Side {};
+  static constexpr int kSideLoads = 0, kTerms = kSplit ? 3 : 2;
+  __device__ __forceinline__ Side load(int) const { return {}; }
+  static __device__ __forceinline__ void touch(Side&) {}
+  // split: pieces 0 and 1 are hi and lo of 8 values; single: two times 8 values
+  template <int kHalf, int kTerm, int kI, int kJ>
+  static __device__ __forceinline__ void multiply(f32x16& acc, const i32x4 (&a)[2], const i32x4 (&b)[2], const Side&) {
+    constexpr int kL = kSplit ? kTerm == 2 : kTerm, kR = kSplit ? kTerm == 1 : kTerm;
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b[kR]), __builtin_bit_cast(f16x8, a[kL]), acc, 0, 0, 0);
+  }
+};
+
+template <int kCount> struct HalfVec;
+template <> struct HalfVec<2> { typedef f16x2 type; };
+template <> struct HalfVec<4> { typedef f16x4 type; };
+
+// Values of kCount consecutive rows in one column, as the transpose's row holds them.
+template <bool kSplit, int kCount> __device__ __forceinline__ void write_column(uint8_t* row, int64_t at, const float (&v)[kCount]) {
+  typename HalfVec<kCount>::type hi, lo;
+#pragma unroll
+  for (int e = 0; e < kCount; ++e) {
+    hi[e] = static_cast<_Float16>(v[e]);
+    lo[e] = static_cast<_Float16>(v[e] - static_cast<float>(hi[e]));
+  }
+  if constexpr (kSplit) {
+    uint8_t* to = row + (at >> 3) * 32 + (at & 7) * 2;
+    __builtin_memcpy(to, &hi, sizeof(hi));
+    __builtin_memcpy(to + 16, &lo, sizeof(lo));
+  } else {
+    __builtin_memcpy(row + at * 2, &hi, sizeof(hi));
+  }
+}
+
+template <typename OT> __device__ __forceinline__ void load_out(const OT* p, float (&v)[8]) {
+  OT w[8];
+  __builtin_memcpy(w, p, sizeof(w));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f32(w[e]);
+}
+
+// The tile of l's rows from m0 and r's rows from n0 on.  kSplit: of the operands; kSplitOut: of the result.
+template <typename T, int kWavesN, bool kSplit, bool kSplitOut, int kEpilogue, typename OT>
+__device__ __forceinline__ void product_tile(const Job& job, float decay, uint8_t* lds, int64_t m0, int64_t n0) {
+  constexpr int kFm = T::kFm, kFn = T::kFn;
+  static_assert(kFn == 2, "a lane's columns are eight places of an operand's row");
+  typename T::Acc acc;
+  T::sums({job.l, m0, job.lrows, job.k_bytes}, {job.r, n0, job.rrows, job.k_bytes}, HalfOp<kSplit>{}, lds, 0,
+          static_cast<int>(job.k_bytes / kStepBytes) - 1, acc);
+  const int lane = threadIdx.x & 63, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t row0 = m0 + wave / kWavesN * T::kWm + kFm * (lane & 31), col0 = n0 + wave % kWavesN * T::kWn;
+  const int64_t pm = padded(job.lrows), pn = padded(job.rrows);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t col = col0 + 2 * (8 * q + 4 * h);
+    float v[kFm][8];
+#pragma unroll
+    for (int i = 0; i < kFm; ++i) {
+      const int64_t row = row0 + i;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[i][2 * e] = acc[i][0][4 * q + e] * job.factor;
+        v[i][2 * e + 1] = acc[i][1][4 * q + e] * job.factor;
+      }
+      if constexpr (kEpilogue == kPolynomial) {
+        if (row < job.lrows && col < pn) {
+          const uint8_t* from = job.add + row * job.k_bytes;
+          f16x8 hi, lo = {0, 0, 0, 0, 0, 0, 0, 0};
+          if constexpr (kSplit) {
+            hi = *reinterpret_cast<const f16x8*>(from + col * 4);
+            lo = *reinterpret_cast<const f16x8*>(from + col * 4 + 16);
+          } else {
+            hi = *reinterpret_cast<const f16x8*>(from + col * 2);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
+            v[i][e] = v[i][e] * kC + x * kB + (row == col + e ? kA * static_cast<float>(1 << kExp) : 0.0f);
+          }
+        }
+      }
+      if constexpr (kEpilogue == kResult || kEpilogue == kUpdate) {
+        if (row < job.lrows) {
+          OT* dst = static_cast<OT*>(job.dst) + row * job.rrows + col;
+          if (col + 8 <= job.rrows) {  // at any alignment
+            OT w[8];
+            float p[8];
+            if constexpr (kEpilogue == kUpdate) load_out(dst, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if constexpr (kEpilogue == kUpdate) v[i][e] = p[e] * decay - v[i][e] * job.rate;
+              store1(w + e, v[i][e]);
+            }
+            __builtin_memcpy(dst, w, sizeof(w));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (col + e < job.rrows) {
+                if constexpr (kEpilogue == kUpdate) v[i][e] = to_f32(dst[e]) * decay - v[i][e] * job.rate;
+                store1(dst + e, v[i][e]);
+              }
+          }
+        }
+      } else {
+        if (row < job.lrows && col < pn) write8<kSplitOut>(job.out + row * job.out_bytes, col, v[i]);
+      }
+    }
+    // the mirror image, or the transpose: rows of the result are places there, up to the padding
+    if constexpr (kEpilogue == kSymmetric || kEpilogue == kPolynomial || kEpilogue == kApply) {
+      uint8_t* out = kEpilogue == kApply ? job.out_t : job.out;
+      const uint32_t bytes = kEpilogue == kApply ? job.out_t_bytes : job.out_bytes;
+      if (row0 < pm && (kEpilogue == kApply || m0 != n0)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float t[kFm];
+#pragma unroll
+          for (int i = 0; i < kFm; ++i) t[i] = v[i][e];
+          if (col + e < job.rrows) write_column<kSplitOut, kFm>(out + (col + e) * bytes, row0, t);
+        }
+      }
+    }
+  }
+}
+
+constexpr uint32_t kGroup = 8;  // tiles counted down before the next one across
+
+template <bool kBig, bool kSplit, bool kSplitOut, int kEpilogue, typename OT>
+__global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a) {
+  constexpr int kSide = kBig ? 256 : 128, kWavesN = kBig ? 4 : 2;
+  typedef Tile<kSide, kSide, 2, kWavesN, kBig ? 2 : 3, HalfOp<kSplit>> T;
+  __shared__ __align__(16) uint8_t lds[T::kLds];
+  uint32_t t = xcd_order(blockIdx.x, gridDim.x);
+  int j = 0;
+  while (j + 1 < a.njobs && t >= a.jobs[j + 1].first) ++j;
+  const Job& job = a.jobs[j];
+  t -= job.first;
+  uint32_t tm, tn;
+  if constexpr (kEpilogue == kSymmetric || kEpilogue == kPolynomial) {
+    // tiles on and below the diagonal: row i begins with number i (i + 1) / 2
+    tm = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
+    while (tm * (tm + 1) / 2 > t) --tm;
+    while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
+    tn = t - tm * (tm + 1) / 2;
+  } else {
+    const uint32_t group = t / (kGroup * job.tiles_n), left = job.tiles_m - group * kGroup;
+    const uint32_t rows = left < kGroup ? left : kGroup, in = t % (kGroup * job.tiles_n);
+    tm = group * kGroup + in % rows;
+    tn = in / rows;
+  }
+  product_tile<T, kWavesN, kSplit, kSplitOut, kEpilogue, OT>(job, a.decay, lds, static_cast<int64_t>(tm) * kSide,
+                                                             static_cast<int64_t>(tn) * kSide);
+}
+
+// ------------------------------------------------------------------ host
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+int launch_status() { return hipGetLastError() == hipSuccess ? QOPT_OK : QOPT_ELAUNCH; }
+bool bad_dtype(int d) { return d != QOPT_F32 && d != QOPT_BF16; }
+uintptr_t size_of(int d) { return d == QOPT_F32 ? 4 : 2; }
+bool finite(float x) { return std::isfinite(x); }
+
+// A matrix under work: its shorter side m, its longer side n, and its buffers in the workspace.
+struct Matrix {
+  const void* src;  // gradient, or the matrix itself
+  void* moment;
+  float* absmax;
+  void* dst;
+  int64_t rows, cols, m, n;
+  float rate;
+  float* u;
+  double* parts;
+  uint32_t groups;
+  uint8_t *x, *xt[2], *g, *p, *h, *q[2];
+};
+
+int64_t up(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
+
+// Lays a matrix's buffers out from `at` on and returns their end.  (u is read before xt[1] is first written.)
+uint8_t* lay_out(Matrix& a, uint8_t* at) {
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = at;
+    at += up(bytes);
+    return p;
+  };
+  a.parts = reinterpret_cast<double*>(take(kMaxParts * 8));
+  a.x = take(a.m * row_bytes(a.n, true));
+  a.xt[0] = take(a.n * row_bytes(a.m, true));
+  a.xt[1] = take(a.n * row_bytes(a.m, true));
+  a.u = reinterpret_cast<float*>(a.xt[1]);
+  for (uint8_t** b : {&a.g, &a.p, &a.h, &a.q[0], &a.q[1]}) *b = take(a.m * row_bytes(a.m, true));
+  return at;
+}
+
+int64_t tiles_of(int64_t m, int64_t side) { return ceil_div(m, side); }
+int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
+
+// Matrices whose products share their launches: of one m at most 16 (a launch has two jobs of each), until
+// their symmetric products fill the chip twice.
+constexpr size_t kMaxBatch = 16;
+size_t batch_end(const std::vector<Matrix>& all, size_t first) {
+  int64_t tiles = 0;
+  size_t i = first;
+  while (i < all.size() && i - first < kMaxBatch && all[i].m == all[first].m && tiles < 512) {
+    tiles += triangle(tiles_of(all[i].m, 256));
+    ++i;
+  }
+  return i;
+}
+
+int64_t workspace_of(std::vector<Matrix>& all) {
+  int64_t most = 0;
+  for (size_t first = 0; first < all.size();) {
+    const size_t end = batch_end(all, first);
+    uint8_t* at = nullptr;
+    for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
+    most = std::max<int64_t>(most, reinterpret_cast<intptr_t>(at));
+    first = end;
+  }
+  return most;
+}
+
+struct Run {
+  int source;  // a Source
+  int src_dtype, dst_dtype;
+  bool update;
+  const qopt_codebook* cb;
+  const float* grad_scale;
+  float mu, omu, eps, decay;
+  int nesterov, steps;
+  hipStream_t stream;
+};
+
+template <typename GT> void launch_source(const SourceArgs& a, int source, dim3 grid, hipStream_t s) {
+  if (source == kPlain) hipLaunchKernelGGL((source_kernel<GT, kPlain>), grid, dim3(256), 0, s, a);
+  else if (source == kMomentum32) hipLaunchKernelGGL((source_kernel<GT, kMomentum32>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((source_kernel<GT, kMomentum8>), grid, dim3(256), 0, s, a);
+}
+
+template <bool kBig, bool kSplit, bool kSplitOut, int kEpilogue, typename OT = float>
+void launch_product(const ProductArgs& a, unsigned tiles, hipStream_t s) {
+  hipLaunchKernelGGL((product_kernel<kBig, kSplit, kSplitOut, kEpilogue, OT>), dim3(tiles), dim3(kBig ? 512 : 256), 0, s, a);
+}
+
+// A launch under construction: jobs, and the tiles that they come to.
+struct Launch {
+  ProductArgs args = {};
+  int epilogue;
+  bool split, split_out;
+  int dst_dtype = QOPT_F32;
+
+  Launch(int e, bool in, bool out) : epilogue(e), split(in), split_out(out) {}
+  bool symmetric() const { return epilogue == kSymmetric || epilogue == kPolynomial; }
+  void add(const Job& j) { args.jobs[args.njobs++] = j; }
+
+  // Tiles of 256 x 256, or of 128 x 128 where the chip takes less time over those: a round of big ones takes
+  // 3.6 times one of small ones.
+  int64_t count(int64_t side) {
+    int64_t all = 0;
+    for (int i = 0; i < args.njobs; ++i) {
+      Job& j = args.jobs[i];
+      j.first = static_cast<uint32_t>(all);
+      j.tiles_m = static_cast<uint32_t>(ceil_div(j.lrows, side));
+      j.tiles_n = static_cast<uint32_t>(ceil_div(j.rrows, side));
+      all += symmetric() ? triangle(j.tiles_m) : static_cast<int64_t>(j.tiles_m) * j.tiles_n;
+    }
+    return all;
+  }
+  int run(hipStream_t s) {
+    const int64_t small = count(128), large = count(256);
+    const bool big = static_cast<double>(ceil_div(large, 256)) * 3.6 <= static_cast<double>(ceil_div(small, 256));
+    const unsigned tiles = static_cast<unsigned>(big ? count(256) : count(128));
+    return big ? pick<true>(tiles, s) : pick<false>(tiles, s);
+  }
+  template <bool kBig> int pick(unsigned tiles, hipStream_t s) {
+    switch (epilogue) {
+      case kSymmetric:
+        if (split) launch_product<kBig, true, true, kSymmetric>(args, tiles, s);
+        else launch_product<kBig, false, false, kSymmetric>(args, tiles, s);
+        break;
+      case kPolynomial:
+        if (split) launch_product<kBig, true, true, kPolynomial>(args, tiles, s);
+        else launch_product<kBig, false, false, kPolynomial>(args, tiles, s);
+        break;
+      case kApply:
+        if (split_out) launch_product<kBig, true, true, kApply>(args, tiles, s);
+        else launch_product<kBig, true, false, kApply>(args, tiles, s);
+        break;
+      case kResult:
+        last<kBig, kResult>(tiles, s);
+        break;
+      default:
+        last<kBig, kUpdate>(tiles, s);
+    }
+    return launch_status();
+  }
+  template <bool kBig, int kEpilogue> void last(unsigned tiles, hipStream_t s) {
+    if (dst_dtype == QOPT_F32) launch_product<kBig, true, true, kEpilogue, float>(args, tiles, s);
+    else if (split) launch_product<kBig, true, true, kEpilogue, uint16_t>(args, tiles, s);
+    else launch_product<kBig, false, false, kEpilogue, uint16_t>(args, tiles, s);
+  }
+};
+
+float power(int e) { return std::ldexp(1.0f, e); }
+
+// l r^T with l [lrows, k], r [rrows, k] as operands; its result has the exponent `to`.
+Job job_of(const uint8_t* l, int64_t lrows, const uint8_t* r, int64_t rrows, int64_t k, bool split, int exp_in, int to) {
+  Job j = {};
+  j.l = l;
+  j.r = r;
+  j.lrows = static_cast<int32_t>(lrows);
+  j.rrows = static_cast<int32_t>(rrows);
+  j.k_bytes = static_cast<uint32_t>(row_bytes(k, split));
+  j.factor = power(to - exp_in);
+  return j;
+}
+
+int run_batch(Matrix* mats, int count, const Run& r) {
+  hipStream_t s = r.stream;
+  {
+    SourceArgs a = {};
+    a.cb = r.cb;
+    a.grad_scale = r.grad_scale;
+    a.mu = r.mu;
+    a.omu = r.omu;
+    a.nesterov = r.nesterov;
+    uint32_t most = 0;
+    for (int i = 0; i < count; ++i) {
+      Matrix& m = mats[i];
+      const int64_t n = m.rows * m.cols;
+      m.groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(n, QOPT_BLOCK), kMaxParts));
+      most = std::max(most, m.groups);
+      a.jobs[i] = {m.src, m.moment, m.absmax, m.u, m.parts, n, m.groups};
+    }
+    const dim3 grid(most, static_cast<unsigned>(count));
+    if (r.src_dtype == QOPT_F32) launch_source<float>(a, r.source, grid, s);
+    else launch_source<uint16_t>(a, r.source, grid, s);
+    if (launch_status() != QOPT_OK) return QOPT_ELAUNCH;
+  }
+  {
+    PackArgs a = {};
+    a.njobs = count;
+    a.eps = static_cast<double>(r.eps);
+    uint32_t tiles = 0;
+    for (int i = 0; i < count; ++i) {
+      const Matrix& m = mats[i];
+      const bool tall = m.rows > m.cols;
+      PackJob& j = a.jobs[i];
+      j = {r.source == kPlain ? m.src : m.u, tall ? m.xt[0] : m.x, tall ? m.x : m.xt[0], m.parts, m.rows, m.cols, m.groups, tiles,
+           static_cast<uint32_t>(ceil_div(padded(m.cols), 256))};
+      tiles += j.across * static_cast<uint32_t>(padded(m.rows) / 64);
+    }
+    if (r.source == kPlain && r.src_dtype == QOPT_BF16) hipLaunchKernelGGL(pack_kernel<uint16_t>, dim3(tiles), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(pack_kernel<float>, dim3(tiles), dim3(256), 0, s, a);
+    if (launch_status() != QOPT_OK) return QOPT_ELAUNCH;
+  }
+  const int64_t m = mats[0].m;
+  auto symmetric = [&](const uint8_t* a, const uint8_t* b, uint8_t* out, int exp_in, int to, bool split) {
+    Job j = job_of(a, m, b, m, m, split, exp_in, to);
+    j.out = out;
+    j.out_bytes = j.k_bytes;
+    return j;
+  };
+  int rc = QOPT_OK, turn = 0;  // xt[turn] is current
+  for (int done = 0; done < r.steps && rc == QOPT_OK;) {
+    const int length = std::min(kGroupSteps, r.steps - done);
+    auto is_split = [&](int from) {  // whether the group that begins there keeps 22 bits
+      return r.dst_dtype == QOPT_F32 || from == 0 || r.steps - from > 2;
+    };
+    const bool split = is_split(done), end = done + length == r.steps;
+    {
+      Launch gram(kSymmetric, split, split);
+      for (int i = 0; i < count; ++i) {
+        Job j = job_of(mats[i].x, m, mats[i].x, m, mats[i].n, split, 2 * kExp, kExp);
+        j.out = mats[i].g;
+        j.out_bytes = static_cast<uint32_t>(row_bytes(m, split));
+        gram.add(j);
+      }
+      rc = gram.run(s);
+    }
+    int q = 0, exp_q = kExp;  // q[q] is the product of the polynomials so far
+    for (int it = 0; it < length && rc == QOPT_OK; ++it) {
+      Launch poly(kPolynomial, split, split);
+      for (int i = 0; i < count; ++i) {
+        Job j = symmetric(mats[i].g, mats[i].g, it == 0 ? mats[i].q[0] : mats[i].p, 2 * kExp, kExp, split);
+        j.add = mats[i].g;
+        poly.add(j);
+      }
+      rc = poly.run(s);
+      if (rc != QOPT_OK) break;
+      Launch both(kSymmetric, split, split);
+      for (int i = 0; i < count; ++i) {
+        const uint8_t* p = it == 0 ? mats[i].q[0] : mats[i].p;
+        if (it > 0) both.add(symmetric(p, mats[i].q[q], mats[i].q[1 - q], kExp + exp_q, kExpQ, split));
+        if (it + 1 < length) both.add(symmetric(p, mats[i].g, mats[i].h, 2 * kExp, kExp, split));
+      }
+      if (it > 0) {
+        q = 1 - q;
+        exp_q = kExpQ;
+      }
+      if (both.args.njobs) rc = both.run(s);
+      if (it + 1 < length && rc == QOPT_OK) {
+        Launch next(kSymmetric, split, split);
+        for (int i = 0; i < count; ++i)
+          next.add(symmetric(mats[i].h, it == 0 ? mats[i].q[0] : mats[i].p, mats[i].g, 2 * kExp, kExp, split));
+        rc = next.run(s);
+      }
+    }
+    if (rc != QOPT_OK) break;
+    done += length;
+    if (!end) {
+      const bool out_split = is_split(done);
+      Launch apply(kApply, split, out_split);
+      for (int i = 0; i < count; ++i) {
+        Job j = job_of(mats[i].q[q], m, mats[i].xt[turn], mats[i].n, m, split, exp_q + kExp, kExp);
+        j.out = mats[i].x;
+        j.out_bytes = static_cast<uint32_t>(row_bytes(mats[i].n, out_split));
+        j.out_t = mats[i].xt[1 - turn];
+        j.out_t_bytes = static_cast<uint32_t>(row_bytes(m, out_split));
+        apply.add(j);
+      }
+      rc = apply.run(s);
+      turn = 1 - turn;
+    } else {
+      Launch last(r.update ? kUpdate : kResult, split, split);
+      last.dst_dtype = r.dst_dtype;
+      last.args.decay = r.decay;
+      for (int i = 0; i < count; ++i) {
+        const Matrix& a = mats[i];
+        // the transpose of Q X is X^T Q: a tall matrix's rows
+        Job j = a.rows > a.cols ? job_of(a.xt[turn], a.n, a.q[q], m, m, split, exp_q + kExp, 0)
+                                : job_of(a.q[q], m, a.xt[turn], a.n, m, split, exp_q + kExp, 0);
+        j.dst = a.dst;
+        j.rate = a.rate;
+        last.add(j);
+      }
+      rc = last.run(s);
+    }
+  }
+  return rc;
+}
+
+int run_all(std::vector<Matrix>& all, const Run& r, void* workspace) {
+  for (size_t first = 0; first < all.size();) {
+    const size_t end = batch_end(all, first);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
+    const int rc = run_batch(all.data() + first, static_cast<int>(end - first), r);
+    if (rc != QOPT_OK) return rc;
+    first = end;
+  }
+  return QOPT_OK;
+}
+
+bool bad_dim(int64_t d) { return d < 0 || d > QOPT_MUON_MAX_DIM; }
+bool bad_steps(int steps) { return steps < 1 || steps > QOPT_MUON_MAX_STEPS; }
+bool bad_eps(float eps) { return !finite(eps) || !(eps > 0.0f); }
+
+Matrix matrix_of(int64_t rows, int64_t cols) {
+  Matrix a = {};
+  a.rows = rows;
+  a.cols = cols;
+  a.m = std::min(rows, cols);
+  a.n = std::max(rows, cols);
+  return a;
+}
+
+// The step's matrices with elements, those of one m together, otherwise in their order.
+int collect(const qopt_muon_tensor* tensors, int32_t ntensors, std::vector<Matrix>& all) {
+  if (ntensors < 0 || (ntensors > 0 && !tensors)) return QOPT_EINVAL;
+  for (int32_t i = 0; i < ntensors; ++i) {
+    const qopt_muon_tensor& t = tensors[i];
+    if (bad_dim(t.rows) || bad_dim(t.cols)) return QOPT_EINVAL;
+    if (t.rows == 0 || t.cols == 0) continue;
+    Matrix a = matrix_of(t.rows, t.cols);
+    a.src = t.grad;
+    a.moment = t.m;
+    a.absmax = t.m_absmax;
+    a.dst = t.param;
+    all.push_back(a);
+  }
+  std::stable_sort(all.begin(), all.end(), [](const Matrix& a, const Matrix& b) { return a.m < b.m; });
+  return QOPT_OK;
+}
+
+int muon_step(const qopt_muon_tensor* tensors, int32_t ntensors, int param_dtype, int grad_dtype, bool coded,
+              const qopt_codebook* cb, const qopt_muon_hparams* hp, const float* grad_scale, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  if (!hp) return QOPT_EINVAL;
+  std::vector<Matrix> all;
+  const int rc = collect(tensors, ntensors, all);
+  if (rc != QOPT_OK) return rc;
+  if (bad_dtype(param_dtype) || bad_dtype(grad_dtype)) return QOPT_EUNSUPPORTED;
+  if (!finite(hp->lr) || hp->lr < 0.0f || !finite(hp->weight_decay) || hp->weight_decay < 0.0f || bad_eps(hp->eps) ||
+      !(hp->momentum >= 0.0f && hp->momentum < 1.0f) || bad_steps(hp->steps) || (hp->nesterov != 0 && hp->nesterov != 1))
+    return QOPT_EINVAL;
+  if (hp->adjust != QOPT_MUON_ORIGINAL && hp->adjust != QOPT_MUON_MATCH_RMS_ADAMW) return QOPT_EUNSUPPORTED;
+  for (Matrix& a : all) {
+    if (!a.src || !a.moment || !a.dst || (coded && !a.absmax)) return QOPT_EINVAL;
+    if (!aligned(a.src, size_of(grad_dtype)) || !aligned(a.dst, size_of(param_dtype)) || !aligned(a.moment, coded ? 1 : 4) ||
+        !aligned(a.absmax, 4))
+      return QOPT_EALIGN;
+    const double r = static_cast<double>(a.rows), c = static_cast<double>(a.cols);
+    const double shape = hp->adjust == QOPT_MUON_ORIGINAL ? std::sqrt(std::max(1.0, r / c)) : 0.2 * std::sqrt(std::max(r, c));
+    a.rate = static_cast<float>(static_cast<double>(hp->lr) * shape);
+  }
+  if (!aligned(grad_scale, 4)) return QOPT_EALIGN;
+  if (all.empty()) return QOPT_OK;
+  if (coded && !cb) return QOPT_EINVAL;
+  if (!aligned(cb, 16) || !aligned(workspace, 256)) return QOPT_EALIGN;
+  if (!workspace || workspace_bytes < static_cast<size_t>(workspace_of(all))) return QOPT_EINVAL;
+  Run r = {};
+  r.source = coded ? kMomentum8 : kMomentum32;
+  r.src_dtype = grad_dtype;
+  r.dst_dtype = param_dtype;
+  r.update = true;
+  r.cb = cb;
+  r.grad_scale = grad_scale;
+  r.mu = hp->momentum;
+  r.omu = 1.0f - hp->momentum;
+  r.eps = hp->eps;
+  r.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * static_cast<double>(hp->weight_decay));
+  r.nesterov = hp->nesterov;
+  r.steps = hp->steps;
+  r.stream = static_cast<hipStream_t>(stream);
+  return run_all(all, r, workspace);
+}
+
+// Nothing thrown on the way (a list that finds no memory) leaves a C entry point.
+template <typename F> int guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return QOPT_EINTERNAL;
+  }
+}
+
+// A batch's matrices in lots that bound the list made for them.
+constexpr int64_t kMaxMatrices = int64_t{1} << 20;
+
+}  // namespace
+
+// ------------------------------------------------------------------ entry points
+
+extern "C" int qopt_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes || batch < 0 || batch > kMaxMatrices || bad_dim(rows) || bad_dim(cols)) return QOPT_EINVAL;
+  *bytes = 0;
+  if (batch == 0 || rows == 0 || cols == 0) return QOPT_OK;
+  return guarded([&] {
+    // the first batch is the largest
+    std::vector<Matrix> all(static_cast<size_t>(std::min<int64_t>(batch, kMaxBatch)), matrix_of(rows, cols));
+    *bytes = static_cast<size_t>(workspace_of(all));
+    return static_cast<int>(QOPT_OK);
+  });
+}
+
+extern "C" int qopt_orthogonalize(const void* x_dev, int dtype, int64_t batch, int64_t rows, int64_t cols, int steps, float eps,
+                                  void* out_dev, int out_dtype, void* workspace_dev, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  const int rc = qopt_orthogonalize_workspace(batch, rows, cols, &need);
+  if (rc != QOPT_OK) return rc;
+  if (bad_steps(steps) || bad_eps(eps)) return QOPT_EINVAL;
+  if (bad_dtype(dtype) || bad_dtype(out_dtype)) return QOPT_EUNSUPPORTED;
+  if (batch == 0 || rows == 0 || cols == 0) return QOPT_OK;
+  if (!x_dev || !out_dev || !workspace_dev || workspace_bytes < need) return QOPT_EINVAL;
+  if (!aligned(x_dev, size_of(dtype)) || !aligned(out_dev, size_of(out_dtype)) || !aligned(workspace_dev, 256)) return QOPT_EALIGN;
+  return guarded([&] {
+    std::vector<Matrix> all(static_cast<size_t>(batch), matrix_of(rows, cols));
+    for (int64_t i = 0; i < batch; ++i) {
+      all[i].src = static_cast<const uint8_t*>(x_dev) + i * rows * cols * static_cast<int64_t>(size_of(dtype));
+      all[i].dst = static_cast<uint8_t*>(out_dev) + i * rows * cols * static_cast<int64_t>(size_of(out_dtype));
+    }
+    Run r = {};
+    r.source = kPlain;
+    r.src_dtype = dtype;
+    r.dst_dtype = out_dtype;
+    r.eps = eps;
+    r.steps = steps;
+    r.stream = static_cast<hipStream_t>(stream);
+    return run_all(all, r, workspace_dev);
+  });
+}
+
+extern "C" int qopt_muon_workspace(const qopt_muon_tensor* tensors, int32_t ntensors, size_t* bytes) {
+  if (!bytes) return QOPT_EINVAL;
+  *bytes = 0;
+  return guarded([&] {
+    std::vector<Matrix> all;
+    const int rc = collect(tensors, ntensors, all);
+    if (rc == QOPT_OK) *bytes = static_cast<size_t>(workspace_of(all));
+    return rc;
+  });
+}
+
+extern "C" int qopt_muon8bit_step(const qopt_muon_tensor* tensors, int32_t ntensors, int param_dtype, int grad_dtype,
+                                  const qopt_codebook* cb_m_dev, const qopt_muon_hparams* hp, const float* grad_scale_dev,
+                                  void* workspace_dev, size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return muon_step(tensors, ntensors, param_dtype, grad_dtype, true, cb_m_dev, hp, grad_scale_dev, workspace_dev, workspace_bytes,
+                     stream);
+  });
+}
+
+extern "C" int qopt_muon32bit_step(const qopt_muon_tensor* tensors, int32_t ntensors, int param_dtype, int grad_dtype,
+                                   const qopt_muon_hparams* hp, const float* grad_scale_dev, void* workspace_dev,
+                                   size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return muon_step(tensors, ntensors, param_dtype, grad_dtype, false, nullptr, hp, grad_scale_dev, workspace_dev, workspace_bytes,
+                     stream);
+  });
+}
