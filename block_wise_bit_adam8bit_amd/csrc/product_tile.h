@@ -157,15 +157,18 @@ template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> stru
         });
       });
     };
-    // The order of a half step's instructions: LDS reads and loads between the matrix instructions.
+    // The order of a half step's instructions: LDS reads between the first matrix instructions, two at a time,
+    // loads between the ones that follow.  (The compiler takes the reads and the loads, which write LDS, in
+    // their order; a pattern that mixes them is dropped as a whole, and all of them come before the second
+    // matrix instruction: ...)
     constexpr int kMatrix = kFm * kFn * Op::kTerms, kReads = 2 * (kFm + kFn), kMemory = kLoads + Op::kSideLoads;
-    constexpr int kReadsEach = (2 * kReads + kMatrix - 1) / kMatrix, kMemoryEach = (kMemory + kMatrix - 1) / kMatrix;
+    constexpr int kReadGaps = (kReads + 1) / 2, kLoadsEach = (kMemory + kMatrix - kReadGaps - 1) / (kMatrix - kReadGaps);
     auto spread = [&](bool loads) {
 #pragma unroll
       for (int i = 0; i < kMatrix; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (i * kReadsEach < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kReadsEach, 0);
-        if (loads && i * kMemoryEach < kMemory) __builtin_amdgcn_sched_group_barrier(0x010, kMemoryEach, 0);
+        if (i < kReadGaps) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        else if (loads && (i - kReadGaps) * kLoadsEach < kMemory) __builtin_amdgcn_sched_group_barrier(0x010, kLoadsEach, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
