@@ -571,7 +571,7 @@ struct Launch {
   }
   int run(hipStream_t s) {
     const int64_t small = count(128), large = count(256);
-    const bool big = static_cast<double>(ceil_div(large, 256)) * 3.6 <= static_cast<double>(ceil_div(small, 256));
+    const bool big = static_cast<double>(ceil_div(large, 256)) * 2.9 <= static_cast<double>(ceil_div(small, 256));
     const unsigned tiles = static_cast<unsigned>(big ? count(256) : count(128));
     return big ? pick<true>(tiles, s) : pick<false>(tiles, s);
   }

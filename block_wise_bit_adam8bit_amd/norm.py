@@ -9,6 +9,7 @@ stream.
 
 import ctypes
 import math
+from functools import lru_cache
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -53,27 +54,35 @@ def _eps(eps):
     return eps
 
 
+@lru_cache(maxsize=1024)
+def _room(rows, dim):
+    """Bytes of the backward pass's workspace."""
+    need = ctypes.c_size_t(0)
+    _lib.check("qopt_layer_norm_backward_workspace",
+               LIB.qopt_layer_norm_backward_workspace(rows, dim, ctypes.byref(need)))
+    return need.value
+
+
+# The launches behind the functions below, for operands that are known to be right; mean and rstd as addresses.
+
 def _forward(x, dx, rows, dim, ldx, weight, bias, dw, eps, out, ldo, mean, rstd):
     if rows and dim:
         _lib.call("qopt_layer_norm_forward", x.device, x.data_ptr(), dx, rows, dim, ldx, _ptr(weight),
-                  _ptr(bias), dw, eps, out.data_ptr(), ldo, _ptr(mean), _ptr(rstd))
+                  _ptr(bias), dw, eps, out.data_ptr(), ldo, mean, rstd)
 
 
 def _backward(x, dx, rows, dim, ldx, weight, dw, mean, rstd, dout, lddo, need_x, need_w, need_b, w_dtype):
     dev = x.device
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev) if need_x else None
+    gx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_x else None
     gw = torch.empty(dim, dtype=w_dtype, device=dev) if need_w else None
     gb = torch.empty(dim, dtype=w_dtype, device=dev) if need_b else None
     ws, size = None, 0
     if need_w or need_b:
-        need = ctypes.c_size_t(0)
-        _lib.check("qopt_layer_norm_backward_workspace",
-                   LIB.qopt_layer_norm_backward_workspace(rows, dim, ctypes.byref(need)))
-        size = need.value
+        size = _room(rows, dim)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
     if dim:
         _lib.call("qopt_layer_norm_backward", dev, x.data_ptr(), dx, rows, dim, ldx, _ptr(weight), dw,
-                  mean.data_ptr(), rstd.data_ptr(), dout.data_ptr(), lddo, _ptr(gx), dim, _ptr(gw), _ptr(gb),
+                  mean, rstd, dout.data_ptr(), lddo, _ptr(gx), dim, _ptr(gw), _ptr(gb),
                   ws.data_ptr() if size else None, size)
     return gx, gw, gb
 
@@ -96,7 +105,7 @@ def qopt_layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, save_stats=T
     mean = rstd = None
     if save_stats:
         mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=dev)
-    _forward(x, dx, rows, dim, ldx, weight, bias, dw, eps, out, ldo, mean, rstd)
+    _forward(x, dx, rows, dim, ldx, weight, bias, dw, eps, out, ldo, _ptr(mean), _ptr(rstd))
     return out, mean, rstd
 
 
@@ -121,19 +130,20 @@ def qopt_layer_norm_backward(x, weight, mean, rstd, dout, *, need_x=True, need_w
             raise ValueError("mean and rstd must be contiguous float32, one value per row")
     _same_gpu(*(t for t in (x, weight, mean, rstd, dout) if t is not None))
     lddo = _check_rows(dout, "dout")[2]
-    return _backward(x, dx, rows, dim, ldx, weight, dw, mean, rstd, dout, lddo, need_x, need_weight, need_bias,
-                     weight_dtype)
+    return _backward(x, dx, rows, dim, ldx, weight, dw, mean.data_ptr(), rstd.data_ptr(), dout, lddo, need_x,
+                     need_weight, need_bias, weight_dtype)
 
 
 def _check_layer(x, weight, bias):
     _check_dtype(x.dtype, "x")
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
+    wanted = x.shape[-1:]
     for t, what in ((bias, "bias"), (weight, "weight")):
         if t is not None:
             _check_dtype(t.dtype, what)
-            if t.shape != x.shape[-1:]:
-                raise ValueError(f"{what} must be [{x.shape[-1]}]")
+            if t.shape != wanted:
+                raise ValueError(f"{what} must be [{wanted[0]}]")
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError("weight and bias must have the same dtype")
     _same_gpu(*(t for t in (x, weight, bias) if t is not None))
@@ -146,16 +156,15 @@ class LayerNormFunction(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps):
         _check_layer(x, weight, bias)
         eps = _eps(eps)
-        x = x.contiguous()
-        weight = None if weight is None else weight.contiguous()
-        bias = None if bias is None else bias.contiguous()
+        x, weight, bias = (t if t is None or t.is_contiguous() else t.contiguous() for t in (x, weight, bias))
         dim = int(x.shape[-1])
         rows = math.prod(int(d) for d in x.shape[:-1])  # tensors, in a trace
         some = weight if weight is not None else bias
         dw = QOPT_F32 if some is None else _DT[some.dtype]
         y = torch.empty_like(x)
         stats = torch.empty(2, rows, dtype=torch.float32, device=x.device)
-        _forward(x, _DT[x.dtype], rows, dim, dim, weight, bias, dw, eps, y, dim, stats[0], stats[1])
+        _forward(x, _DT[x.dtype], rows, dim, dim, weight, bias, dw, eps, y, dim,
+                 stats.data_ptr(), stats.data_ptr() + 4 * rows)
         ctx.w_dtype = torch.float32 if some is None else some.dtype
         ctx.rows = rows
         ctx.save_for_backward(x, weight, stats)
@@ -173,8 +182,8 @@ class LayerNormFunction(torch.autograd.Function):
         dout = dout.contiguous()
         if dout.dtype != x.dtype:
             dout = dout.to(x.dtype)
-        gx, gw, gb = _backward(x, _DT[x.dtype], ctx.rows, dim, dim, weight, _DT[ctx.w_dtype], stats[0], stats[1],
-                               dout, dim, need[0], need[1], need[2], ctx.w_dtype)
+        gx, gw, gb = _backward(x, _DT[x.dtype], ctx.rows, dim, dim, weight, _DT[ctx.w_dtype], stats.data_ptr(),
+                               stats.data_ptr() + 4 * ctx.rows, dout, dim, need[0], need[1], need[2], ctx.w_dtype)
         return gx, gw, gb, None
 
 
