@@ -7,12 +7,11 @@
 // and Q is applied to X at its end; every product but that one is symmetric, so that only the tiles on and
 // below the diagonal are computed, each stored with its mirror image.  For n / m = r a group of L iterations
 // takes (in products of m x m matrices) r / 2 + L / 2 + (L - 1) / 2 + (L - 1) + r, where the iterations by
-// themselves take L (3 r / 2 + 1 / 2): for five iterations as 3 + 2, 3 r + 7 against 7.5 r + 2.5, the same
-// for square matrices and less than half for r = 8.
-// Groups are at most three long, because a singular value s of X stands in A as s^2: what rounding adds to a
-// small one grows by a^2 = 11.9 per iteration on A, a fresh A = X X^T brings it back.  (With rounding to 22
-// bits: three and two iterations are as exact as one at a time on every matrix tried, 4e-7 for normal
-// entries, 5e-6 with eight directions 170 times the rest; four in one group end in infinities there.)
+// themselves take L (3 r / 2 + 1 / 2): for five iterations as 3 + 2, 3 r + 7, as 2 + 2 + 1, 4.5 r + 5.5, against
+// 7.5 r + 2.5: the same for square matrices and less than half for r = 8.
+// Groups are at most three long (`group_steps`), because a singular value s of X stands in A as s^2: what rounding
+// adds to a small one grows by a^2 = 11.9 per iteration on A, a fresh A = X X^T brings it back.  (With rounding to 22
+// bits four in one group end in infinities where eight directions are 170 times the rest.)
 //
 // Numbers.  A value is kept as hi + lo, two binary16 numbers, times a power of two that keeps the largest
 // possible value (|X| <= 1.203, A <= 1.45, P <= 3.4445, Q <= 3.4445^3) under 65504; hi hi + hi lo + lo hi
@@ -36,9 +35,9 @@ using namespace product;
 using blockwise::BlockScale;
 using blockwise::Encoder;
 
-constexpr float kA = 3.4445f, kB = -4.775f, kC = 2.0315f;
+constexpr double kExactA = 3.4445, kExactB = -4.775, kExactC = 2.0315;
+constexpr float kA = kExactA, kB = kExactB, kC = kExactC;
 constexpr int kExp = 12, kExpQ = 10;  // powers of two of X, A, P and P A, and of a product Q
-constexpr int kGroupSteps = 3;        // iterations on A before it is made anew
 constexpr int kMaxJobs = 32;          // of one launch (its arguments are 4 KB at most)
 constexpr int kMaxParts = 512;        // partial sums of squares per matrix
 
@@ -634,6 +633,12 @@ template <bool kSplit> __global__ void __launch_bounds__(256, 1) chain_kernel(Ch
           a[f][e] = *reinterpret_cast<const i32x4*>(image[bl] + 64 * wm * kStepBytes + at);
           b[f][e] = *reinterpret_cast<const i32x4*>(image[br] + 64 * wn * kStepBytes + at);
         }
+      // lo lo too: small matrices are where it shows
+      if constexpr (kSplit)
+        each_pair<2, 2>([&](auto i, auto j) {
+          constexpr int I = decltype(i)::value, J = decltype(j)::value;
+          x[I][J] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b[J][1]), __builtin_bit_cast(f16x8, a[I][1]), x[I][J], 0, 0, 0);
+        });
       each<Op::kTerms>([&](auto term) {
         each_pair<2, 2>([&](auto i, auto j) {
           constexpr int I = decltype(i)::value, J = decltype(j)::value;
@@ -710,6 +715,158 @@ template <bool kSplit> __global__ void __launch_bounds__(256, 1) chain_kernel(Ch
   });
 }
 
+// ------------------------------------------------------------------ matrices of few rows or columns
+
+// Up to kTiny on the shorter side (an adapter's rank) the products with U are short sums and what would bound the
+// way above is its launches.  Here it takes three, in binary64, where five iterations on A need no fresh start:
+// A = U U^T, whose trace is the squared norm; the polynomial Q of A / |U|^2; and Q U / |U|.
+// 16 x 4096: 28 us of GPU time instead of 140 by single iterations, 1e-7 off instead of 8e-7.
+constexpr int kTiny = 32;
+constexpr int kTinyColumns = 256;  // of the longer side, per workgroup and turn
+constexpr int kTinyParts = 64;     // partial A per matrix
+
+struct TinyJob {
+  const void* u;
+  double *parts, *q;
+  void* dst;
+  int64_t n, along, across;  // element (i, c) of U's short rows lies at i * across + c * along
+  int32_t m;
+  uint32_t groups;
+  float rate;
+};
+struct TinyArgs {
+  TinyJob jobs[kMaxJobs];
+  double eps;
+  int steps;
+  float decay;
+};
+static_assert(sizeof(TinyArgs) <= 4096, "kernel arguments");
+
+// Columns c0 to c0 + 255 of U's short rows in LDS, 0 behind the end.
+template <typename ST> __device__ __forceinline__ void load_columns(const TinyJob& job, int64_t c0, float (*x)[kTinyColumns + 1]) {
+  const ST* u = static_cast<const ST*>(job.u);
+  const int all = job.m * kTinyColumns;
+  for (int i = threadIdx.x; i < all; i += 256) {
+    // the index that runs along memory first
+    const int row = job.along == 1 ? i / kTinyColumns : i % job.m, c = job.along == 1 ? i % kTinyColumns : i / job.m;
+    x[row][c] = c0 + c < job.n ? to_f32(u[row * job.across + (c0 + c) * job.along]) : 0.0f;
+  }
+}
+
+// A thread holds A[i][j] for i = 2 ti, 2 ti + 1 and j likewise.
+template <typename ST> __global__ void __launch_bounds__(256) tiny_gram_kernel(TinyArgs a) {
+  __shared__ float x[kTiny][kTinyColumns + 1];
+  const TinyJob& job = a.jobs[blockIdx.y];
+  if (blockIdx.x >= job.groups) return;
+  const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
+  double s[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTinyColumns; c0 < job.n; c0 += static_cast<int64_t>(job.groups) * kTinyColumns) {
+    load_columns<ST>(job, c0, x);
+    __syncthreads();
+    if (2 * ti < job.m && 2 * tj < job.m) {  // rows from m on hold anything, and make sums that nobody reads
+      const int most = job.n - c0 < kTinyColumns ? static_cast<int>(job.n - c0) : kTinyColumns;
+      for (int c = 0; c < most; ++c) {
+        const double l0 = x[2 * ti][c], l1 = x[2 * ti + 1][c], r0 = x[2 * tj][c], r1 = x[2 * tj + 1][c];
+        s[0][0] += l0 * r0;
+        s[0][1] += l0 * r1;
+        s[1][0] += l1 * r0;
+        s[1][1] += l1 * r1;
+      }
+    }
+    __syncthreads();
+  }
+  double* to = job.parts + static_cast<int64_t>(blockIdx.x) * job.m * job.m;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (2 * ti + i < job.m && 2 * tj + j < job.m) to[(2 * ti + i) * job.m + 2 * tj + j] = s[i][j];
+}
+
+// Q = the product of a I + b A + c A^2 over the iterations, A = P A P after each, over |U|.
+__global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
+  typedef double Mat[kTiny][kTiny + 1];
+  __shared__ Mat a, p, q, h;
+  const TinyJob& job = args.jobs[blockIdx.x];
+  const int m = job.m, ti = threadIdx.x / 16, tj = threadIdx.x % 16;
+  auto own = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) f(2 * ti + i, 2 * tj + j, 2 * i + j);
+  };
+  auto product = [&](const Mat& l, const Mat& r, double (&s)[4]) {  // r is symmetric
+    s[0] = s[1] = s[2] = s[3] = 0.0;
+    if (2 * ti >= m || 2 * tj >= m) return;
+    for (int k = 0; k < m; ++k) {
+      const double l0 = l[2 * ti][k], l1 = l[2 * ti + 1][k], r0 = r[2 * tj][k], r1 = r[2 * tj + 1][k];
+      s[0] += l0 * r0;
+      s[1] += l0 * r1;
+      s[2] += l1 * r0;
+      s[3] += l1 * r1;
+    }
+  };
+  own([&](int i, int j, int) {
+    double s = 0.0;
+    if (i < m && j < m)
+      for (uint32_t g = 0; g < job.groups; ++g) s += job.parts[(static_cast<int64_t>(g) * m + i) * m + j];
+    a[i][j] = s;
+  });
+  __syncthreads();
+  double trace = 0.0;
+  for (int i = 0; i < m; ++i) trace += a[i][i];
+  __syncthreads();
+  const double norm = sqrt(trace), size = norm < args.eps ? args.eps : norm;
+  own([&](int i, int j, int) { a[i][j] = a[i][j] / size / size; });
+  __syncthreads();
+  for (int it = 0; it < args.steps; ++it) {
+    double s[4];
+    product(a, a, s);
+    own([&](int i, int j, int e) {
+      p[i][j] = s[e] * kExactC + a[i][j] * kExactB + (i == j ? kExactA : 0.0);
+    });
+    __syncthreads();
+    if (it == 0) own([&](int i, int j, int e) { s[e] = p[i][j]; });
+    else product(p, q, s);
+    __syncthreads();
+    own([&](int i, int j, int e) { q[i][j] = s[e]; });
+    if (it + 1 < args.steps) {
+      product(p, a, s);
+      own([&](int i, int j, int e) { h[i][j] = s[e]; });
+      __syncthreads();
+      product(h, p, s);
+      own([&](int i, int j, int e) { a[i][j] = s[e]; });
+    }
+    __syncthreads();
+  }
+  const bool fine = trace - trace == 0.0;  // neither an infinity nor a NaN
+  own([&](int i, int j, int) {
+    if (i < m && j < m) job.q[i * m + j] = fine ? q[i][j] / size : __builtin_nan("");
+  });
+}
+
+// dst = Q U, or dst * decay - Q U * rate: a thread per column of U's short rows.
+template <typename ST, typename OT, bool kStep> __global__ void __launch_bounds__(256) tiny_result_kernel(TinyArgs a) {
+  __shared__ float x[kTiny][kTinyColumns + 1];
+  __shared__ double q[kTiny][kTiny];
+  const TinyJob& job = a.jobs[blockIdx.y];
+  if (blockIdx.x >= job.groups) return;
+  for (int i = threadIdx.x; i < job.m * job.m; i += 256) q[i / job.m][i % job.m] = job.q[i];
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTinyColumns; c0 < job.n; c0 += static_cast<int64_t>(job.groups) * kTinyColumns) {
+    load_columns<ST>(job, c0, x);
+    __syncthreads();
+    const int64_t c = c0 + threadIdx.x;
+    for (int i = 0; c < job.n && i < job.m; ++i) {
+      double s = 0.0;
+      for (int k = 0; k < job.m; ++k) s += q[i][k] * static_cast<double>(x[k][threadIdx.x]);
+      OT* to = static_cast<OT*>(job.dst) + i * job.across + c * job.along;
+      const float o = static_cast<float>(s);
+      store1(to, kStep ? to_f32(*to) * a.decay - o * job.rate : o);
+    }
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------ host
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -730,6 +887,7 @@ struct Matrix {
   double* parts;
   uint32_t groups;
   uint8_t *x, *xt[2], *g, *p, *h, *q[2];
+  double *tiny_parts, *tiny_q;
 };
 
 int64_t up(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
@@ -742,6 +900,12 @@ uint8_t* lay_out(Matrix& a, uint8_t* at) {
     return p;
   };
   a.parts = reinterpret_cast<double*>(take(kMaxParts * 8));
+  if (a.m <= kTiny) {
+    a.u = reinterpret_cast<float*>(take(a.rows * a.cols * 4));
+    a.tiny_parts = reinterpret_cast<double*>(take(kTinyParts * a.m * a.m * 8));
+    a.tiny_q = reinterpret_cast<double*>(take(a.m * a.m * 8));
+    return at;
+  }
   a.x = take(a.m * row_bytes(a.n, true));
   a.xt[0] = take(a.n * row_bytes(a.m, true));
   a.xt[1] = take(a.n * row_bytes(a.m, true));
@@ -750,16 +914,27 @@ uint8_t* lay_out(Matrix& a, uint8_t* at) {
   return at;
 }
 
+// Iterations on A before it is made anew: fewer where rounding shows in a binary32 destination.  Groups of three, of
+// two and single iterations end (1e-6 of the result; products in binary32 in brackets) 3.7, 1.2 and 0.8 off for 17 x
+// 23 (0.7), 3.4, 1.5 and 0.9 for 64 x 64 (1.0), 5.9, 1.5 and 1.5 for 99 x 300 (1.4), 2.0, 1.4 and 1.1 for 300 x 1000 (1.6),
+// 2.2, 1.6 and 1.9 for 1024 x 1024 (2.6).
+int group_steps(int64_t m, int dst_dtype) { return dst_dtype != QOPT_F32 || m > 768 ? 3 : m > 48 ? 2 : 1; }
+// Matrices that a batch may hold together.
+bool alike(int64_t m, int64_t other, int dst_dtype) {
+  return (m <= kTiny) == (other <= kTiny) && (m <= kTiny || group_steps(m, dst_dtype) == group_steps(other, dst_dtype));
+}
+
 int64_t tiles_of(int64_t m, int64_t side) { return ceil_div(m, side); }
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
-// Matrices whose products share their launches, in the order of their m: at most 32, of which 16 that take their
+// Matrices whose products share their launches, in the order of their m and of one length of groups: at most 32, of which 16 that take their
 // products in launches of their own (two jobs each), until their symmetric products fill the chip twice.
 constexpr size_t kMaxBatch = kMaxJobs, kMaxLarge = kMaxJobs / 2;
-size_t batch_end(const std::vector<Matrix>& all, size_t first) {
+size_t batch_end(const std::vector<Matrix>& all, size_t first, int dst_dtype) {
   int64_t tiles = 0;
   size_t i = first, large = 0;
-  while (i < all.size() && i - first < kMaxBatch && large < kMaxLarge && tiles < 512) {
+  while (i < all.size() && i - first < kMaxBatch && large < kMaxLarge && tiles < 512 &&
+         alike(all[i].m, all[first].m, dst_dtype)) {
     if (all[i].m > kChainDim) ++large;
     tiles += triangle(tiles_of(all[i].m, 256));
     ++i;
@@ -932,40 +1107,79 @@ int64_t parts_of(const Matrix* mats, int count) {
   return most;
 }
 
-int64_t workspace_of(std::vector<Matrix>& all) {
+int64_t workspace_of(std::vector<Matrix>& all, int dst_dtype) {
   int64_t most = 0;
   for (size_t first = 0; first < all.size();) {
-    const size_t end = batch_end(all, first);
+    const size_t end = batch_end(all, first, dst_dtype);
     uint8_t* at = nullptr;
     for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
-    most = std::max<int64_t>(most, reinterpret_cast<intptr_t>(at) + parts_of(all.data() + first, static_cast<int>(end - first)));
+    const int64_t parts = all[first].m <= kTiny ? 0 : parts_of(all.data() + first, static_cast<int>(end - first));
+    most = std::max<int64_t>(most, reinterpret_cast<intptr_t>(at) + parts);
     first = end;
   }
   return most;
 }
+// Whatever the destination's type.
+int64_t workspace_of(std::vector<Matrix>& all) { return std::max(workspace_of(all, QOPT_F32), workspace_of(all, QOPT_BF16)); }
+
+int run_source(Matrix* mats, int count, const Run& r) {
+  SourceArgs a = {};
+  a.cb = r.cb;
+  a.grad_scale = r.grad_scale;
+  a.mu = r.mu;
+  a.omu = r.omu;
+  a.nesterov = r.nesterov;
+  uint32_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    Matrix& m = mats[i];
+    const int64_t n = m.rows * m.cols;
+    m.groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(n, QOPT_BLOCK), kMaxParts));
+    most = std::max(most, m.groups);
+    a.jobs[i] = {m.src, m.moment, m.absmax, m.u, m.parts, n, m.groups};
+  }
+  const dim3 grid(most, static_cast<unsigned>(count));
+  if (r.src_dtype == QOPT_F32) launch_source<float>(a, r.source, grid, r.stream);
+  else launch_source<uint16_t>(a, r.source, grid, r.stream);
+  return launch_status();
+}
+
+template <typename ST, typename OT> void launch_tiny_result(const TinyArgs& a, bool step, dim3 grid, hipStream_t s) {
+  if (step) hipLaunchKernelGGL((tiny_result_kernel<ST, OT, true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((tiny_result_kernel<ST, OT, false>), grid, dim3(256), 0, s, a);
+}
+
+int run_tiny(Matrix* mats, int count, const Run& r) {
+  if (r.source != kPlain && run_source(mats, count, r) != QOPT_OK) return QOPT_ELAUNCH;
+  TinyArgs a = {};
+  a.eps = static_cast<double>(r.eps);
+  a.steps = r.steps;
+  a.decay = r.decay;
+  uint32_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    const Matrix& m = mats[i];
+    const bool tall = m.rows > m.cols;
+    const uint32_t groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(m.n, kTinyColumns), kTinyParts));
+    most = std::max(most, groups);
+    a.jobs[i] = {r.source == kPlain ? m.src : m.u, m.tiny_parts, m.tiny_q, m.dst, m.n, tall ? m.cols : 1, tall ? 1 : m.cols,
+                 static_cast<int32_t>(m.m), groups, m.rate};
+  }
+  const dim3 grid(most, static_cast<unsigned>(count));
+  hipStream_t s = r.stream;
+  const bool half = r.source == kPlain && r.src_dtype == QOPT_BF16;
+  if (half) hipLaunchKernelGGL(tiny_gram_kernel<uint16_t>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(tiny_gram_kernel<float>, grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL(tiny_polynomial_kernel, dim3(static_cast<unsigned>(count)), dim3(256), 0, s, a);
+  if (half && r.dst_dtype == QOPT_F32) launch_tiny_result<uint16_t, float>(a, r.update, grid, s);
+  else if (half) launch_tiny_result<uint16_t, uint16_t>(a, r.update, grid, s);
+  else if (r.dst_dtype == QOPT_F32) launch_tiny_result<float, float>(a, r.update, grid, s);
+  else launch_tiny_result<float, uint16_t>(a, r.update, grid, s);
+  return launch_status();
+}
 
 int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
+  if (mats[0].m <= kTiny) return run_tiny(mats, count, r);
   hipStream_t s = r.stream;
-  {
-    SourceArgs a = {};
-    a.cb = r.cb;
-    a.grad_scale = r.grad_scale;
-    a.mu = r.mu;
-    a.omu = r.omu;
-    a.nesterov = r.nesterov;
-    uint32_t most = 0;
-    for (int i = 0; i < count; ++i) {
-      Matrix& m = mats[i];
-      const int64_t n = m.rows * m.cols;
-      m.groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(n, QOPT_BLOCK), kMaxParts));
-      most = std::max(most, m.groups);
-      a.jobs[i] = {m.src, m.moment, m.absmax, m.u, m.parts, n, m.groups};
-    }
-    const dim3 grid(most, static_cast<unsigned>(count));
-    if (r.src_dtype == QOPT_F32) launch_source<float>(a, r.source, grid, s);
-    else launch_source<uint16_t>(a, r.source, grid, s);
-    if (launch_status() != QOPT_OK) return QOPT_ELAUNCH;
-  }
+  if (run_source(mats, count, r) != QOPT_OK) return QOPT_ELAUNCH;
   {
     PackArgs a = {};
     a.njobs = count;
@@ -993,7 +1207,7 @@ int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
   };
   int rc = QOPT_OK, turn = 0;  // xt[turn] is current
   for (int done = 0; done < r.steps && rc == QOPT_OK;) {
-    const int length = std::min(kGroupSteps, r.steps - done);
+    const int length = std::min(group_steps(mats[0].m, r.dst_dtype), r.steps - done);
     auto is_split = [&](int from) {  // whether the group that begins there keeps 22 bits
       return r.dst_dtype == QOPT_F32 || from == 0 || r.steps - from > 2;
     };
@@ -1076,7 +1290,7 @@ int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
 
 int run_all(std::vector<Matrix>& all, const Run& r, void* workspace) {
   for (size_t first = 0; first < all.size();) {
-    const size_t end = batch_end(all, first);
+    const size_t end = batch_end(all, first, r.dst_dtype);
     uint8_t* at = static_cast<uint8_t*>(workspace);
     for (size_t i = first; i < end; ++i) at = lay_out(all[i], at);
     const int rc = run_batch(all.data() + first, static_cast<int>(end - first), at, r);
