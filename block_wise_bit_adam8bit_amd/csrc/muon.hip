@@ -720,10 +720,9 @@ template <bool kSplit> __global__ void __launch_bounds__(256, 1) chain_kernel(Ch
 // Up to kTiny on the shorter side (an adapter's rank) the products with U are short sums and what would bound the
 // way above is its launches.  Here it takes three, in binary64, where five iterations on A need no fresh start:
 // A = U U^T, whose trace is the squared norm; the polynomial Q of A / |U|^2; and Q U / |U|.
-// 16 x 4096: 28 us of GPU time instead of 140 by single iterations, 1e-7 off instead of 8e-7.
 constexpr int kTiny = 32;
-constexpr int kTinyColumns = 256;  // of the longer side, per workgroup and turn
-constexpr int kTinyParts = 64;     // partial A per matrix
+constexpr int kGramColumns = 64, kResultColumns = 256;  // of the longer side, per workgroup and turn
+constexpr int kTinyParts = 128;                         // partial A per matrix
 
 struct TinyJob {
   const void* u;
@@ -731,7 +730,7 @@ struct TinyJob {
   void* dst;
   int64_t n, along, across;  // element (i, c) of U's short rows lies at i * across + c * along
   int32_t m;
-  uint32_t groups;
+  uint32_t groups, result_groups;
   float rate;
 };
 struct TinyArgs {
@@ -742,30 +741,31 @@ struct TinyArgs {
 };
 static_assert(sizeof(TinyArgs) <= 4096, "kernel arguments");
 
-// Columns c0 to c0 + 255 of U's short rows in LDS, 0 behind the end.
-template <typename ST> __device__ __forceinline__ void load_columns(const TinyJob& job, int64_t c0, float (*x)[kTinyColumns + 1]) {
+// Columns c0 to c0 + kColumns - 1 of U's short rows in LDS, 0 behind the end.
+template <typename ST, int kColumns> __device__ __forceinline__ void load_columns(const TinyJob& job, int64_t c0, float (*x)[kColumns + 1]) {
   const ST* u = static_cast<const ST*>(job.u);
-  const int all = job.m * kTinyColumns;
+  const int all = job.m * kColumns;
+#pragma unroll 4
   for (int i = threadIdx.x; i < all; i += 256) {
     // the index that runs along memory first
-    const int row = job.along == 1 ? i / kTinyColumns : i % job.m, c = job.along == 1 ? i % kTinyColumns : i / job.m;
+    const int row = job.along == 1 ? i / kColumns : i % job.m, c = job.along == 1 ? i % kColumns : i / job.m;
     x[row][c] = c0 + c < job.n ? to_f32(u[row * job.across + (c0 + c) * job.along]) : 0.0f;
   }
 }
 
 // A thread holds A[i][j] for i = 2 ti, 2 ti + 1 and j likewise.
 template <typename ST> __global__ void __launch_bounds__(256) tiny_gram_kernel(TinyArgs a) {
-  __shared__ float x[kTiny][kTinyColumns + 1];
+  __shared__ float x[kTiny][kGramColumns + 1];
   const TinyJob& job = a.jobs[blockIdx.y];
   if (blockIdx.x >= job.groups) return;
   const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
   double s[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
-  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTinyColumns; c0 < job.n; c0 += static_cast<int64_t>(job.groups) * kTinyColumns) {
-    load_columns<ST>(job, c0, x);
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kGramColumns; c0 < job.n; c0 += static_cast<int64_t>(job.groups) * kGramColumns) {
+    load_columns<ST, kGramColumns>(job, c0, x);
     __syncthreads();
     if (2 * ti < job.m && 2 * tj < job.m) {  // rows from m on hold anything, and make sums that nobody reads
-      const int most = job.n - c0 < kTinyColumns ? static_cast<int>(job.n - c0) : kTinyColumns;
-      for (int c = 0; c < most; ++c) {
+#pragma unroll 8
+      for (int c = 0; c < kGramColumns; ++c) {
         const double l0 = x[2 * ti][c], l1 = x[2 * ti + 1][c], r0 = x[2 * tj][c], r1 = x[2 * tj + 1][c];
         s[0][0] += l0 * r0;
         s[0][1] += l0 * r1;
@@ -798,18 +798,22 @@ __global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
   auto product = [&](const Mat& l, const Mat& r, double (&s)[4]) {  // r is symmetric
     s[0] = s[1] = s[2] = s[3] = 0.0;
     if (2 * ti >= m || 2 * tj >= m) return;
-    for (int k = 0; k < m; ++k) {
-      const double l0 = l[2 * ti][k], l1 = l[2 * ti + 1][k], r0 = r[2 * tj][k], r1 = r[2 * tj + 1][k];
-      s[0] += l0 * r0;
-      s[1] += l0 * r1;
-      s[2] += l1 * r0;
-      s[3] += l1 * r1;
-    }
+    for (int k0 = 0; k0 < m; k0 += 8)  // places from m on are 0 in the rows before it
+#pragma unroll
+      for (int k = k0; k < k0 + 8; ++k) {
+        const double l0 = l[2 * ti][k], l1 = l[2 * ti + 1][k], r0 = r[2 * tj][k], r1 = r[2 * tj + 1][k];
+        s[0] += l0 * r0;
+        s[1] += l0 * r1;
+        s[2] += l1 * r0;
+        s[3] += l1 * r1;
+      }
   };
   own([&](int i, int j, int) {
     double s = 0.0;
-    if (i < m && j < m)
+    if (i < m && j < m) {
+#pragma unroll 16
       for (uint32_t g = 0; g < job.groups; ++g) s += job.parts[(static_cast<int64_t>(g) * m + i) * m + j];
+    }
     a[i][j] = s;
   });
   __syncthreads();
@@ -822,9 +826,7 @@ __global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
   for (int it = 0; it < args.steps; ++it) {
     double s[4];
     product(a, a, s);
-    own([&](int i, int j, int e) {
-      p[i][j] = s[e] * kExactC + a[i][j] * kExactB + (i == j ? kExactA : 0.0);
-    });
+    own([&](int i, int j, int e) { p[i][j] = s[e] * kExactC + a[i][j] * kExactB + (i == j ? kExactA : 0.0); });
     __syncthreads();
     if (it == 0) own([&](int i, int j, int e) { s[e] = p[i][j]; });
     else product(p, q, s);
@@ -845,23 +847,35 @@ __global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
   });
 }
 
-// dst = Q U, or dst * decay - Q U * rate: a thread per column of U's short rows.
+// dst = Q U, or dst * decay - Q U * rate: a thread per column of U's short rows, eight results of it at a time.
 template <typename ST, typename OT, bool kStep> __global__ void __launch_bounds__(256) tiny_result_kernel(TinyArgs a) {
-  __shared__ float x[kTiny][kTinyColumns + 1];
-  __shared__ double q[kTiny][kTiny];
+  __shared__ float x[kTiny][kResultColumns + 1];
+  __shared__ __align__(16) double q[kTiny][kTiny];  // q[k][i]: Q is symmetric
   const TinyJob& job = a.jobs[blockIdx.y];
-  if (blockIdx.x >= job.groups) return;
-  for (int i = threadIdx.x; i < job.m * job.m; i += 256) q[i / job.m][i % job.m] = job.q[i];
-  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTinyColumns; c0 < job.n; c0 += static_cast<int64_t>(job.groups) * kTinyColumns) {
-    load_columns<ST>(job, c0, x);
+  if (blockIdx.x >= job.result_groups) return;
+  for (int i = threadIdx.x; i < kTiny * kTiny; i += 256) {
+    const int k = i / kTiny, c = i % kTiny;
+    q[k][c] = k < job.m && c < job.m ? job.q[k * job.m + c] : 0.0;
+  }
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kResultColumns; c0 < job.n; c0 += static_cast<int64_t>(job.result_groups) * kResultColumns) {
+    load_columns<ST, kResultColumns>(job, c0, x);
     __syncthreads();
     const int64_t c = c0 + threadIdx.x;
-    for (int i = 0; c < job.n && i < job.m; ++i) {
-      double s = 0.0;
-      for (int k = 0; k < job.m; ++k) s += q[i][k] * static_cast<double>(x[k][threadIdx.x]);
-      OT* to = static_cast<OT*>(job.dst) + i * job.across + c * job.along;
-      const float o = static_cast<float>(s);
-      store1(to, kStep ? to_f32(*to) * a.decay - o * job.rate : o);
+    for (int i0 = 0; c < job.n && i0 < job.m; i0 += 8) {
+      double s[8] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+      for (int k = 0; k < job.m; ++k) {
+        const double v = x[k][threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += q[k][i0 + i] * v;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < job.m) {
+          OT* to = static_cast<OT*>(job.dst) + (i0 + i) * job.across + c * job.along;
+          const float o = static_cast<float>(s[i]);
+          store1(to, kStep ? to_f32(*to) * a.decay - o * job.rate : o);
+        }
     }
     __syncthreads();
   }
@@ -1154,25 +1168,27 @@ int run_tiny(Matrix* mats, int count, const Run& r) {
   a.eps = static_cast<double>(r.eps);
   a.steps = r.steps;
   a.decay = r.decay;
-  uint32_t most = 0;
+  uint32_t most = 0, most_results = 0;
   for (int i = 0; i < count; ++i) {
     const Matrix& m = mats[i];
     const bool tall = m.rows > m.cols;
-    const uint32_t groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(m.n, kTinyColumns), kTinyParts));
+    const uint32_t groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(m.n, kGramColumns), kTinyParts));
+    const uint32_t results = static_cast<uint32_t>(ceil_div(m.n, kResultColumns));  // QOPT_MUON_MAX_DIM / 256 at most
     most = std::max(most, groups);
+    most_results = std::max(most_results, results);
     a.jobs[i] = {r.source == kPlain ? m.src : m.u, m.tiny_parts, m.tiny_q, m.dst, m.n, tall ? m.cols : 1, tall ? 1 : m.cols,
-                 static_cast<int32_t>(m.m), groups, m.rate};
+                 static_cast<int32_t>(m.m), groups, results, m.rate};
   }
-  const dim3 grid(most, static_cast<unsigned>(count));
+  const dim3 grid(most, static_cast<unsigned>(count)), wide(most_results, static_cast<unsigned>(count));
   hipStream_t s = r.stream;
   const bool half = r.source == kPlain && r.src_dtype == QOPT_BF16;
   if (half) hipLaunchKernelGGL(tiny_gram_kernel<uint16_t>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(tiny_gram_kernel<float>, grid, dim3(256), 0, s, a);
   hipLaunchKernelGGL(tiny_polynomial_kernel, dim3(static_cast<unsigned>(count)), dim3(256), 0, s, a);
-  if (half && r.dst_dtype == QOPT_F32) launch_tiny_result<uint16_t, float>(a, r.update, grid, s);
-  else if (half) launch_tiny_result<uint16_t, uint16_t>(a, r.update, grid, s);
-  else if (r.dst_dtype == QOPT_F32) launch_tiny_result<float, float>(a, r.update, grid, s);
-  else launch_tiny_result<float, uint16_t>(a, r.update, grid, s);
+  if (half && r.dst_dtype == QOPT_F32) launch_tiny_result<uint16_t, float>(a, r.update, wide, s);
+  else if (half) launch_tiny_result<uint16_t, uint16_t>(a, r.update, wide, s);
+  else if (r.dst_dtype == QOPT_F32) launch_tiny_result<float, float>(a, r.update, wide, s);
+  else launch_tiny_result<float, uint16_t>(a, r.update, wide, s);
   return launch_status();
 }
 
