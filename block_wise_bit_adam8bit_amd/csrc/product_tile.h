@@ -1,5 +1,5 @@
 // One tile of a matrix product a b^T on gfx950's matrix units, for operands whose rows are runs of
-// 128-byte steps along the sum: what 256 4-bit values, 64 16-bit values, or 32 values in two 16-bit
+// 128-byte steps along the sum: what 256 4-bit values, 64 16-bit values, or 32 values in several
 // parts take.  What a step's bytes mean is the business of an `Op`.
 #ifndef QOPT_PRODUCT_TILE_H
 #define QOPT_PRODUCT_TILE_H
@@ -84,7 +84,8 @@ struct Rows {
 // acc[i][j][4 q + e] of lane (r, h) is row kFm r + i, column kFn (8 q + 4 h + e) + j of the wave's part.
 //
 // Op: `Side` (what comes with a step's codes: scales), load(t), kSideLoads (memory instructions of a load),
-// touch(side), kTerms and multiply<half, term, i, j>(acc, a, b, side), a and b the two pieces of a fragment.
+// touch(side), terms(half) and multiply<half, term, i, j>(acc, a, b, side), a and b the two pieces of a fragment.
+// kCross: in half 1 lane (r, h) takes the pieces of b that (r, 1 - h) would.
 template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> struct Tile {
   static constexpr int kWaves = kWavesM * kWavesN, kThreads = kWaves * kWave;
   static constexpr int kWm = kM / kWavesM, kWn = kN / kWavesN;  // a wave's part of the tile
@@ -136,7 +137,7 @@ template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> stru
     };
     auto read_half = [&](Frags& f, int buf, int half) {
       asm volatile("" : "+v"(oa), "+v"(ob));  // addresses are made anew, not kept in registers
-      const uint32_t a0 = (oa ^ (half * 32)) + buf * (kRows * kStepBytes), b0 = (ob ^ (half * 32)) + buf * (kRows * kStepBytes);
+      const uint32_t a0 = (oa ^ (half * 32)) + buf * (kRows * kStepBytes), b0 = (ob ^ (half * (Op::kCross ? 96 : 32))) + buf * (kRows * kStepBytes);
 #pragma unroll
       for (int j = 0; j < kFn; ++j) {
         f.b[j][0] = *reinterpret_cast<const i32x4*>(lds + b0 + j * (32 * kStepBytes));
@@ -150,25 +151,28 @@ template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> stru
     };
     auto multiply = [&](auto half, const Frags& f, const typename Op::Side& c) {
       // the terms one after the other, so that an accumulator's instructions do not follow each other at once
-      each<Op::kTerms>([&](auto term) {
+      each<Op::terms(decltype(half)::value)>([&](auto term) {
         each_pair<kFm, kFn>([&](auto i, auto j) {
           constexpr int I = decltype(i)::value, J = decltype(j)::value;
           Op::template multiply<decltype(half)::value, decltype(term)::value, I, J>(acc[I][J], f.a[I], f.b[J], c);
         });
       });
     };
-    // The order of a half step's instructions: LDS reads between the first matrix instructions, two at a time,
-    // loads between the ones that follow.  (The compiler takes the reads and the loads, which write LDS, in
-    // their order; a pattern that mixes them is dropped as a whole, and all of them come before the second
-    // matrix instruction: ...)
-    constexpr int kMatrix = kFm * kFn * Op::kTerms, kReads = 2 * (kFm + kFn), kMemory = kLoads + Op::kSideLoads;
-    constexpr int kReadGaps = (kReads + 1) / 2, kLoadsEach = (kMemory + kMatrix - kReadGaps - 1) / (kMatrix - kReadGaps);
-    auto spread = [&](bool loads) {
+    // The order of a half step's instructions: LDS reads between the matrix instructions of its first half,
+    // loads between the ones that follow.  (The compiler keeps the reads and the loads, which write LDS, in
+    // their order; a pattern that mixes them is dropped as a whole, and all of them then come before the second
+    // matrix instruction: 9 % slower over 4-bit operands, 265 and 239 us for 8192^3.)
+    constexpr int kReads = 2 * (kFm + kFn), kMemory = kLoads + Op::kSideLoads;
+    auto spread = [&](auto half) {
+      constexpr bool kLoading = decltype(half)::value == 1;
+      constexpr int kMatrix = kFm * kFn * Op::terms(decltype(half)::value);
+      constexpr int kReadsEach = (2 * kReads + kMatrix - 1) / kMatrix, kReadGaps = (kReads + kReadsEach - 1) / kReadsEach;
+      constexpr int kLoadsEach = (kMemory + kMatrix - kReadGaps - 1) / (kMatrix - kReadGaps);
 #pragma unroll
       for (int i = 0; i < kMatrix; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (i < kReadGaps) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        else if (loads && (i - kReadGaps) * kLoadsEach < kMemory) __builtin_amdgcn_sched_group_barrier(0x010, kLoadsEach, 0);
+        if (i < kReadGaps) __builtin_amdgcn_sched_group_barrier(0x100, kReadsEach, 0);
+        else if (kLoading && (i - kReadGaps) * kLoadsEach < kMemory) __builtin_amdgcn_sched_group_barrier(0x010, kLoadsEach, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -217,13 +221,13 @@ template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> stru
           c[(u + kLast) % kBufs] = op.load(upto_last(t + kLast));
           read_half(f1, u, 1);
           multiply(half0, f0, c[u]);
-          spread(false);
+          spread(half0);
           step_barrier();
           Op::touch(c[(u + 1) % kBufs]);
           read_half(f0, (u + 1) % kBufs, 0);
           load_step(u, upto_last(t + kBufs));
           multiply(half1, f1, c[u]);
-          spread(true);
+          spread(half1);
           if (++t > last) break;
         }
       }
@@ -239,14 +243,14 @@ template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> stru
         const int buf = (t - first) & 1, ahead = upto_last(t + 2);
         read_half(f1, buf, 1);
         multiply(half0, f0, c0);
-        spread(false);
+        spread(half0);
         step_barrier();
         Op::touch(c1);  // not used before the wait that it landed with
         read_half(f0, buf ^ 1, 0);
         const typename Op::Side c2 = op.load(ahead);
         load_step(buf, ahead);
         multiply(half1, f1, c0);
-        spread(true);
+        spread(half1);
         c0 = c1;
         c1 = c2;
       }

@@ -33,8 +33,8 @@ def _round(x, bits):
 
 
 def rounded(u, steps=5, eps=1e-7, bf16=False):
-    """``newton_schulz`` with stored values of 22 bits; for a bf16 destination the last group, if it is not
-    the first and has at most two iterations, with 11."""
+    """``newton_schulz`` with stored values of 22 bits; for a bf16 destination of 15, and the last group, if it
+    is not the first and has at most two iterations, with 11."""
     a, b, c = COEFFICIENTS
     x = np.asarray(u, np.float64)
     x = x / max(np.linalg.norm(x), eps)
@@ -42,10 +42,10 @@ def rounded(u, steps=5, eps=1e-7, bf16=False):
     x = x.T if tall else x
     one = np.eye(x.shape[0])
     done = 0
-    x = _round(x, 22)
+    x = _round(x, 15 if bf16 else 22)
     while done < steps:
         length = min(3, steps - done)
-        bits = 11 if bf16 and done and steps - done <= 2 else 22
+        bits = 22 if not bf16 else 11 if done and steps - done <= 2 else 15
         r = lambda v: _round(v, bits)  # noqa: E731,B023
         x = r(x)
         g, q = r(x @ x.T), None
@@ -57,7 +57,7 @@ def rounded(u, steps=5, eps=1e-7, bf16=False):
         x = q @ x
         done += length
         if done < steps:
-            x = _round(x, 22)
+            x = _round(x, 15 if bf16 else 22)
     return x.T if tall else x
 
 
