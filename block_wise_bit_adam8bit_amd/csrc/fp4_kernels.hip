@@ -112,6 +112,7 @@ struct QuantArgs {
   uint32_t across;  // workgroups along a row
 };
 
+// Reading x bounds it: 11008 x 4096 in bf16 take 21 us (5.5 TB/s, in part from the last-level cache), 8192 x 4096 18 us.
 // A workgroup takes 16 rows of 512 columns, a wave four of the rows one after the other: a lane holds 8
 // elements and four lanes a block, so a row is read in whole 1 KB pieces (bf16) and its codes written in 256
 // bytes.  The scales of 16 rows and 128 columns, 64 bytes that lie together, meet in LDS.
@@ -168,7 +169,8 @@ struct DequantArgs {
   uint32_t across;
 };
 
-// Sixteen rows of 512 columns per workgroup, as above: a lane turns 4 code bytes into 8 values.
+// Sixteen rows of 512 columns per workgroup, as above: a lane turns 4 code bytes into 8 values.  Writing them bounds it:
+// 11008 x 4096 to bf16 take 18 us (6.4 TB/s).
 template <typename OT> __global__ void __launch_bounds__(256) dequantize_kernel(DequantArgs q) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x / q.across) * 16;
@@ -216,7 +218,9 @@ struct FewArgs {
   int64_t ldo;
 };
 
-constexpr int kFewWaves = 8;
+// Waves per workgroup: 8, but 4 where each holds most registers and LDS (32 rows of 50257 x 2048 30 us with 8 and 27
+// with 4, at four runs of weight rows; 24 of 11008 x 4096, three runs, 12.0 and 12.5).
+constexpr int few_waves(int frags, int runs) { return frags == 2 && runs >= 4 ? 4 : 8; }
 
 // x w^T for at most 16 * kFrags rows of x: the time of reading the weights.  A workgroup owns 16 * kRuns rows
 // of w; its waves take turns at the steps of 256 along k, and their sums are added in LDS in the order of the
@@ -227,7 +231,8 @@ constexpr int kFewWaves = 8;
 // row are read past the end of a buffer, as 0, and a lane without a row of x takes the last one's values,
 // which no result uses.  What k has beyond whole steps comes after the loop.
 template <typename XT, typename OT, int kFrags, int kRuns>
-__global__ void __launch_bounds__(kFewWaves* kWave) few_rows_kernel(FewArgs g) {
+__global__ void __launch_bounds__(few_waves(kFrags, kRuns) * kWave) few_rows_kernel(FewArgs g) {
+  constexpr int kFewWaves = few_waves(kFrags, kRuns);
   __shared__ f32x4 sums[kFewWaves][kFrags * kRuns][kWave];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, h = lane >> 4;
@@ -524,19 +529,26 @@ int64_t scale_bytes(int64_t rows, int64_t cols) { return padded(cols) / 128 * pa
 bool too_many_tiles(int64_t rows, int64_t cols) { return ceil_div(rows, 128) * ceil_div(cols, 128) > kMaxGrid; }
 
 template <typename XT, typename OT, int kRuns> int launch_few_runs(const FewArgs& g, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(g.n, 16 * kRuns))), block(kFewWaves * kWave);
-  if (g.m <= 16) hipLaunchKernelGGL((few_rows_kernel<XT, OT, 1, kRuns>), grid, block, 0, s, g);
-  else hipLaunchKernelGGL((few_rows_kernel<XT, OT, 2, kRuns>), grid, block, 0, s, g);
+  const dim3 grid(static_cast<unsigned>(ceil_div(g.n, 16 * kRuns))), block(few_waves(g.m <= 16 ? 1 : 2, kRuns) * kWave);
+  if constexpr (kRuns <= 4) {
+    if (g.m <= 16) {
+      hipLaunchKernelGGL((few_rows_kernel<XT, OT, 1, kRuns>), grid, block, 0, s, g);
+      return launch_status();
+    }
+  }
+  hipLaunchKernelGGL((few_rows_kernel<XT, OT, 2, kRuns>), grid, block, 0, s, g);
   return launch_status();
 }
 
-// More weight rows per workgroup let more of them share one reading of x, fewer fill the chip more evenly.
-// The time goes by what a CU has to read, per column of k: its rounds of workgroups times their rows of
-// weights (half a byte) and of x.
+// More weight rows per workgroup let more of them share one reading and quantizing of x, fewer fill the chip more
+// evenly.  The time goes by what a CU has to read, per column of k: its rounds of workgroups times their rows
+// of weights (half a byte) and of x.  Up to eight runs of 16 above 16 rows of x (32 rows of 50257 x 2048 27 us with
+// four runs, 21 with eight), up to four below, where x weighs less.
 template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t s) {
   int runs = 1;
   int64_t least = 0;
-  for (int r = 1; r <= 4; ++r) {
+  for (int r : {1, 2, 3, 4, 6, 8}) {
+    if (r > 4 && g.m <= 16) break;  // no such instance
     const int64_t bytes = ceil_div(ceil_div(g.n, 16 * r), 256) * (8 * r + g.m * static_cast<int64_t>(sizeof(XT)));
     if (r == 1 || bytes < least) {
       least = bytes;
@@ -547,7 +559,9 @@ template <typename XT, typename OT> int launch_few(const FewArgs& g, hipStream_t
     case 1: return launch_few_runs<XT, OT, 1>(g, s);
     case 2: return launch_few_runs<XT, OT, 2>(g, s);
     case 3: return launch_few_runs<XT, OT, 3>(g, s);
-    default: return launch_few_runs<XT, OT, 4>(g, s);
+    case 4: return launch_few_runs<XT, OT, 4>(g, s);
+    case 6: return launch_few_runs<XT, OT, 6>(g, s);
+    default: return launch_few_runs<XT, OT, 8>(g, s);
   }
 }
 
@@ -561,6 +575,9 @@ struct Plan {
 // The plan of least time by this model, in microseconds on 256 CUs.  A step (256 along k) takes a CU
 //   1.70 for one tile of 256 x 256, 0.92 for half of one, 1.06 for two tiles of 128 x 128 side by
 //   side, 0.70 for one, and 0.50 with three buffers, where no CU has more than one.
+// (8192 x 11008 x 4096 takes 197 to 210 us, 3.5 to 3.75 PFLOP/s, of which the matrix instructions alone would take 95 at
+// the full clock; the chip's power holds the clock at 1.9 GHz, and a tile's first loads and results cost it 7 us, as
+// much as four steps.  8192^3 4.5 PFLOP/s.  With operands of zeros, which draw less power, 5.4 to 5.9.)
 // Splitting k, for products of too few tiles, adds a launch that joins the partial results (4) and
 // their way to memory and back (4 TB/s).
 Plan plan_for(int64_t m, int64_t n, int64_t k) {

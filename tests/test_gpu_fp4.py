@@ -253,7 +253,7 @@ def test_sizes_at_the_ends_of_the_range(q, x_size, w_size, m):
 @pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 31, 32, 33, 130])
 def test_linear(q, m, x_dtype, out):
     """Few rows in one launch and more in two, for widths of each number of weight rows per workgroup."""
-    for n, k in ((1, 1), (5, 33), (16, 256), (70, 300), (500, 2048), (4096, 511), (9000, 520), (13000, 257), (17000, 70)):
+    for n, k in ((1, 1), (5, 33), (16, 256), (70, 300), (500, 2048), (4096, 511), (9000, 520), (13000, 257), (17000, 70), (30000, 300)):
         rng = np.random.default_rng(m + n + k)
         x, w = integers(rng, m, k, x_dtype), q.qopt_fp4_quantize(integers(rng, n, k, BF16))
         got = q.qopt_fp4_linear(x, *w, out)
