@@ -1468,8 +1468,10 @@ extern "C" int qopt_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t
   *bytes = 0;
   if (batch == 0 || rows == 0 || cols == 0) return QOPT_OK;
   return guarded([&] {
-    // the first batch is the largest
+    // the batches but the last are alike; the last has smaller buffers, but may share tiles' steps where they do not
     std::vector<Matrix> all(static_cast<size_t>(std::min<int64_t>(batch, kMaxBatch)), matrix_of(rows, cols));
+    const size_t full = batch_end(all, 0, QOPT_F32);  // of equal matrices in either type
+    if (batch > static_cast<int64_t>(full)) all.resize(full + batch % full, all[0]);
     *bytes = static_cast<size_t>(workspace_of(all));
     return static_cast<int>(QOPT_OK);
   });

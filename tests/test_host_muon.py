@@ -88,6 +88,16 @@ def test_workspace_queries():
     assert L.qopt_muon_workspace(None, 1, ctypes.byref(n)) == EINVAL and L.qopt_muon_workspace(None, 0, None) == EINVAL
 
 
+@pytest.mark.parametrize("batch,rows,cols", [
+    (47, 311, 1713), (79, 856, 1029), (44, 1593, 270), (62, 1689, 325), (63, 747, 2144), (77, 1548, 311),  # smaller last lots ask for more
+    (1, 64, 64), (16, 200, 300), (17, 200, 300), (32, 100, 100), (33, 100, 100), (33, 20, 4000), (65, 32, 33), (5, 2048, 2048)])
+def test_a_batch_asks_for_what_its_matrices_one_by_one_do(batch, rows, cols):
+    one, each = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert L.qopt_orthogonalize_workspace(batch, rows, cols, ctypes.byref(one)) == OK
+    assert L.qopt_muon_workspace(tensors(*[(0, 0, 0, 0, rows, cols)] * batch), batch, ctypes.byref(each)) == OK
+    assert one.value == each.value
+
+
 def test_wrappers_refuse():
     x = torch.zeros(4, 8)
     codes, am = torch.zeros(32, dtype=torch.uint8), torch.zeros(1)
