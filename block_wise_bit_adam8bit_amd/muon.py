@@ -137,7 +137,10 @@ def _muon_plan(tensors, bits):
 def qopt_muon8bit_plan(tensors):
     """Plan of a Muon step with 8-bit momentum over a list of (param, grad, m_codes, m_absmax)
     tuples: matrices of any shapes, fp32 or bf16 params and grads; none may overlap another."""
-    return _muon_plan(tensors, 8).keep()
+    plan = _muon_plan(tensors, 8)
+    if plan.device is not None:
+        codebook(SIGNED, plan.device)  # on the device from here on: its first copy cannot be captured
+    return plan.keep()
 
 
 def qopt_muon32bit_plan(tensors):
@@ -227,7 +230,8 @@ class Muon(torch.optim.Optimizer):
     orthogonalisation at the precision of qopt_orthogonalize.  Parameters and gradients must be
     contiguous float32 or bfloat16 GPU tensors; all matrices of a group, device and type take one
     fused step.  ``step(grad_scale=t)`` multiplies every gradient with the float32 GPU value
-    ``t`` inside the step.
+    ``t`` inside the step.  A step that begins states is not captured into a graph; a captured one
+    keeps its settings and its parameters' and gradients' memory.
     """
 
     def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.1, *, nesterov=True, adjust="original",
@@ -294,6 +298,8 @@ class Muon(torch.optim.Optimizer):
             new = [p for p in live if not self.state[p]]
             fresh += new
             work.append((group, live, new, settings))
+        if fresh and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step would begin its state anew in every replay: step once before the capture")
         # every list is made, which is where overlaps are found, before the first one runs
         jobs = []
         try:

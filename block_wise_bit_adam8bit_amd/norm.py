@@ -191,7 +191,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """Layer normalisation over the last axis of x (float32 or bfloat16), times ``weight`` plus
     ``bias`` ([dim], both float32 or both bfloat16; either may be None), with gradients for all three.  A
     trace (torch.jit.trace) holds it as one operation; forward-mode derivatives are refused
-    (NotImplementedError)."""
+    (NotImplementedError).  For passes that are captured into a graph the conditions of
+    ``fp8_linear`` hold."""
     given = [t for t in (x, weight, bias) if t is not None]
     if torch.is_grad_enabled() and any(t.requires_grad for t in given) or _is_tracing() or _has_tangent(*given):
         return LayerNormFunction.apply(x, weight, bias, eps)

@@ -506,6 +506,50 @@ def test_optimizer_refuses_before_any_state(q):
     assert not opt.state and all(torch.equal(p, b) for p, b in zip(ps[:2], before))
 
 
+def test_a_captured_step_begins_no_state(q, monkeypatch):
+    rng = np.random.default_rng(19)
+    ps = model(rng)
+    opt = q.Muon(ps, min_8bit_size=1)
+    set_grads(rng, ps)
+    before = [p.detach().clone() for p in ps]
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        with pytest.raises(RuntimeError, match="capture"):
+            opt.step()
+        assert not any(opt.state.values()) and all(torch.equal(p, b) for p, b in zip(ps, before))
+    opt.step()
+    assert all(opt.state[p] for p in ps)
+
+
+def test_an_optimizers_step_replayed(q):
+    """Three replays of a captured step, each with its own gradients and eager work between them, against eager steps."""
+    rng = np.random.default_rng(20)
+    ps, twin = model(rng), None
+    opt = q.Muon(ps, lr=2e-3, min_8bit_size=4096)
+    set_grads(rng, ps)
+    opt.step()
+    twin = [torch.nn.Parameter(p.detach().clone()) for p in ps]
+    other = q.Muon(twin, lr=2e-3, min_8bit_size=4096)
+    other.load_state_dict(opt.state_dict())
+    grads = [p.grad for p in ps]
+    kept = [p.detach().clone() for p in ps]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    assert all(torch.equal(p, k) for p, k in zip(ps, kept))  # a capture steps nothing
+    for _ in range(3):
+        for p, t, g in zip(ps, twin, grads):
+            g.copy_(torch.from_numpy(rng.standard_normal(p.shape)))
+            t.grad = g.clone()
+        other.step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, t in zip(ps, twin):
+            a, b = opt.state[p], other.state[t]
+            assert torch.equal(p, t) and all(torch.equal(a[k], b[k]) for k in a)
+
+
 def test_a_block_trains_with_all_of_them(q):
     """A feed-forward block's step: normalised, through two 4-bit products, matrices by Muon, the norm's vectors
     by AdamW.  The same step from the parts called by hand gives the same parameters."""
