@@ -575,7 +575,7 @@ struct Plan {
 // The plan of least time by this model, in microseconds on 256 CUs.  A step (256 along k) takes a CU
 //   1.70 for one tile of 256 x 256, 0.92 for half of one, 1.06 for two tiles of 128 x 128 side by
 //   side, 0.70 for one, and 0.50 with three buffers, where no CU has more than one.
-// (8192 x 11008 x 4096 takes 197 to 210 us, 3.5 to 3.75 PFLOP/s, of which the matrix instructions alone would take 95 at
+// (8192 x 11008 x 4096 takes 197 to 210 us, 3.5 to 3.75 PFLOP/s, of which the matrix instructions alone would take 73 at
 // the full clock; the chip's power holds the clock at 1.9 GHz, and a tile's first loads and results cost it 7 us, as
 // much as four steps.  8192^3 4.5 PFLOP/s.  With operands of zeros, which draw less power, 5.4 to 5.9.)
 // Splitting k, for products of too few tiles, adds a launch that joins the partial results (4) and

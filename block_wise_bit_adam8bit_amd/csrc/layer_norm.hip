@@ -6,6 +6,14 @@
 // the same wave or workgroup is loaded meanwhile, and a workgroup goes through many rows, so
 // that the weight and the bias are read, and the sums of their gradients written, once for all
 // of them.
+//
+// Measured (bf16, 65536 rows of 4096; a large copy moves 4.9 TB/s): forward 217 us for its 1.07 GB, 4.95 TB/s;
+// backward 309 us for 1.61 GB, 5.2 TB/s, and 5.6 us to join the groups' sums.  fp32, 1999 rows of 2048, which the
+// last-level cache holds: 9.9, 12.8 and 4.7.  One row of 4096: 3.0, a launch.
+//
+// The mean is taken first and the squares of what differs from it are summed then: both from registers, so that
+// it costs no second reading, and a row far from zero loses nothing to cancellation.  Every sum is held in
+// binary32 and joined in a fixed order; a result is rounded to bfloat16 once, where it is stored.
 
 #include <hip/hip_runtime.h>
 
@@ -218,8 +226,10 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardAr
   }
 }
 
-// The same walk for the gradients.  A thread's columns are the same in every row, so the sums of dout h and
-// of dout stay in its registers; the workgroup's waves that hold rows of their own add theirs in LDS.
+// The same walk for the gradients: with h = (x - mean) rstd and v = dout w,
+//   dx = (v - mean of v - h (mean of v h)) rstd,  dw = sum of dout h,  db = sum of dout.
+// A thread's columns are the same in every row, so the sums of dout h and of dout stay in its registers; the
+// workgroup's waves that hold rows of their own add theirs in LDS.
 template <typename XT, typename WT, int kWaves, int kChunks, bool kWhole>
 __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(BackwardArgs a) {
   constexpr int kLanes = kWaves * kWave, kRows = rows_at_once<kWaves>();
@@ -415,7 +425,8 @@ template <typename XT> __global__ void __launch_bounds__(256) columns_long_kerne
 // ------------------------------------------------------------------ joining the groups' sums
 
 // dw and db from `groups` partial sums [groups][2][dim].  A workgroup owns 64 columns; its 16 waves take turns
-// at the groups.
+// at the groups, with eight of their sums' loads under way: 4.7 us for 2048 columns (one by one, 9.6), of which
+// the 8 MB themselves are 2.
 constexpr int kJoinWaves = 16;
 template <typename WT>
 __global__ void __launch_bounds__(kJoinWaves * kWave) join_kernel(const float* part, int64_t dim, int groups, WT* dw, WT* db) {
@@ -426,6 +437,7 @@ __global__ void __launch_bounds__(kJoinWaves * kWave) join_kernel(const float* p
   if (!to) return;
   float s = 0.0f;
   if (j < dim)
+#pragma unroll 8
     for (int g = wave; g < groups; g += kJoinWaves) s += part[(static_cast<int64_t>(g) * 2 + blockIdx.y) * dim + j];
   sums[wave][lane] = s;
   __syncthreads();
@@ -444,6 +456,8 @@ bool bad_dtype(int d) { return d != QOPT_F32 && d != QOPT_BF16; }
 uintptr_t size_of(int d) { return d == QOPT_F32 ? 4 : 2; }
 
 constexpr int64_t kLongDim = 16384;  // longest row in registers
+// Forward: as many workgroups as are on the chip at once.  Backward: two per CU, since every group writes, and the join
+// reads, a row of sums of its own.
 constexpr int64_t kForwardGroups = 2048, kBackwardGroups = 512;
 
 // f with the number of waves and chunks of a row as types: forward 32 elements per thread at most, backward,

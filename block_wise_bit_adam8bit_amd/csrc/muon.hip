@@ -109,6 +109,8 @@ enum Source : int { kPlain = 0, kMomentum32 = 1, kMomentum8 = 2 };
 
 // Blocks of 2048 of one matrix (blockIdx.y), every groups-th by a workgroup: the new momentum, the update u
 // and its sum of squares (binary64: squares of any binary32 numbers neither overflow nor vanish).
+// Bound by memory: 4096 x 11008 with binary32 momentum, 631 MB, 140 to 145 us, 4.4 TB/s; with codes, 58.7 M parameters in six
+// matrices, 124 us for 470 MB, in which the encoder's search shows.
 template <typename GT, int kSource> __global__ void __launch_bounds__(256) source_kernel(SourceArgs a) {
   __shared__ __align__(16) qopt_codebook cb;  // kMomentum8
   __shared__ double slots[4];
@@ -299,7 +301,7 @@ struct PackArgs {
 
 // X = U 2^kExp / max(|U|, eps) and its transpose.  A wave takes 64 x 64 values, a lane 8 x 8 of them:
 // it reads 8 runs of 8, writes them as 8 places of the operand's rows, and of the transpose's; the lanes next
-// to each other make runs of 256 bytes either way.
+// to each other make runs of 256 bytes either way.  4096 x 11008 in kWide, 541 MB: 122 to 126 us, 4.4 TB/s.
 template <typename ST, int kForm> __global__ void __launch_bounds__(256) pack_kernel(PackArgs a) {
   __shared__ double slots[4];
   int j = 0;
@@ -507,6 +509,11 @@ template <bool kBig, typename Op> struct TileOf {
 // Whole tiles leave CUs idle in the last round: 136 tiles of 256 x 256 below the diagonal of 4096 x 4096 use
 // half of the chip.  Runs of equal length over the tiles' steps use all of it; a tile that lies in several runs is
 // joined by a launch of its own, which reads the runs' sums in their order and does what follows a product.
+//
+// Measured: Q X of 4096 x 4096 x 11008 in kWide 920 to 980 us, 1.2 PFLOP/s of single numbers (three instructions each),
+// the matrix units busy 79 to 81 % of the CUs' time at 1.7 GHz, which is where the chip's power holds the clock: that is what
+// bounds it.  X X^T of the same: 360 us, and 26 to join.  A symmetric product of 4096 x 4096: 170 to 183 us, and 38
+// to join.  Four of 2048 x 2048 in kMiddle: 104 to 120 us, matrix units busy 56 % of 144 CUs' time; in kNarrow 52 to 56 and 65 %.
 template <bool kBig, int kIn, int kOut, int kEpilogue, typename OT>
 __global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a) {
   typedef TileOf<kBig, HalfOp<kIn>> O;
@@ -610,6 +617,9 @@ __global__ void __launch_bounds__(kBig ? 512 : 256) join_kernel(ProductArgs a) {
 // A group on matrices of at most 128 x 128: one workgroup per matrix takes it from A to Q.  A, P and Q stay in
 // registers in binary32, 64 of a lane's 512 each, laid out as a product's sums; LDS holds the two operands of the
 // product at hand as `Tile` would have loaded them, and since they are symmetric, as either side of it.
+// One iteration takes 10 us, two 20 to 22, three 34, where each of their products in a launch of its own takes 6 to 9: in all
+// of 99 x 300, 103 us against 146 (in groups of three, before their length went by the size).  What bounds it is one
+// workgroup's chain of products on four matrix units, whatever the number of matrices up to one per CU.
 constexpr int64_t kChainDim = 128;
 
 struct ChainJob {
@@ -765,6 +775,9 @@ template <int kForm> __global__ void __launch_bounds__(256, 1) chain_kernel(Chai
 // Up to kTiny on the shorter side (an adapter's rank) the products with U are short sums and what would bound the
 // way above is its launches.  Here it takes three, in binary64, where five iterations on A need no fresh start:
 // A = U U^T, whose trace is the squared norm; the polynomial Q of A / |U|^2; and Q U / |U|.
+// 16 x 4096 takes 34 us, 32 x 4096 57, 5 x 300 21 (the way above: 99 x 300 120, 33 x 4096 182), and the results are within 2.5e-8.  The
+// polynomial's products in one workgroup are most of it at 32: twice as many rows would make that chain eight times as long, and
+// its four matrices, 34 KB of LDS now, four times as large.
 constexpr int kTiny = 32;
 constexpr int kGramColumns = 64, kResultColumns = 256;  // of the longer side, per workgroup and turn
 constexpr int kTinyParts = 128;                         // partial A per matrix
