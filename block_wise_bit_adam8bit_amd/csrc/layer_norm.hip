@@ -38,8 +38,6 @@ template <typename T> struct Raw {
   uint32_t r[kChunk * sizeof(T) / 4];
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const bf16x2 v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
   return __builtin_bit_cast(uint32_t, v);
@@ -351,8 +349,14 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
 
 constexpr int kLongThreads = 1024;
 
-// The row is read again for each of its sums (from the caches, where it still fits).
-template <typename XT, typename WT> __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(ForwardArgs a) {
+// f(at, in_row) for the thread's chunks of a row.
+template <bool kWhole, typename F> __device__ __forceinline__ void chunks_of(int64_t dim, F&& f) {
+  for (int64_t at = static_cast<int64_t>(threadIdx.x) * kChunk; at < dim; at += kLongThreads * kChunk) f(at, in_row<kWhole>(at, dim));
+}
+
+// The row is read again for each of its sums (from the caches, where it still fits).  4096 x 20000 in bf16: 98 us forward
+// and 208 backward, where the sums over the rows are a launch of their own.
+template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(ForwardArgs a) {
   constexpr int kWaves = kLongThreads / kWave;
   __shared__ float slots[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -362,19 +366,35 @@ template <typename XT, typename WT> __global__ void __launch_bounds__(kLongThrea
     const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
     XT* out = static_cast<XT*>(a.out) + row * a.ldo;
     float sum = 0.0f, square = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) sum += to_f32(x[j]);
+    chunks_of<kWhole>(a.dim, [&](int64_t at, int valid) {
+      float v[kChunk], part = 0.0f;
+      widen(load_chunk<kWhole>(x, at, a.dim), v);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) part += e < valid ? v[e] : 0.0f;
+      sum += part;
+    });
     const float mean = row_sum<kWaves>(sum, slots, 0, wave) / n;
-    for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
-      const float d = to_f32(x[j]) - mean;
-      square += d * d;
-    }
+    chunks_of<kWhole>(a.dim, [&](int64_t at, int valid) {
+      float v[kChunk], part = 0.0f;
+      widen(load_chunk<kWhole>(x, at, a.dim), v);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) part += e < valid ? (v[e] - mean) * (v[e] - mean) : 0.0f;
+      square += part;
+    });
     const float rstd = 1.0f / sqrtf(row_sum<kWaves>(square, slots, 1, wave) / n + a.eps);
-    for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
-      float v = (to_f32(x[j]) - mean) * rstd;
-      if (pw) v *= to_f32(pw[j]);
-      if (pb) v += to_f32(pb[j]);
-      store1(out + j, v);
-    }
+    chunks_of<kWhole>(a.dim, [&](int64_t at, int) {
+      float v[kChunk], wv[kChunk], bv[kChunk];
+      widen(load_chunk<kWhole>(x, at, a.dim), v);
+      if (pw) widen(load_chunk<kWhole>(pw, at, a.dim), wv);
+      if (pb) widen(load_chunk<kWhole>(pb, at, a.dim), bv);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        v[e] = (v[e] - mean) * rstd;
+        if (pw) v[e] *= wv[e];
+        if (pb) v[e] += bv[e];
+      }
+      store_chunk<kWhole>(out, at, a.dim, v);
+    });
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -382,7 +402,7 @@ template <typename XT, typename WT> __global__ void __launch_bounds__(kLongThrea
   }
 }
 
-template <typename XT, typename WT> __global__ void __launch_bounds__(kLongThreads) dx_long_kernel(BackwardArgs a) {
+template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds__(kLongThreads) dx_long_kernel(BackwardArgs a) {
   constexpr int kWaves = kLongThreads / kWave;
   __shared__ float slots[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -393,33 +413,62 @@ template <typename XT, typename WT> __global__ void __launch_bounds__(kLongThrea
     XT* dx = static_cast<XT*>(a.dx) + row * a.lddx;
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s0 = 0.0f, s1 = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
-      const float v = to_f32(dout[j]) * (pw ? to_f32(pw[j]) : 1.0f);
-      s0 += v;
-      s1 += v * ((to_f32(x[j]) - mean) * rstd);
-    }
+    auto load = [&](int64_t at, float (&v)[kChunk], float (&h)[kChunk]) {
+      widen(load_chunk<kWhole>(dout, at, a.dim), v);
+      widen(load_chunk<kWhole>(x, at, a.dim), h);
+      float wv[kChunk];
+      if (pw) widen(load_chunk<kWhole>(pw, at, a.dim), wv);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        if (pw) v[e] *= wv[e];
+        h[e] = (h[e] - mean) * rstd;
+      }
+    };
+    chunks_of<kWhole>(a.dim, [&](int64_t at, int valid) {
+      float v[kChunk], h[kChunk], p0 = 0.0f, p1 = 0.0f;
+      load(at, v, h);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) {
+        p0 += e < valid ? v[e] : 0.0f;
+        p1 += e < valid ? v[e] * h[e] : 0.0f;
+      }
+      s0 += p0;
+      s1 += p1;
+    });
     s0 = row_sum<kWaves>(s0, slots, 0, wave) / n;
     s1 = row_sum<kWaves>(s1, slots, 1, wave) / n;
-    for (int64_t j = threadIdx.x; j < a.dim; j += kLongThreads) {
-      const float v = to_f32(dout[j]) * (pw ? to_f32(pw[j]) : 1.0f);
-      store1(dx + j, (v - s0 - (to_f32(x[j]) - mean) * rstd * s1) * rstd);
-    }
+    chunks_of<kWhole>(a.dim, [&](int64_t at, int) {
+      float v[kChunk], h[kChunk];
+      load(at, v, h);
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) v[e] = (v[e] - s0 - h[e] * s1) * rstd;
+      store_chunk<kWhole>(dx, at, a.dim, v);
+    });
   }
 }
 
-// Sums of dout h and dout over every gridDim.y-th row, one column per thread.
-template <typename XT> __global__ void __launch_bounds__(256) columns_long_kernel(BackwardArgs a) {
-  const int64_t j = blockIdx.x * int64_t{256} + threadIdx.x;
-  if (j >= a.dim) return;
-  float dw = 0.0f, db = 0.0f;
+// Sums of dout h and dout over every gridDim.y-th row, a chunk of columns per thread.
+template <typename XT, bool kWhole> __global__ void __launch_bounds__(256) columns_long_kernel(BackwardArgs a) {
+  const int64_t at = (blockIdx.x * int64_t{256} + threadIdx.x) * kChunk;
+  if (at >= a.dim) return;
+  float dw[kChunk], db[kChunk];
+#pragma unroll
+  for (int e = 0; e < kChunk; ++e) dw[e] = db[e] = 0.0f;
+#pragma unroll 4
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    const float g = to_f32(static_cast<const XT*>(a.dout)[row * a.lddo + j]);
-    dw += g * ((to_f32(static_cast<const XT*>(a.x)[row * a.ldx + j]) - a.mean[row]) * a.rstd[row]);
-    db += g;
+    float g[kChunk], h[kChunk];
+    widen(load_chunk<kWhole>(static_cast<const XT*>(a.dout) + row * a.lddo, at, a.dim), g);
+    widen(load_chunk<kWhole>(static_cast<const XT*>(a.x) + row * a.ldx, at, a.dim), h);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) {
+      dw[e] += g[e] * ((h[e] - mean) * rstd);
+      db[e] += g[e];
+    }
   }
   float* part = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.dim;
-  part[j] = dw;
-  part[a.dim + j] = db;
+  store_chunk<kWhole>(part, at, a.dim, dw);
+  store_chunk<kWhole>(part + a.dim, at, a.dim, db);
 }
 
 // ------------------------------------------------------------------ joining the groups' sums
@@ -456,12 +505,16 @@ bool bad_dtype(int d) { return d != QOPT_F32 && d != QOPT_BF16; }
 uintptr_t size_of(int d) { return d == QOPT_F32 ? 4 : 2; }
 
 constexpr int64_t kLongDim = 16384;  // longest row in registers
-// Forward: as many workgroups as are on the chip at once.  Backward: two per CU, since every group writes, and the join
-// reads, a row of sums of its own.
+// Workgroups: as many as are on the chip at once, since each reads the weight and the bias, and in backward
+// writes sums of its own: of rows behind 8192 elements forward has two per CU (4096 x 16384 in fp32: 105 us; four
+// times as many 119), and backward one behind 6144 (16384 x 8192 in bf16: 150 us; two 158, half of one 197).
+// Backward of 65536 x 4096 with 256, 512 and 1024 groups: 330, 293 and 343 us.
 constexpr int64_t kForwardGroups = 2048, kBackwardGroups = 512;
 
 // f with the number of waves and chunks of a row as types: forward 32 elements per thread at most, backward,
-// which keeps two sums for each of its columns, 16.
+// which keeps two sums for each of its columns, 24 (the most whose next row fits the registers too).  A shape of
+// three chunks between two powers of two, so that no more than a third of the lanes is idle: 8192 x 11008 in bf16
+// takes 73 us forward and 109 backward, 91 and 142 with the shapes of 16384; 8192 x 5120 30 and 50 (33 and 55).
 template <int kW, int kC> struct Shape {
   static constexpr int kWaves = kW, kChunks = kC;
 };
@@ -470,7 +523,9 @@ template <typename F> int forward_shape(int64_t dim, F&& f) {
   if (dim <= 1024) return f(Shape<1, 2>{});
   if (dim <= 2048) return f(Shape<1, 4>{});
   if (dim <= 4096) return f(Shape<4, 2>{});
+  if (dim <= 6144) return f(Shape<4, 3>{});
   if (dim <= 8192) return f(Shape<4, 4>{});
+  if (dim <= 12288) return f(Shape<8, 3>{});
   return f(Shape<8, 4>{});
 }
 template <typename F> int backward_shape(int64_t dim, F&& f) {
@@ -478,7 +533,9 @@ template <typename F> int backward_shape(int64_t dim, F&& f) {
   if (dim <= 1024) return f(Shape<1, 2>{});
   if (dim <= 2048) return f(Shape<4, 1>{});
   if (dim <= 4096) return f(Shape<4, 2>{});
+  if (dim <= 6144) return f(Shape<4, 3>{});
   if (dim <= 8192) return f(Shape<8, 2>{});
+  if (dim <= 12288) return f(Shape<8, 3>{});
   return f(Shape<16, 2>{});
 }
 // Workgroups for so many rows.
@@ -486,13 +543,14 @@ int64_t groups_of(int64_t rows, bool one_wave, int64_t most) {
   const int64_t units = one_wave ? ceil_div(rows, rows_at_once<1>()) : rows;
   return units < most ? units : most;
 }
-int64_t forward_groups(int64_t rows, int64_t dim) { return groups_of(rows, dim <= 2048, kForwardGroups); }
-int64_t backward_groups(int64_t rows, int64_t dim) { return groups_of(rows, dim <= 1024, kBackwardGroups); }
+int64_t forward_groups(int64_t rows, int64_t dim) { return groups_of(rows, dim <= 2048, dim <= 8192 ? kForwardGroups : kForwardGroups / 4); }
+int64_t backward_groups(int64_t rows, int64_t dim) { return groups_of(rows, dim <= 1024, dim <= 6144 ? kBackwardGroups : kBackwardGroups / 2); }
 
 template <typename XT, typename WT> int launch_forward(const ForwardArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(forward_groups(a.rows, a.dim)));
   if (a.dim > kLongDim) {
-    hipLaunchKernelGGL((forward_long_kernel<XT, WT>), grid, dim3(kLongThreads), 0, s, a);
+    if (a.dim % kChunk == 0) hipLaunchKernelGGL((forward_long_kernel<XT, WT, true>), grid, dim3(kLongThreads), 0, s, a);
+    else hipLaunchKernelGGL((forward_long_kernel<XT, WT, false>), grid, dim3(kLongThreads), 0, s, a);
     return launch_status();
   }
   return forward_shape(a.dim, [&](auto shape) {
@@ -507,10 +565,14 @@ template <typename XT, typename WT> int launch_forward(const ForwardArgs& a, hip
 template <typename XT, typename WT> int launch_backward(const BackwardArgs& a, hipStream_t s) {
   const unsigned groups = static_cast<unsigned>(backward_groups(a.rows, a.dim));
   if (a.dim > kLongDim) {
-    if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT>), dim3(groups), dim3(kLongThreads), 0, s, a);
-    if (a.part)
-      hipLaunchKernelGGL((columns_long_kernel<XT>), dim3(static_cast<unsigned>(ceil_div(a.dim, 256)), groups), dim3(256),
-                         0, s, a);
+    const dim3 columns(static_cast<unsigned>(ceil_div(a.dim, 256 * kChunk)), groups), block(kLongThreads);
+    if (a.dim % kChunk == 0) {
+      if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT, true>), dim3(groups), block, 0, s, a);
+      if (a.part) hipLaunchKernelGGL((columns_long_kernel<XT, true>), columns, dim3(256), 0, s, a);
+    } else {
+      if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT, false>), dim3(groups), block, 0, s, a);
+      if (a.part) hipLaunchKernelGGL((columns_long_kernel<XT, false>), columns, dim3(256), 0, s, a);
+    }
     return launch_status();
   }
   return backward_shape(a.dim, [&](auto shape) {
