@@ -60,27 +60,50 @@ template <typename T> __device__ __forceinline__ void widen(const Raw<T>& w, flo
   }
 }
 
-// Elements `at` to `at` + 7 of a row of `dim`.  kWhole: dim is a multiple of 8, so that a chunk lies
-// inside of the row or behind it; one behind it loads the row's first elements (no branch, which would
-// keep the compiler from issuing the loads together).  What lies behind the row's end is not to be used.
-template <bool kWhole, typename T>
-__device__ __forceinline__ Raw<T> load_chunk(const T* row, int64_t at, int64_t dim) {
+// How the chunks of a row of `dim` lie.
+//   kWhole   dim is a multiple of 8
+//   kRagged  it is not: the row's last chunk begins at dim - 8 and shares elements with the one before, whose
+//            results both write, the same bits; in sums over the row they count once
+//   kShort   dim is less than 8: a single chunk
+enum Width : int { kWhole, kRagged, kShort };
+
+// The chunk that begins with element `at` if it is whole.  One behind the row's end has the row's first elements (no
+// branch, which would keep the compiler from issuing the loads together), counts none of them and stores nothing.
+// (16384 x 1999 in fp32 takes 49 us forward and 76 backward, as 16384 x 2000; with a branch around the loads of a chunk that
+// the row's end may cut, 155 and 161.  What alignment the address has costs next to nothing, but rows of bf16 at odd
+// ones a quarter: 8192 x 9001 74 us, 9000 54.)
+template <Width kWidth> struct Place {
+  int at, first, last;  // elements `first` to `last` - 1 of the eight count
+  bool in;
+  __device__ __forceinline__ Place(int i, int dim) {
+    in = i < dim;
+    at = !in || kWidth == kShort ? 0 : kWidth == kRagged && i > dim - kChunk ? dim - kChunk : i;
+    first = in ? i - at : kChunk;
+    last = kWidth == kShort ? dim : kChunk;
+  }
+  __device__ __forceinline__ bool counts(int e) const { return e >= first && (kWidth != kShort || e < last); }
+};
+
+template <Width kWidth, typename T> __device__ __forceinline__ Raw<T> load_chunk(const T* row, const Place<kWidth>& p) {
   Raw<T> w;
-  if constexpr (kWhole) {
-    __builtin_memcpy(&w, row + (at < dim ? at : 0), sizeof(w));
-  } else if (at + kChunk <= dim) {
-    __builtin_memcpy(&w, row + at, sizeof(w));
-  } else {
+  if constexpr (kWidth == kShort) {
     T one[kChunk];
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e) one[e] = row[at + e < dim ? at + e : dim - 1];
+    for (int e = 0; e < kChunk; ++e) one[e] = row[e < p.last ? e : p.last - 1];
     __builtin_memcpy(&w, one, sizeof(w));
+  } else {
+    __builtin_memcpy(&w, row + p.at, sizeof(w));
   }
   return w;
 }
-template <bool kWhole, typename T>
-__device__ __forceinline__ void store_chunk(T* row, int64_t at, int64_t dim, const float (&v)[kChunk]) {
-  if (kWhole ? at < dim : at + kChunk <= dim) {
+template <Width kWidth, typename T>
+__device__ __forceinline__ void store_chunk(T* row, const Place<kWidth>& p, const float (&v)[kChunk]) {
+  if (!p.in) return;
+  if constexpr (kWidth == kShort) {
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+      if (e < p.last) store1(row + e, v[e]);
+  } else {
     Raw<T> w;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -89,18 +112,8 @@ __device__ __forceinline__ void store_chunk(T* row, int64_t at, int64_t dim, con
 #pragma unroll
       for (int e = 0; e < kChunk / 2; ++e) w.r[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
     }
-    __builtin_memcpy(row + at, &w, sizeof(w));
-  } else if (!kWhole) {
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e)
-      if (at + e < dim) store1(row + at + e, v[e]);
+    __builtin_memcpy(row + p.at, &w, sizeof(w));
   }
-}
-// How many of the chunk's elements lie in the row.
-template <bool kWhole> __device__ __forceinline__ int in_row(int64_t at, int64_t dim) {
-  if (kWhole) return at < dim ? kChunk : 0;
-  const int64_t left = dim - at;
-  return left >= kChunk ? kChunk : left > 0 ? static_cast<int>(left) : 0;
 }
 
 // ------------------------------------------------------------------ sums over a row
@@ -147,20 +160,20 @@ template <int kWaves> constexpr int rows_at_once() { return kWaves == 1 ? 4 : 1;
 template <int kWaves> constexpr int threads_of() { return kWaves == 1 ? 256 : kWaves * kWave; }
 
 // A row by kWaves waves, kChunks chunks of 8 elements per thread: dim <= kWaves * 64 * 8 * kChunks.
-template <typename XT, typename WT, int kWaves, int kChunks, bool kWhole>
+template <typename XT, typename WT, int kWaves, int kChunks, Width kWidth>
 __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardArgs a) {
   __shared__ float slots[2][kWaves];
   constexpr int kLanes = kWaves * kWave, kRows = rows_at_once<kWaves>();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = threadIdx.x % kLanes;
+  const int lane = threadIdx.x % kLanes, dim = static_cast<int>(a.dim);
+  auto place = [&](int c) { return Place<kWidth>((c * kLanes + lane) * kChunk, dim); };
   const XT* x = static_cast<const XT*>(a.x);
   const WT *pw = static_cast<const WT*>(a.w), *pb = static_cast<const WT*>(a.b);
   Raw<WT> w[kChunks], b[kChunks];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    const int64_t at = (static_cast<int64_t>(c) * kLanes + lane) * kChunk;
-    if (pw) w[c] = load_chunk<kWhole>(pw, at, a.dim);
-    if (pb) b[c] = load_chunk<kWhole>(pb, at, a.dim);
+    if (pw) w[c] = load_chunk(pw, place(c));
+    if (pb) b[c] = load_chunk(pb, place(c));
   }
   const float n = static_cast<float>(a.dim);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
@@ -169,8 +182,7 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardAr
   Raw<XT> next[kChunks];
   auto load = [&](int64_t i) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-      next[c] = load_chunk<kWhole>(x + i * a.ldx, (static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim);
+    for (int c = 0; c < kChunks; ++c) next[c] = load_chunk(x + i * a.ldx, place(c));
   };
   load(row);
   for (; row < a.rows; row += step) {
@@ -178,14 +190,11 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardAr
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int valid = in_row<kWhole>((static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim);
+      const auto p = place(c);
       widen(next[c], v[c]);
       float part = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) {
-        if (e >= valid) v[c][e] = 0.0f;
-        part += v[c][e];
-      }
+      for (int e = 0; e < kChunk; ++e) part += p.counts(e) ? v[c][e] : 0.0f;
       sum += part;
     }
     load(row + step < a.rows ? row + step : row);
@@ -193,12 +202,12 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardAr
     float square = 0.0f;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int valid = in_row<kWhole>((static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim);
+      const auto p = place(c);
       float part = 0.0f;
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
         v[c][e] -= mean;
-        part += e < valid ? v[c][e] * v[c][e] : 0.0f;
+        part += p.counts(e) ? v[c][e] * v[c][e] : 0.0f;
       }
       square += part;
     }
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardAr
         if (pw) v[c][e] *= wv[e];
         if (pb) v[c][e] += bv[e];
       }
-      store_chunk<kWhole>(out, (static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim, v[c]);
+      store_chunk(out, place(c), v[c]);
     }
     if (lane == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -228,21 +237,22 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) forward_kernel(ForwardAr
 //   dx = (v - mean of v - h (mean of v h)) rstd,  dw = sum of dout h,  db = sum of dout.
 // A thread's columns are the same in every row, so the sums of dout h and of dout stay in its registers; the
 // workgroup's waves that hold rows of their own add theirs in LDS.
-template <typename XT, typename WT, int kWaves, int kChunks, bool kWhole>
+template <typename XT, typename WT, int kWaves, int kChunks, Width kWidth>
 __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(BackwardArgs a) {
   constexpr int kLanes = kWaves * kWave, kRows = rows_at_once<kWaves>();
   constexpr bool kAhead = kWaves < 16;  // 16 waves have 128 registers each, too few for the next row
   __shared__ float slots[4][kWaves];
   __shared__ float sums[kRows > 1 ? kLanes * kChunk : 1];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = threadIdx.x % kLanes;
+  const int lane = threadIdx.x % kLanes, dim = static_cast<int>(a.dim);
+  auto place = [&](int c) { return Place<kWidth>((c * kLanes + lane) * kChunk, dim); };
   const XT *x = static_cast<const XT*>(a.x), *dout = static_cast<const XT*>(a.dout);
   const WT* pw = static_cast<const WT*>(a.w);
   Raw<WT> w[kChunks];
   float dw[kChunks][kChunk], db[kChunks][kChunk];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) {
-    if (pw) w[c] = load_chunk<kWhole>(pw, (static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim);
+    if (pw) w[c] = load_chunk(pw, place(c));
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) dw[c][e] = db[c][e] = 0.0f;
   }
@@ -254,9 +264,8 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
   auto load = [&](int64_t i) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int64_t at = (static_cast<int64_t>(c) * kLanes + lane) * kChunk;
-      next_x[c] = load_chunk<kWhole>(x + i * a.ldx, at, a.dim);
-      next_g[c] = load_chunk<kWhole>(dout + i * a.lddo, at, a.dim);
+      next_x[c] = load_chunk(x + i * a.ldx, place(c));
+      next_g[c] = load_chunk(dout + i * a.lddo, place(c));
     }
     next_mean = a.mean[i];
     next_rstd = a.rstd[i];
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      const int valid = in_row<kWhole>((static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim);
+      const auto p = place(c);
       float wv[kChunk];
       widen(next_x[c], h[c]);
       widen(next_g[c], v[c]);
@@ -277,13 +286,12 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
       float p0 = 0.0f, p1 = 0.0f;
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
-        h[c][e] = e < valid ? (h[c][e] - mean) * rstd : 0.0f;
-        if (e >= valid) v[c][e] = 0.0f;
+        h[c][e] = (h[c][e] - mean) * rstd;
         dw[c][e] += v[c][e] * h[c][e];
         db[c][e] += v[c][e];
-        if (pw) v[c][e] *= e < valid ? wv[e] : 0.0f;
-        p0 += v[c][e];
-        p1 += v[c][e] * h[c][e];
+        if (pw) v[c][e] *= wv[e];
+        p0 += p.counts(e) ? v[c][e] : 0.0f;
+        p1 += p.counts(e) ? v[c][e] * h[c][e] : 0.0f;
       }
       s0 += p0;
       s1 += p1;
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
       for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) v[c][e] = (v[c][e] - s0 - h[c][e] * s1) * rstd;
-        store_chunk<kWhole>(dx, (static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim, v[c]);
+        store_chunk(dx, place(c), v[c]);
       }
     }
   }
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
         __syncthreads();
         if (wave != 0) continue;
       }
-      store_chunk<kWhole>(to, (static_cast<int64_t>(c) * kLanes + lane) * kChunk, a.dim, s[c]);
+      store_chunk(to, place(c), s[c]);
     }
   };
   finish(dw, part);
@@ -349,14 +357,15 @@ __global__ void __launch_bounds__(threads_of<kWaves>()) backward_kernel(Backward
 
 constexpr int kLongThreads = 1024;
 
-// f(at, in_row) for the thread's chunks of a row.
-template <bool kWhole, typename F> __device__ __forceinline__ void chunks_of(int64_t dim, F&& f) {
-  for (int64_t at = static_cast<int64_t>(threadIdx.x) * kChunk; at < dim; at += kLongThreads * kChunk) f(at, in_row<kWhole>(at, dim));
+// f(place) for the thread's chunks of a row.
+template <Width kWidth, typename F> __device__ __forceinline__ void chunks_of(int64_t dim, F&& f) {
+  const int d = static_cast<int>(dim);
+  for (int i = threadIdx.x * kChunk; i < d; i += kLongThreads * kChunk) f(Place<kWidth>(i, d));
 }
 
 // The row is read again for each of its sums (from the caches, where it still fits).  4096 x 20000 in bf16: 98 us forward
 // and 208 backward, where the sums over the rows are a launch of their own.
-template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(ForwardArgs a) {
+template <typename XT, typename WT, Width kWidth> __global__ void __launch_bounds__(kLongThreads) forward_long_kernel(ForwardArgs a) {
   constexpr int kWaves = kLongThreads / kWave;
   __shared__ float slots[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -366,34 +375,34 @@ template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds
     const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
     XT* out = static_cast<XT*>(a.out) + row * a.ldo;
     float sum = 0.0f, square = 0.0f;
-    chunks_of<kWhole>(a.dim, [&](int64_t at, int valid) {
+    chunks_of<kWidth>(a.dim, [&](const Place<kWidth>& p) {
       float v[kChunk], part = 0.0f;
-      widen(load_chunk<kWhole>(x, at, a.dim), v);
+      widen(load_chunk(x, p), v);
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) part += e < valid ? v[e] : 0.0f;
+      for (int e = 0; e < kChunk; ++e) part += p.counts(e) ? v[e] : 0.0f;
       sum += part;
     });
     const float mean = row_sum<kWaves>(sum, slots, 0, wave) / n;
-    chunks_of<kWhole>(a.dim, [&](int64_t at, int valid) {
+    chunks_of<kWidth>(a.dim, [&](const Place<kWidth>& p) {
       float v[kChunk], part = 0.0f;
-      widen(load_chunk<kWhole>(x, at, a.dim), v);
+      widen(load_chunk(x, p), v);
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) part += e < valid ? (v[e] - mean) * (v[e] - mean) : 0.0f;
+      for (int e = 0; e < kChunk; ++e) part += p.counts(e) ? (v[e] - mean) * (v[e] - mean) : 0.0f;
       square += part;
     });
     const float rstd = 1.0f / sqrtf(row_sum<kWaves>(square, slots, 1, wave) / n + a.eps);
-    chunks_of<kWhole>(a.dim, [&](int64_t at, int) {
+    chunks_of<kWidth>(a.dim, [&](const Place<kWidth>& p) {
       float v[kChunk], wv[kChunk], bv[kChunk];
-      widen(load_chunk<kWhole>(x, at, a.dim), v);
-      if (pw) widen(load_chunk<kWhole>(pw, at, a.dim), wv);
-      if (pb) widen(load_chunk<kWhole>(pb, at, a.dim), bv);
+      widen(load_chunk(x, p), v);
+      if (pw) widen(load_chunk(pw, p), wv);
+      if (pb) widen(load_chunk(pb, p), bv);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
         v[e] = (v[e] - mean) * rstd;
         if (pw) v[e] *= wv[e];
         if (pb) v[e] += bv[e];
       }
-      store_chunk<kWhole>(out, at, a.dim, v);
+      store_chunk(out, p, v);
     });
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -402,7 +411,7 @@ template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds
   }
 }
 
-template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds__(kLongThreads) dx_long_kernel(BackwardArgs a) {
+template <typename XT, typename WT, Width kWidth> __global__ void __launch_bounds__(kLongThreads) dx_long_kernel(BackwardArgs a) {
   constexpr int kWaves = kLongThreads / kWave;
   __shared__ float slots[2][kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -413,52 +422,52 @@ template <typename XT, typename WT, bool kWhole> __global__ void __launch_bounds
     XT* dx = static_cast<XT*>(a.dx) + row * a.lddx;
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s0 = 0.0f, s1 = 0.0f;
-    auto load = [&](int64_t at, float (&v)[kChunk], float (&h)[kChunk]) {
-      widen(load_chunk<kWhole>(dout, at, a.dim), v);
-      widen(load_chunk<kWhole>(x, at, a.dim), h);
+    auto load = [&](const Place<kWidth>& p, float (&v)[kChunk], float (&h)[kChunk]) {
+      widen(load_chunk(dout, p), v);
+      widen(load_chunk(x, p), h);
       float wv[kChunk];
-      if (pw) widen(load_chunk<kWhole>(pw, at, a.dim), wv);
+      if (pw) widen(load_chunk(pw, p), wv);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
         if (pw) v[e] *= wv[e];
         h[e] = (h[e] - mean) * rstd;
       }
     };
-    chunks_of<kWhole>(a.dim, [&](int64_t at, int valid) {
+    chunks_of<kWidth>(a.dim, [&](const Place<kWidth>& p) {
       float v[kChunk], h[kChunk], p0 = 0.0f, p1 = 0.0f;
-      load(at, v, h);
+      load(p, v, h);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) {
-        p0 += e < valid ? v[e] : 0.0f;
-        p1 += e < valid ? v[e] * h[e] : 0.0f;
+        p0 += p.counts(e) ? v[e] : 0.0f;
+        p1 += p.counts(e) ? v[e] * h[e] : 0.0f;
       }
       s0 += p0;
       s1 += p1;
     });
     s0 = row_sum<kWaves>(s0, slots, 0, wave) / n;
     s1 = row_sum<kWaves>(s1, slots, 1, wave) / n;
-    chunks_of<kWhole>(a.dim, [&](int64_t at, int) {
+    chunks_of<kWidth>(a.dim, [&](const Place<kWidth>& p) {
       float v[kChunk], h[kChunk];
-      load(at, v, h);
+      load(p, v, h);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) v[e] = (v[e] - s0 - h[e] * s1) * rstd;
-      store_chunk<kWhole>(dx, at, a.dim, v);
+      store_chunk(dx, p, v);
     });
   }
 }
 
 // Sums of dout h and dout over every gridDim.y-th row, a chunk of columns per thread.
-template <typename XT, bool kWhole> __global__ void __launch_bounds__(256) columns_long_kernel(BackwardArgs a) {
-  const int64_t at = (blockIdx.x * int64_t{256} + threadIdx.x) * kChunk;
-  if (at >= a.dim) return;
+template <typename XT, Width kWidth> __global__ void __launch_bounds__(256) columns_long_kernel(BackwardArgs a) {
+  const Place<kWidth> p((blockIdx.x * 256 + threadIdx.x) * kChunk, static_cast<int>(a.dim));
+  if (!p.in) return;
   float dw[kChunk], db[kChunk];
 #pragma unroll
   for (int e = 0; e < kChunk; ++e) dw[e] = db[e] = 0.0f;
 #pragma unroll 4
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     float g[kChunk], h[kChunk];
-    widen(load_chunk<kWhole>(static_cast<const XT*>(a.dout) + row * a.lddo, at, a.dim), g);
-    widen(load_chunk<kWhole>(static_cast<const XT*>(a.x) + row * a.ldx, at, a.dim), h);
+    widen(load_chunk(static_cast<const XT*>(a.dout) + row * a.lddo, p), g);
+    widen(load_chunk(static_cast<const XT*>(a.x) + row * a.ldx, p), h);
     const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) {
@@ -467,8 +476,8 @@ template <typename XT, bool kWhole> __global__ void __launch_bounds__(256) colum
     }
   }
   float* part = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.dim;
-  store_chunk<kWhole>(part, at, a.dim, dw);
-  store_chunk<kWhole>(part + a.dim, at, a.dim, db);
+  store_chunk(part, p, dw);
+  store_chunk(part + a.dim, p, db);
 }
 
 // ------------------------------------------------------------------ joining the groups' sums
@@ -549,15 +558,21 @@ int64_t backward_groups(int64_t rows, int64_t dim) { return groups_of(rows, dim 
 template <typename XT, typename WT> int launch_forward(const ForwardArgs& a, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(forward_groups(a.rows, a.dim)));
   if (a.dim > kLongDim) {
-    if (a.dim % kChunk == 0) hipLaunchKernelGGL((forward_long_kernel<XT, WT, true>), grid, dim3(kLongThreads), 0, s, a);
-    else hipLaunchKernelGGL((forward_long_kernel<XT, WT, false>), grid, dim3(kLongThreads), 0, s, a);
+    if (a.dim % kChunk == 0) hipLaunchKernelGGL((forward_long_kernel<XT, WT, kWhole>), grid, dim3(kLongThreads), 0, s, a);
+    else hipLaunchKernelGGL((forward_long_kernel<XT, WT, kRagged>), grid, dim3(kLongThreads), 0, s, a);
     return launch_status();
   }
   return forward_shape(a.dim, [&](auto shape) {
     constexpr int kW = decltype(shape)::kWaves, kC = decltype(shape)::kChunks;
     const dim3 block(threads_of<kW>());
-    if (a.dim % kChunk == 0) hipLaunchKernelGGL((forward_kernel<XT, WT, kW, kC, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((forward_kernel<XT, WT, kW, kC, false>), grid, block, 0, s, a);
+    if constexpr (kW == 1 && kC == 1) {
+      if (a.dim < kChunk) {
+        hipLaunchKernelGGL((forward_kernel<XT, WT, kW, kC, kShort>), grid, block, 0, s, a);
+        return launch_status();
+      }
+    }
+    if (a.dim % kChunk == 0) hipLaunchKernelGGL((forward_kernel<XT, WT, kW, kC, kWhole>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((forward_kernel<XT, WT, kW, kC, kRagged>), grid, block, 0, s, a);
     return launch_status();
   });
 }
@@ -567,19 +582,25 @@ template <typename XT, typename WT> int launch_backward(const BackwardArgs& a, h
   if (a.dim > kLongDim) {
     const dim3 columns(static_cast<unsigned>(ceil_div(a.dim, 256 * kChunk)), groups), block(kLongThreads);
     if (a.dim % kChunk == 0) {
-      if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT, true>), dim3(groups), block, 0, s, a);
-      if (a.part) hipLaunchKernelGGL((columns_long_kernel<XT, true>), columns, dim3(256), 0, s, a);
+      if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT, kWhole>), dim3(groups), block, 0, s, a);
+      if (a.part) hipLaunchKernelGGL((columns_long_kernel<XT, kWhole>), columns, dim3(256), 0, s, a);
     } else {
-      if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT, false>), dim3(groups), block, 0, s, a);
-      if (a.part) hipLaunchKernelGGL((columns_long_kernel<XT, false>), columns, dim3(256), 0, s, a);
+      if (a.dx) hipLaunchKernelGGL((dx_long_kernel<XT, WT, kRagged>), dim3(groups), block, 0, s, a);
+      if (a.part) hipLaunchKernelGGL((columns_long_kernel<XT, kRagged>), columns, dim3(256), 0, s, a);
     }
     return launch_status();
   }
   return backward_shape(a.dim, [&](auto shape) {
     constexpr int kW = decltype(shape)::kWaves, kC = decltype(shape)::kChunks;
     const dim3 block(threads_of<kW>());
-    if (a.dim % kChunk == 0) hipLaunchKernelGGL((backward_kernel<XT, WT, kW, kC, true>), dim3(groups), block, 0, s, a);
-    else hipLaunchKernelGGL((backward_kernel<XT, WT, kW, kC, false>), dim3(groups), block, 0, s, a);
+    if constexpr (kW == 1 && kC == 1) {
+      if (a.dim < kChunk) {
+        hipLaunchKernelGGL((backward_kernel<XT, WT, kW, kC, kShort>), dim3(groups), block, 0, s, a);
+        return launch_status();
+      }
+    }
+    if (a.dim % kChunk == 0) hipLaunchKernelGGL((backward_kernel<XT, WT, kW, kC, kWhole>), dim3(groups), block, 0, s, a);
+    else hipLaunchKernelGGL((backward_kernel<XT, WT, kW, kC, kRagged>), dim3(groups), block, 0, s, a);
     return launch_status();
   });
 }

@@ -27,7 +27,7 @@ HALF = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
 SIZES = [(1, 1), (3, 2), (1, 16), (3, 7), (5, 512), (4, 513), (7, 1000), (2, 1024), (3, 1025), (9, 2048), (601, 2047),
          (1030, 600), (5, 4096), (3, 4099), (2, 8192), (2, 8200), (3, 16384), (2, 16383), (2, 16391), (3, 20000),
          (2500, 40), (530, 2500), (3, 4104), (600, 5121), (520, 6144), (2, 6145), (300, 9000), (270, 10241), (3, 12288), (2, 12289),
-         (3, 24569), (300, 16392)]
+         (3, 24569), (300, 16392), (4, 9), (700, 15), (9, 511), (70, 5), (2049, 8), (300, 1023), (40, 8193)]
 
 
 @pytest.fixture(scope="module")
