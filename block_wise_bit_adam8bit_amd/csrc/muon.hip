@@ -44,7 +44,9 @@ constexpr double kExactA = 3.4445, kExactB = -4.775, kExactC = 2.0315;
 constexpr float kA = kExactA, kB = kExactB, kC = kExactC;
 constexpr int kExp = 12, kExpQ = 10;  // powers of two of X, A, P and P A, and of a product Q
 constexpr int kMaxJobs = 32;          // of one launch (its arguments are 4 KB at most)
-constexpr int kMaxParts = 512;        // partial sums of squares per matrix
+// Workgroups, and partial sums of squares, per matrix at most: with codes, whose encoder's chains want more of them on a CU,
+// 1024 (six matrices of 58.7 M elements 107 us; 512 of each 123), without 512 (4096 x 11008 145 us; 1024 152).
+constexpr int kMaxParts = 512, kMaxCodedParts = 1024;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -110,7 +112,7 @@ enum Source : int { kPlain = 0, kMomentum32 = 1, kMomentum8 = 2 };
 // Blocks of 2048 of one matrix (blockIdx.y), every groups-th by a workgroup: the new momentum, the update u
 // and its sum of squares (binary64: squares of any binary32 numbers neither overflow nor vanish).
 // Bound by memory: 4096 x 11008 with binary32 momentum, 631 MB, 140 to 145 us, 4.4 TB/s; with codes, 58.7 M parameters in six
-// matrices, 124 us for 470 MB, in which the encoder's search shows.
+// matrices, 107 us for 470 MB, also 4.4 TB/s.  (Loading the next block before this one's work took 10 to 30 % longer.)
 template <typename GT, int kSource> __global__ void __launch_bounds__(256) source_kernel(SourceArgs a) {
   __shared__ __align__(16) qopt_codebook cb;  // kMomentum8
   __shared__ double slots[4];
@@ -301,7 +303,8 @@ struct PackArgs {
 
 // X = U 2^kExp / max(|U|, eps) and its transpose.  A wave takes 64 x 64 values, a lane 8 x 8 of them:
 // it reads 8 runs of 8, writes them as 8 places of the operand's rows, and of the transpose's; the lanes next
-// to each other make runs of 256 bytes either way.  4096 x 11008 in kWide, 541 MB: 122 to 126 us, 4.4 TB/s.
+// to each other make runs of 256 bytes either way.  4096 x 11008 in kWide, 541 MB: 109 to 113 us, 4.9 TB/s (122 to 126 with
+// a branch at every row).
 template <typename ST, int kForm> __global__ void __launch_bounds__(256) pack_kernel(PackArgs a) {
   __shared__ double slots[4];
   int j = 0;
@@ -318,15 +321,26 @@ template <typename ST, int kForm> __global__ void __launch_bounds__(256) pack_ke
   if (c0 >= padded(job.cols)) return;  // r0 lies within the padded rows always
   float v[8][8];
   const ST* src = static_cast<const ST*>(job.src);
+  if (r0 - 8 * (lane >> 3) + 64 <= job.rows && c0 - 8 * (lane & 7) + 64 <= job.cols) {
+    // all of the wave's values lie in the matrix: no branch between the loads
+    ST w[8][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (r0 + i < job.rows) {
-      load8(src + (r0 + i) * job.cols, c0, job.cols, v[i]);
+    for (int i = 0; i < 8; ++i) __builtin_memcpy(w[i], src + (r0 + i) * job.cols + c0, sizeof(w[i]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = c0 + e < job.cols ? static_cast<float>(static_cast<double>(v[i][e]) * scale) : 0.0f;
-    } else {
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) v[i][e] = static_cast<float>(static_cast<double>(to_f32(w[i][e])) * scale);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i < job.rows) {
+        load8(src + (r0 + i) * job.cols, c0, job.cols, v[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = c0 + e < job.cols ? static_cast<float>(static_cast<double>(v[i][e]) * scale) : 0.0f;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+      }
     }
   }
 #pragma unroll
@@ -971,7 +985,7 @@ uint8_t* lay_out(Matrix& a, uint8_t* at) {
     at += up(bytes);
     return p;
   };
-  a.parts = reinterpret_cast<double*>(take(kMaxParts * 8));
+  a.parts = reinterpret_cast<double*>(take(kMaxCodedParts * 8));
   if (a.m <= kTiny) {
     a.u = reinterpret_cast<float*>(take(a.rows * a.cols * 4));
     a.tiny_parts = reinterpret_cast<double*>(take(kTinyParts * a.m * a.m * 8));
@@ -1210,7 +1224,7 @@ int run_source(Matrix* mats, int count, const Run& r) {
   for (int i = 0; i < count; ++i) {
     Matrix& m = mats[i];
     const int64_t n = m.rows * m.cols;
-    m.groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(n, QOPT_BLOCK), kMaxParts));
+    m.groups = static_cast<uint32_t>(std::min<int64_t>(ceil_div(n, QOPT_BLOCK), r.source == kMomentum8 ? kMaxCodedParts : kMaxParts));
     most = std::max(most, m.groups);
     a.jobs[i] = {m.src, m.moment, m.absmax, m.u, m.parts, n, m.groups};
   }
