@@ -355,7 +355,6 @@ template <int kFm, int kFn> struct Fp4Op {
     uint32_t a[kFm], b[kFn];
   };
   static constexpr int kSideLoads = 2;
-  static constexpr bool kCross = false;
   static constexpr int terms(int) { return 2; }
   __amdgpu_buffer_rsrc_t sa, sb;
   uint32_t at_a, at_b, step_a, step_b;

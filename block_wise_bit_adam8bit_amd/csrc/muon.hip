@@ -14,14 +14,10 @@
 // bits four in one group end in infinities where eight directions are 170 times the rest.)
 //
 // Numbers.  A value is kept times a power of two that holds the largest possible one (|X| <= 1.203, A <= 1.45,
-// P <= 3.4445, Q <= 3.4445^3) under 65504, in one of three forms:
-//   kWide    hi + lo, two binary16 numbers: 22 bits, or 23.  hi hi + hi lo + lo hi with binary32 sums leaves out 2^-22
-//            of a product.  For binary32 destinations.
-//   kMiddle  hi, and hi and lo rounded to e4m3 once more: hi hi in binary16, hi lo + lo hi in one 8-bit instruction,
-//            which is off by 2^-15 of a product at two thirds of the time.  For bfloat16 destinations, whose last
-//            iterations round more than that: 8e-4 to 2.8e-3 of the result, with kWide in its place 7e-4 to 2.5e-3.
-//   kNarrow  hi alone, 11 bits, a third of kWide's time.  The last iterations, at most two, of a bfloat16 destination:
-//            singular values are near 1 there.  (All of them in kNarrow: 2e-3 to 2.4e-2.)
+// P <= 3.4445, Q <= 3.4445^3) under 65504, as hi + lo, two binary16 numbers: 22 bits, or 23, down to 2^-24, under which lo
+// ends: 2^-36 of X's largest possible value.  A product is hi hi + hi lo + lo hi with binary32 sums, which leaves out 2^-22
+// of it.  That holds for either destination: fewer bits would be faster (hi alone a third of the time) and next to a bfloat16
+// result's own rounding as large as it, 8e-4 to 2.4e-2 of the result.
 
 #include <hip/hip_runtime.h>
 
@@ -52,16 +48,11 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-// A matrix as an operand: rows of a multiple of 64 values, in pieces of 16 bytes as a product's lanes take them.
-//   kWide    for every 8 values one piece of hi and one of lo
-//   kMiddle  for every 32 values hi of 16 of them, e4m3 of all their hi / 2^7, hi of the other 16, and e4m3 of all
-//            their lo 2^4: two pieces each
-//   kNarrow  2 bytes per value
-enum Form : int { kWide, kMiddle, kNarrow };
+// A matrix as an operand: rows of a multiple of 64 values, for every 8 of them one piece of 16 bytes of hi and one of
+// lo, as a product's lanes take them.
 constexpr int64_t kPad = 64;
 __host__ __device__ constexpr int64_t padded(int64_t d) { return ceil_div(d, kPad) * kPad; }
-__host__ __device__ constexpr int64_t row_bytes(int64_t cols, int form) { return padded(cols) * (form == kNarrow ? 2 : 4); }
-constexpr float kHi8 = 128.0f, kLo8 = 0.0625f;  // what the e4m3 numbers are multiples of
+__host__ __device__ constexpr int64_t row_bytes(int64_t cols) { return padded(cols) * 4; }
 
 // ------------------------------------------------------------------ momentum and norms
 
@@ -215,77 +206,29 @@ template <typename GT, int kSource> __global__ void __launch_bounds__(256) sourc
 
 // ------------------------------------------------------------------ operands from the update
 
-typedef short s16x2 __attribute__((ext_vector_type(2)));
-
-// Four values over a power of two as e4m3.  None exceeds 448 of them.
-__device__ __forceinline__ uint32_t e4m3(float a, float b, float c, float d, float scale) {
-  s16x2 w = {0, 0};
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
-  return __builtin_bit_cast(uint32_t, w);
-}
-
 template <int kCount> struct HalfVec;
 template <> struct HalfVec<2> { typedef f16x2 type; };
 template <> struct HalfVec<4> { typedef f16x4 type; };
 template <> struct HalfVec<8> { typedef f16x8 type; };
 
 // kCount consecutive values of an operand's row, from place `at` on: a multiple of kCount.
-template <int kForm, int kCount> __device__ __forceinline__ void write_run(uint8_t* row, int64_t at, const float (&v)[kCount]) {
+template <int kCount> __device__ __forceinline__ void write_run(uint8_t* row, int64_t at, const float (&v)[kCount]) {
   typename HalfVec<kCount>::type hi, lo;
-  float h[kCount], l[kCount];
 #pragma unroll
   for (int e = 0; e < kCount; ++e) {
     hi[e] = static_cast<_Float16>(v[e]);
-    h[e] = static_cast<float>(hi[e]);
-    l[e] = v[e] - h[e];
-    lo[e] = static_cast<_Float16>(l[e]);
+    lo[e] = static_cast<_Float16>(v[e] - static_cast<float>(hi[e]));
   }
-  if constexpr (kForm == kNarrow) {
-    __builtin_memcpy(row + at * 2, &hi, sizeof(hi));
-  } else if constexpr (kForm == kWide) {
-    uint8_t* to = row + (at >> 3) * 32 + (at & 7) * 2;
-    __builtin_memcpy(to, &hi, sizeof(hi));
-    __builtin_memcpy(to + 16, &lo, sizeof(lo));
-  } else {
-    uint8_t* group = row + (at >> 5) * 128;
-    __builtin_memcpy(group + ((at >> 4) & 1) * 64 + (at & 15) * 2, &hi, sizeof(hi));
-    uint32_t h8[(kCount + 3) / 4], l8[(kCount + 3) / 4];
-#pragma unroll
-    for (int e = 0; e < kCount; e += 4) {
-      auto both = [&](const float (&x)[kCount], float scale) {
-        return e4m3(x[e], x[e + 1], kCount > 2 ? x[(e + 2) % kCount] : 0.0f, kCount > 2 ? x[(e + 3) % kCount] : 0.0f, scale);
-      };
-      h8[e / 4] = both(h, kHi8);
-      l8[e / 4] = both(l, kLo8);
-    }
-    __builtin_memcpy(group + 32 + (at & 31), h8, kCount);
-    __builtin_memcpy(group + 96 + (at & 31), l8, kCount);
-  }
+  uint8_t* to = row + (at >> 3) * 32 + (at & 7) * 2;
+  __builtin_memcpy(to, &hi, sizeof(hi));
+  __builtin_memcpy(to + 16, &lo, sizeof(lo));
 }
 
 // Eight values of an operand's row, from place `at` on: a multiple of 8.
-template <int kForm> __device__ __forceinline__ void read_run(const uint8_t* row, int64_t at, float (&v)[8]) {
-  f16x8 hi;
-  if constexpr (kForm == kMiddle) {
-    const uint8_t* group = row + (at >> 5) * 128;
-    hi = *reinterpret_cast<const f16x8*>(group + ((at >> 4) & 1) * 64 + (at & 15) * 2);
-    const uint32_t l0 = *reinterpret_cast<const uint32_t*>(group + 96 + (at & 31)), l1 = *reinterpret_cast<const uint32_t*>(group + 100 + (at & 31));
-    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(l0, kLo8, false), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(l0, kLo8, true);
-    const auto c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(l1, kLo8, false), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(l1, kLo8, true);
-    const float lo[8] = {a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+__device__ __forceinline__ void read_run(const uint8_t* row, int64_t at, float (&v)[8]) {
+  const f16x8 hi = *reinterpret_cast<const f16x8*>(row + at * 4), lo = *reinterpret_cast<const f16x8*>(row + at * 4 + 16);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(hi[e]) + lo[e];
-  } else if constexpr (kForm == kWide) {
-    hi = *reinterpret_cast<const f16x8*>(row + at * 4);
-    const f16x8 lo = *reinterpret_cast<const f16x8*>(row + at * 4 + 16);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
-  } else {
-    hi = *reinterpret_cast<const f16x8*>(row + at * 2);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(hi[e]);
-  }
+  for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(hi[e]) + static_cast<float>(lo[e]);
 }
 
 struct PackJob {
@@ -303,9 +246,9 @@ struct PackArgs {
 
 // X = U 2^kExp / max(|U|, eps) and its transpose.  A wave takes 64 x 64 values, a lane 8 x 8 of them:
 // it reads 8 runs of 8, writes them as 8 places of the operand's rows, and of the transpose's; the lanes next
-// to each other make runs of 256 bytes either way.  4096 x 11008 in kWide, 541 MB: 109 to 113 us, 4.9 TB/s (122 to 126 with
+// to each other make runs of 256 bytes either way.  4096 x 11008, 541 MB: 109 to 113 us, 4.9 TB/s (122 to 126 with
 // a branch at every row).
-template <typename ST, int kForm> __global__ void __launch_bounds__(256) pack_kernel(PackArgs a) {
+template <typename ST> __global__ void __launch_bounds__(256) pack_kernel(PackArgs a) {
   __shared__ double slots[4];
   int j = 0;
   while (j + 1 < a.njobs && blockIdx.x >= a.jobs[j + 1].first) ++j;
@@ -345,13 +288,13 @@ template <typename ST, int kForm> __global__ void __launch_bounds__(256) pack_ke
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (r0 + i < job.rows) write_run<kForm, 8>(job.same + (r0 + i) * row_bytes(job.cols, kForm), c0, v[i]);
+    if (r0 + i < job.rows) write_run<8>(job.same + (r0 + i) * row_bytes(job.cols), c0, v[i]);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = v[i][e];
-    if (c0 + e < job.cols) write_run<kForm, 8>(job.other + (c0 + e) * row_bytes(job.rows, kForm), r0, t);
+    if (c0 + e < job.cols) write_run<8>(job.other + (c0 + e) * row_bytes(job.rows), r0, t);
   }
 }
 
@@ -388,26 +331,17 @@ enum Epilogue : int {
   kUpdate       // dst = dst * decay - factor l r^T * rate
 };
 
-template <int kForm> struct HalfOp {
+// A lane's two pieces of a fragment are hi and lo of the same 8 values.
+struct HalfOp {
   struct Side {};
   static constexpr int kSideLoads = 0;
-  static constexpr bool kCross = kForm == kMiddle;
-  static constexpr int terms(int half) { return kForm == kWide ? 3 : kForm == kMiddle && half == 1 ? 1 : 2; }
+  static constexpr int terms(int) { return 3; }
   __device__ __forceinline__ Side load(int) const { return {}; }
   static __device__ __forceinline__ void touch(Side&) {}
-  // kWide: pieces 0 and 1 are hi and lo of 8 values; kNarrow and half 0 of kMiddle: two times 8 values; half 1 of
-  // kMiddle: the e4m3 numbers of 32 values, hi in lanes (r, 0) of a and (r, 1) of b, lo in the others
   template <int kHalf, int kTerm, int kI, int kJ>
   static __device__ __forceinline__ void multiply(f32x16& acc, const i32x4 (&a)[2], const i32x4 (&b)[2], const Side&) {
-    if constexpr (kCross && kHalf == 1) {
-      // formats 0: e4m3; scales of 2^3 and 1 undo / kHi8 and / kLo8
-      acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(__builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7),
-                                                            __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7), acc, 0, 0, 0,
-                                                            130, 0, 127);
-    } else {
-      constexpr int kL = kForm == kWide ? kTerm == 2 : kTerm, kR = kForm == kWide ? kTerm == 1 : kTerm;
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b[kR]), __builtin_bit_cast(f16x8, a[kL]), acc, 0, 0, 0);
-    }
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b[kTerm == 1]), __builtin_bit_cast(f16x8, a[kTerm == 2]), acc,
+                                                 0, 0, 0);
   }
 };
 
@@ -418,9 +352,8 @@ template <typename OT> __device__ __forceinline__ void load_out(const OT* p, flo
   for (int e = 0; e < 8; ++e) v[e] = to_f32(w[e]);
 }
 
-// What a tile's sums become: quarter q of its columns.  s[i][j][e] is acc[i][j][4 q + e].  kOut: the result's
-// form; the polynomial's A has the same.
-template <typename T, int kWavesN, int kOut, int kEpilogue, typename OT>
+// What a tile's sums become: quarter q of its columns.  s[i][j][e] is acc[i][j][4 q + e].
+template <typename T, int kWavesN, int kEpilogue, typename OT>
 __device__ __forceinline__ void finish(const Job& job, float decay, int64_t m0, int64_t n0, int q, const f32x4 (&s)[T::kFm][2]) {
   constexpr int kFm = T::kFm;
   static_assert(T::kFn == 2, "a lane's columns are eight places of an operand's row");
@@ -441,7 +374,7 @@ __device__ __forceinline__ void finish(const Job& job, float decay, int64_t m0, 
     if constexpr (kEpilogue == kPolynomial) {
       if (row < job.lrows && col < pn) {
         float x[8];
-        read_run<kOut>(job.add + row * job.k_bytes, col, x);
+        read_run(job.add + row * job.k_bytes, col, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           v[i][e] = v[i][e] * kC + x[e] * kB + (row == col + e ? kA * static_cast<float>(1 << kExp) : 0.0f);
@@ -470,7 +403,7 @@ __device__ __forceinline__ void finish(const Job& job, float decay, int64_t m0, 
         }
       }
     } else {
-      if (row < job.lrows && col < pn) write_run<kOut, 8>(job.out + row * job.out_bytes, col, v[i]);
+      if (row < job.lrows && col < pn) write_run<8>(job.out + row * job.out_bytes, col, v[i]);
     }
   }
   // the mirror image, or the transpose: rows of the result are places there, up to the padding
@@ -483,7 +416,7 @@ __device__ __forceinline__ void finish(const Job& job, float decay, int64_t m0, 
         float t[kFm];
 #pragma unroll
         for (int i = 0; i < kFm; ++i) t[i] = v[i][e];
-        if (col + e < job.rrows) write_run<kOut, kFm>(out + (col + e) * bytes, row0, t);
+        if (col + e < job.rrows) write_run<kFm>(out + (col + e) * bytes, row0, t);
       }
     }
   }
@@ -512,25 +445,23 @@ __device__ __forceinline__ uint32_t run_start(const ProductArgs& a, uint32_t w) 
   return a.first_step + static_cast<uint32_t>(static_cast<uint64_t>(a.shared) * w / a.workers);
 }
 
-template <bool kBig, typename Op> struct TileOf {
+template <bool kBig> struct TileOf {
   static constexpr int kSide = kBig ? 256 : 128, kWavesN = kBig ? 4 : 2;
-  typedef Tile<kSide, kSide, 2, kWavesN, kBig ? 2 : 3, Op> T;
+  typedef Tile<kSide, kSide, 2, kWavesN, kBig ? 2 : 3, HalfOp> T;
   static constexpr int kQuarter = T::kFm * 2 * T::kThreads;  // f32x4 of a quarter of the columns
 };
 
-// kIn: the operands' form; kOut: the result's.
-//
 // Whole tiles leave CUs idle in the last round: 136 tiles of 256 x 256 below the diagonal of 4096 x 4096 use
 // half of the chip.  Runs of equal length over the tiles' steps use all of it; a tile that lies in several runs is
 // joined by a launch of its own, which reads the runs' sums in their order and does what follows a product.
 //
-// Measured: Q X of 4096 x 4096 x 11008 in kWide 920 to 980 us, 1.2 PFLOP/s of single numbers (three instructions each),
+// Measured: Q X of 4096 x 4096 x 11008 920 to 1000 us, 1.2 PFLOP/s of single numbers (three instructions each),
 // the matrix units busy 79 to 81 % of the CUs' time at 1.7 GHz, which is where the chip's power holds the clock: that is what
 // bounds it.  X X^T of the same: 360 us, and 26 to join.  A symmetric product of 4096 x 4096: 170 to 183 us, and 38
-// to join.  Four of 2048 x 2048 in kMiddle: 104 to 120 us, matrix units busy 56 % of 144 CUs' time; in kNarrow 52 to 56 and 65 %.
-template <bool kBig, int kIn, int kOut, int kEpilogue, typename OT>
+// to join.  Four of 2048 x 2048: 126 to 142 us on 144 CUs, whose matrix units are busy 78 % of the time.
+template <bool kBig, int kEpilogue, typename OT>
 __global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a) {
-  typedef TileOf<kBig, HalfOp<kIn>> O;
+  typedef TileOf<kBig> O;
   typedef typename O::T T;
   __shared__ __align__(16) uint8_t lds[T::kLds];
   auto sums = [&](const Job& job, uint32_t tile, int first, int last, int64_t& m0, int64_t& n0, typename T::Acc& acc) {
@@ -538,7 +469,7 @@ __global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a
     tile_at<kEpilogue>(job, tile, tm, tn);
     m0 = static_cast<int64_t>(tm) * O::kSide;
     n0 = static_cast<int64_t>(tn) * O::kSide;
-    T::sums({job.l, m0, job.lrows, job.k_bytes}, {job.r, n0, job.rrows, job.k_bytes}, HalfOp<kIn>{}, lds, first, last, acc);
+    T::sums({job.l, m0, job.lrows, job.k_bytes}, {job.r, n0, job.rrows, job.k_bytes}, HalfOp{}, lds, first, last, acc);
   };
   auto quarter = [](const typename T::Acc& acc, int q, f32x4 (&s)[T::kFm][2]) {
 #pragma unroll
@@ -574,7 +505,7 @@ __global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a
       for (int q = 0; q < 4; ++q) {
         f32x4 s[T::kFm][2];
         quarter(acc, q, s);
-        finish<T, O::kWavesN, kOut, kEpilogue, OT>(job, a.decay, m0, n0, q, s);
+        finish<T, O::kWavesN, kEpilogue, OT>(job, a.decay, m0, n0, q, s);
       }
     } else {
       // at most the first and the last piece of a run are not whole
@@ -596,9 +527,9 @@ __global__ void __launch_bounds__(kBig ? 512 : 256) product_kernel(ProductArgs a
 }
 
 // One quarter (blockIdx.y) of the columns of each tile behind the whole ones that lies in more than one run.
-template <bool kBig, int kOut, int kEpilogue, typename OT>
+template <bool kBig, int kEpilogue, typename OT>
 __global__ void __launch_bounds__(kBig ? 512 : 256) join_kernel(ProductArgs a) {
-  typedef TileOf<kBig, HalfOp<kOut>> O;
+  typedef TileOf<kBig> O;
   typedef typename O::T T;
   const uint32_t tile = a.whole + blockIdx.x;
   int j = 0;
@@ -624,7 +555,7 @@ __global__ void __launch_bounds__(kBig ? 512 : 256) join_kernel(ProductArgs a) {
   }
   uint32_t tm, tn;
   tile_at<kEpilogue>(job, tile - job.first, tm, tn);
-  finish<T, O::kWavesN, kOut, kEpilogue, OT>(job, a.decay, static_cast<int64_t>(tm) * O::kSide, static_cast<int64_t>(tn) * O::kSide,
+  finish<T, O::kWavesN, kEpilogue, OT>(job, a.decay, static_cast<int64_t>(tm) * O::kSide, static_cast<int64_t>(tn) * O::kSide,
                                                   blockIdx.y, s);
 }
 
@@ -646,16 +577,14 @@ struct ChainArgs {
   int length;
 };
 
-template <int kForm> __global__ void __launch_bounds__(256, 1) chain_kernel(ChainArgs args) {
-  constexpr bool kSplit = kForm != kNarrow;  // kMiddle: the products here have room for kWide
-  typedef HalfOp<kSplit ? kWide : kNarrow> Op;
-  constexpr int kSteps = kSplit ? 4 : 2, kStep = 128 * kStepBytes;  // bytes of a step's rows
+__global__ void __launch_bounds__(256, 1) chain_kernel(ChainArgs args) {
+  constexpr int kSteps = 4, kStep = 128 * kStepBytes;  // bytes of a step's rows
   __shared__ __align__(16) uint8_t image[2][kSteps * kStep];
   typedef f32x16 Mat[2][2];
   const ChainJob& job = args.jobs[blockIdx.x];
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), wm = wave / 2, wn = wave % 2;
-  const int64_t bytes = row_bytes(job.m, kForm), pn = padded(job.m);
+  const int64_t bytes = row_bytes(job.m), pn = padded(job.m);
   const uint32_t swizzle = (lane >> 1) & 7;
 
   // f(i, q, row, col) for the lane's runs of eight columns
@@ -677,14 +606,10 @@ template <int kForm> __global__ void __launch_bounds__(256, 1) chain_kernel(Chai
           hi[e] = static_cast<_Float16>(v);
           lo[e] = static_cast<_Float16>(v - static_cast<float>(hi[e]));
         }
-        uint8_t* row = image[b] + (kSplit ? 2 * wn + q / 2 : wn) * kStep + (64 * wm + 32 * i + r) * kStepBytes;
-        if constexpr (kSplit) {
-          const uint32_t piece = 2 * (2 * (q & 1) + h);
-          *reinterpret_cast<f16x8*>(row + ((piece ^ swizzle) << 4)) = hi;
-          *reinterpret_cast<f16x8*>(row + (((piece + 1) ^ swizzle) << 4)) = lo;
-        } else {
-          *reinterpret_cast<f16x8*>(row + (((2 * q + h) ^ swizzle) << 4)) = hi;
-        }
+        uint8_t* row = image[b] + (2 * wn + q / 2) * kStep + (64 * wm + 32 * i + r) * kStepBytes;
+        const uint32_t piece = 2 * (2 * (q & 1) + h);
+        *reinterpret_cast<f16x8*>(row + ((piece ^ swizzle) << 4)) = hi;
+        *reinterpret_cast<f16x8*>(row + (((piece + 1) ^ swizzle) << 4)) = lo;
       }
   };
   // x = factor times the product of images l and r
@@ -707,15 +632,14 @@ template <int kForm> __global__ void __launch_bounds__(256, 1) chain_kernel(Chai
           b[f][e] = *reinterpret_cast<const i32x4*>(image[br] + 64 * wn * kStepBytes + at);
         }
       // lo lo too: small matrices are where it shows
-      if constexpr (kSplit)
+      each_pair<2, 2>([&](auto i, auto j) {
+        constexpr int I = decltype(i)::value, J = decltype(j)::value;
+        x[I][J] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b[J][1]), __builtin_bit_cast(f16x8, a[I][1]), x[I][J], 0, 0, 0);
+      });
+      each<HalfOp::terms(0)>([&](auto term) {
         each_pair<2, 2>([&](auto i, auto j) {
           constexpr int I = decltype(i)::value, J = decltype(j)::value;
-          x[I][J] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b[J][1]), __builtin_bit_cast(f16x8, a[I][1]), x[I][J], 0, 0, 0);
-        });
-      each<Op::terms(0)>([&](auto term) {
-        each_pair<2, 2>([&](auto i, auto j) {
-          constexpr int I = decltype(i)::value, J = decltype(j)::value;
-          Op::template multiply<0, decltype(term)::value, I, J>(x[I][J], a[I], b[J], {});
+          HalfOp::multiply<0, decltype(term)::value, I, J>(x[I][J], a[I], b[J], {});
         });
       });
     }
@@ -730,7 +654,7 @@ template <int kForm> __global__ void __launch_bounds__(256, 1) chain_kernel(Chai
   Mat a, p, q, x;
   runs([&](int i, int c, int row, int col) {
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (row < job.m && col < pn) read_run<kForm>(job.a + row * bytes, col, v);
+    if (row < job.m && col < pn) read_run(job.a + row * bytes, col, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) a[i][e & 1][4 * c + e / 2] = v[e];
   });
@@ -780,7 +704,7 @@ template <int kForm> __global__ void __launch_bounds__(256, 1) chain_kernel(Chai
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = q[i][e & 1][4 * c + e / 2];
-    if (row < job.m && col < pn) write_run<kForm, 8>(job.q + row * bytes, col, v);
+    if (row < job.m && col < pn) write_run<8>(job.q + row * bytes, col, v);
   });
 }
 
@@ -992,11 +916,11 @@ uint8_t* lay_out(Matrix& a, uint8_t* at) {
     a.tiny_q = reinterpret_cast<double*>(take(a.m * a.m * 8));
     return at;
   }
-  a.x = take(a.m * row_bytes(a.n, kWide));
-  a.xt[0] = take(a.n * row_bytes(a.m, kWide));
-  a.xt[1] = take(a.n * row_bytes(a.m, kWide));
+  a.x = take(a.m * row_bytes(a.n));
+  a.xt[0] = take(a.n * row_bytes(a.m));
+  a.xt[1] = take(a.n * row_bytes(a.m));
   a.u = reinterpret_cast<float*>(a.xt[1]);
-  for (uint8_t** b : {&a.g, &a.p, &a.h, &a.q[0], &a.q[1]}) *b = take(a.m * row_bytes(a.m, kWide));
+  for (uint8_t** b : {&a.g, &a.p, &a.h, &a.q[0], &a.q[1]}) *b = take(a.m * row_bytes(a.m));
   return at;
 }
 
@@ -1045,11 +969,11 @@ template <typename GT> void launch_source(const SourceArgs& a, int source, dim3 
   else hipLaunchKernelGGL((source_kernel<GT, kMomentum8>), grid, dim3(256), 0, s, a);
 }
 
-template <bool kBig, int kIn, int kOut, int kEpilogue, typename OT = float>
+template <bool kBig, int kEpilogue, typename OT = float>
 void launch_product(const ProductArgs& a, hipStream_t s) {
   const dim3 block(kBig ? 512 : 256);
-  hipLaunchKernelGGL((product_kernel<kBig, kIn, kOut, kEpilogue, OT>), dim3(a.whole + a.workers), block, 0, s, a);
-  if (a.rest) hipLaunchKernelGGL((join_kernel<kBig, kOut, kEpilogue, OT>), dim3(a.rest, 4), block, 0, s, a);
+  hipLaunchKernelGGL((product_kernel<kBig, kEpilogue, OT>), dim3(a.whole + a.workers), block, 0, s, a);
+  if (a.rest) hipLaunchKernelGGL((join_kernel<kBig, kEpilogue, OT>), dim3(a.rest, 4), block, 0, s, a);
 }
 
 constexpr int64_t kCus = 256;
@@ -1059,26 +983,24 @@ constexpr int64_t kLeastRun = 8;  // steps
 struct Launch {
   ProductArgs args = {};
   int epilogue;
-  int form, form_out;
   int dst_dtype = QOPT_F32;
   bool big = false;
 
-  Launch(int e, int in, int out) : epilogue(e), form(in), form_out(out) {}
+  explicit Launch(int e) : epilogue(e) {}
   bool symmetric() const { return epilogue == kSymmetric || epilogue == kPolynomial; }
   void add(const Job& j) { args.jobs[args.njobs++] = j; }
   int64_t part_bytes() const { return big ? 256 * 256 * 4 : 128 * 128 * 4; }
   int64_t parts() const { return up(2 * static_cast<int64_t>(args.workers) * part_bytes()); }
 
   // Tiles of one size, whole or with the last round's steps shared; returns the time by this model, in
-  // microseconds.  A step takes a CU 0.72 for a tile of 128 x 128, and for one of 256 x 256 1.8 (1.7 with single
-  // numbers) while half of the CUs are idle, and 0.95 and 2.7 (2.3) with all of them busy: the chip's power then holds its
-  // clock at 1.7 GHz (2.4), so that idle CUs in the last round cost less than they seem to.
+  // microseconds.  A step takes a CU 0.72 for a tile of 128 x 128 and 1.8 for one of 256 x 256 while half of the CUs are
+  // idle, and 0.95 and 2.7 with all of them busy: the chip's power then holds its clock at 1.7 GHz (2.4), so that
+  // idle CUs in the last round cost less than they seem to.
   // Sharing costs a launch (12) and the partial sums' way to memory and back (6 TB/s).
   double cut(bool large, bool share) {
     big = large;
     const int64_t side = large ? 256 : 128;
-    const double fast = large ? (form == kWide ? 1.8 : 1.7) : 0.72;
-    const double busy = large ? (form == kWide ? 2.7 : 2.3) : 0.95;
+    const double fast = large ? 1.8 : 0.72, busy = large ? 2.7 : 0.95;
     int64_t tiles = 0, steps = 0, longest = 0;
     bool even = true;
     for (int i = 0; i < args.njobs; ++i) {
@@ -1132,15 +1054,13 @@ struct Launch {
   template <bool kBig> int pick(hipStream_t s) {
     switch (epilogue) {
       case kSymmetric:
-        same<kBig, kSymmetric>(s);
+        launch_product<kBig, kSymmetric>(args, s);
         break;
       case kPolynomial:
-        same<kBig, kPolynomial>(s);
+        launch_product<kBig, kPolynomial>(args, s);
         break;
       case kApply:
-        if (form == kWide) launch_product<kBig, kWide, kWide, kApply>(args, s);
-        else if (form_out == kMiddle) launch_product<kBig, kMiddle, kMiddle, kApply>(args, s);
-        else launch_product<kBig, kMiddle, kNarrow, kApply>(args, s);
+        launch_product<kBig, kApply>(args, s);
         break;
       case kResult:
         last<kBig, kResult>(s);
@@ -1150,28 +1070,22 @@ struct Launch {
     }
     return launch_status();
   }
-  template <bool kBig, int kEpilogue> void same(hipStream_t s) {
-    if (form == kWide) launch_product<kBig, kWide, kWide, kEpilogue>(args, s);
-    else if (form == kMiddle) launch_product<kBig, kMiddle, kMiddle, kEpilogue>(args, s);
-    else launch_product<kBig, kNarrow, kNarrow, kEpilogue>(args, s);
-  }
   template <bool kBig, int kEpilogue> void last(hipStream_t s) {
-    if (dst_dtype == QOPT_F32) launch_product<kBig, kWide, kWide, kEpilogue, float>(args, s);
-    else if (form == kMiddle) launch_product<kBig, kMiddle, kMiddle, kEpilogue, uint16_t>(args, s);
-    else launch_product<kBig, kNarrow, kNarrow, kEpilogue, uint16_t>(args, s);
+    if (dst_dtype == QOPT_F32) launch_product<kBig, kEpilogue, float>(args, s);
+    else launch_product<kBig, kEpilogue, uint16_t>(args, s);
   }
 };
 
 float power(int e) { return std::ldexp(1.0f, e); }
 
 // l r^T with l [lrows, k], r [rrows, k] as operands; its result has the exponent `to`.
-Job job_of(const uint8_t* l, int64_t lrows, const uint8_t* r, int64_t rrows, int64_t k, int form, int exp_in, int to) {
+Job job_of(const uint8_t* l, int64_t lrows, const uint8_t* r, int64_t rrows, int64_t k, int exp_in, int to) {
   Job j = {};
   j.l = l;
   j.r = r;
   j.lrows = static_cast<int32_t>(lrows);
   j.rrows = static_cast<int32_t>(rrows);
-  j.k_bytes = static_cast<uint32_t>(row_bytes(k, form));
+  j.k_bytes = static_cast<uint32_t>(row_bytes(k));
   j.factor = power(to - exp_in);
   return j;
 }
@@ -1179,22 +1093,20 @@ Job job_of(const uint8_t* l, int64_t lrows, const uint8_t* r, int64_t rrows, int
 // Bytes that the partial sums of a batch's launches take at most: every kind of launch by its sizes.
 int64_t parts_of(const Matrix* mats, int count) {
   int64_t most = 0;
-  for (int form : {kWide, kMiddle, kNarrow}) {
-    auto see = [&](int epilogue, int per, auto sizes) {  // per: jobs of a large matrix, none of the others; 0: one of each
-      Launch l(epilogue, form, form);
-      for (int i = 0; i < count; ++i)
-        for (int k = 0; k < (per ? mats[i].m > kChainDim ? per : 0 : 1); ++k) l.add(sizes(mats[i]));
-      if (l.args.njobs == 0) return;
-      l.plan();
-      most = std::max(most, l.parts());
-    };
-    auto job = [&](int64_t lrows, int64_t rrows, int64_t k) { return job_of(nullptr, lrows, nullptr, rrows, k, form, 0, 0); };
-    see(kSymmetric, 0, [&](const Matrix& a) { return job(a.m, a.m, a.n); });
-    see(kSymmetric, 1, [&](const Matrix& a) { return job(a.m, a.m, a.m); });
-    see(kSymmetric, 2, [&](const Matrix& a) { return job(a.m, a.m, a.m); });
-    see(kApply, 0, [&](const Matrix& a) { return job(a.m, a.n, a.m); });
-    see(kResult, 0, [&](const Matrix& a) { return a.rows > a.cols ? job(a.n, a.m, a.m) : job(a.m, a.n, a.m); });
-  }
+  auto see = [&](int epilogue, int per, auto sizes) {  // per: jobs of a large matrix, none of the others; 0: one of each
+    Launch l(epilogue);
+    for (int i = 0; i < count; ++i)
+      for (int k = 0; k < (per ? mats[i].m > kChainDim ? per : 0 : 1); ++k) l.add(sizes(mats[i]));
+    if (l.args.njobs == 0) return;
+    l.plan();
+    most = std::max(most, l.parts());
+  };
+  auto job = [&](int64_t lrows, int64_t rrows, int64_t k) { return job_of(nullptr, lrows, nullptr, rrows, k, 0, 0); };
+  see(kSymmetric, 0, [&](const Matrix& a) { return job(a.m, a.m, a.n); });
+  see(kSymmetric, 1, [&](const Matrix& a) { return job(a.m, a.m, a.m); });
+  see(kSymmetric, 2, [&](const Matrix& a) { return job(a.m, a.m, a.m); });
+  see(kApply, 0, [&](const Matrix& a) { return job(a.m, a.n, a.m); });
+  see(kResult, 0, [&](const Matrix& a) { return a.rows > a.cols ? job(a.n, a.m, a.m) : job(a.m, a.n, a.m); });
   return most;
 }
 
@@ -1286,18 +1198,15 @@ int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
            static_cast<uint32_t>(ceil_div(padded(m.cols), 256))};
       tiles += j.across * static_cast<uint32_t>(padded(m.rows) / 64);
     }
-    const bool half = r.source == kPlain && r.src_dtype == QOPT_BF16, wide = r.dst_dtype == QOPT_F32;
     const dim3 grid(tiles), block(256);
-    if (half && wide) hipLaunchKernelGGL((pack_kernel<uint16_t, kWide>), grid, block, 0, s, a);
-    else if (half) hipLaunchKernelGGL((pack_kernel<uint16_t, kMiddle>), grid, block, 0, s, a);
-    else if (wide) hipLaunchKernelGGL((pack_kernel<float, kWide>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((pack_kernel<float, kMiddle>), grid, block, 0, s, a);
+    if (r.source == kPlain && r.src_dtype == QOPT_BF16) hipLaunchKernelGGL(pack_kernel<uint16_t>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(pack_kernel<float>, grid, block, 0, s, a);
     if (launch_status() != QOPT_OK) return QOPT_ELAUNCH;
   }
   int small = 0;  // matrices whose groups are one launch; they come first
   while (small < count && mats[small].m <= kChainDim) ++small;
-  auto symmetric = [&](int64_t m, const uint8_t* a, const uint8_t* b, uint8_t* out, int exp_in, int to, int form) {
-    Job j = job_of(a, m, b, m, m, form, exp_in, to);
+  auto symmetric = [&](int64_t m, const uint8_t* a, const uint8_t* b, uint8_t* out, int exp_in, int to) {
+    Job j = job_of(a, m, b, m, m, exp_in, to);
     j.out = out;
     j.out_bytes = j.k_bytes;
     return j;
@@ -1305,17 +1214,13 @@ int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
   int rc = QOPT_OK, turn = 0;  // xt[turn] is current
   for (int done = 0; done < r.steps && rc == QOPT_OK;) {
     const int length = std::min(group_steps(mats[0].m, r.dst_dtype), r.steps - done);
-    auto form_from = [&](int first) {  // of the group that begins there
-      return r.dst_dtype == QOPT_F32 ? kWide : first == 0 || r.steps - first > 2 ? kMiddle : kNarrow;
-    };
-    const int form = form_from(done);
     const bool end = done + length == r.steps;
     {
-      Launch gram(kSymmetric, form, form);
+      Launch gram(kSymmetric);
       for (int i = 0; i < count; ++i) {
-        Job j = job_of(mats[i].x, mats[i].m, mats[i].x, mats[i].m, mats[i].n, form, 2 * kExp, kExp);
+        Job j = job_of(mats[i].x, mats[i].m, mats[i].x, mats[i].m, mats[i].n, 2 * kExp, kExp);
         j.out = mats[i].g;
-        j.out_bytes = static_cast<uint32_t>(row_bytes(mats[i].m, form));
+        j.out_bytes = static_cast<uint32_t>(row_bytes(mats[i].m));
         gram.add(j);
       }
       rc = gram.run(parts, s);
@@ -1325,25 +1230,22 @@ int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
       a.length = length;
       for (int i = 0; i < small; ++i)
         a.jobs[i] = {mats[i].g, mats[i].q[(length - 1) % 2], static_cast<int32_t>(mats[i].m)};
-      const dim3 grid(static_cast<unsigned>(small)), block(256);
-      if (form == kWide) hipLaunchKernelGGL(chain_kernel<kWide>, grid, block, 0, s, a);
-      else if (form == kMiddle) hipLaunchKernelGGL(chain_kernel<kMiddle>, grid, block, 0, s, a);
-      else hipLaunchKernelGGL(chain_kernel<kNarrow>, grid, block, 0, s, a);
+      hipLaunchKernelGGL(chain_kernel, dim3(static_cast<unsigned>(small)), dim3(256), 0, s, a);
       rc = launch_status();
     }
     int q = 0, exp_q = kExp;  // q[q] is the product of the polynomials so far
     for (int it = 0; it < length; ++it) {
-      Launch poly(kPolynomial, form, form), both(kSymmetric, form, form), next(kSymmetric, form, form);
+      Launch poly(kPolynomial), both(kSymmetric), next(kSymmetric);
       for (int i = small; i < count; ++i) {
         const Matrix& a = mats[i];
         uint8_t* p = it == 0 ? a.q[0] : a.p;
-        Job j = symmetric(a.m, a.g, a.g, p, 2 * kExp, kExp, form);
+        Job j = symmetric(a.m, a.g, a.g, p, 2 * kExp, kExp);
         j.add = a.g;
         poly.add(j);
-        if (it > 0) both.add(symmetric(a.m, p, a.q[q], a.q[1 - q], kExp + exp_q, kExpQ, form));
+        if (it > 0) both.add(symmetric(a.m, p, a.q[q], a.q[1 - q], kExp + exp_q, kExpQ));
         if (it + 1 < length) {
-          both.add(symmetric(a.m, p, a.g, a.h, 2 * kExp, kExp, form));
-          next.add(symmetric(a.m, a.h, p, a.g, 2 * kExp, kExp, form));
+          both.add(symmetric(a.m, p, a.g, a.h, 2 * kExp, kExp));
+          next.add(symmetric(a.m, a.h, p, a.g, 2 * kExp, kExp));
         }
       }
       if (it > 0) {
@@ -1356,28 +1258,27 @@ int run_batch(Matrix* mats, int count, uint8_t* parts, const Run& r) {
     if (rc != QOPT_OK) break;
     done += length;
     if (!end) {
-      const int form_out = form_from(done);
-      Launch apply(kApply, form, form_out);
+      Launch apply(kApply);
       for (int i = 0; i < count; ++i) {
         const Matrix& a = mats[i];
-        Job j = job_of(a.q[q], a.m, a.xt[turn], a.n, a.m, form, exp_q + kExp, kExp);
+        Job j = job_of(a.q[q], a.m, a.xt[turn], a.n, a.m, exp_q + kExp, kExp);
         j.out = a.x;
-        j.out_bytes = static_cast<uint32_t>(row_bytes(a.n, form_out));
+        j.out_bytes = static_cast<uint32_t>(row_bytes(a.n));
         j.out_t = a.xt[1 - turn];
-        j.out_t_bytes = static_cast<uint32_t>(row_bytes(a.m, form_out));
+        j.out_t_bytes = static_cast<uint32_t>(row_bytes(a.m));
         apply.add(j);
       }
       rc = apply.run(parts, s);
       turn = 1 - turn;
     } else {
-      Launch last(r.update ? kUpdate : kResult, form, form);
+      Launch last(r.update ? kUpdate : kResult);
       last.dst_dtype = r.dst_dtype;
       last.args.decay = r.decay;
       for (int i = 0; i < count; ++i) {
         const Matrix& a = mats[i];
         // the transpose of Q X is X^T Q: a tall matrix's rows
-        Job j = a.rows > a.cols ? job_of(a.xt[turn], a.n, a.q[q], a.m, a.m, form, exp_q + kExp, 0)
-                                : job_of(a.q[q], a.m, a.xt[turn], a.n, a.m, form, exp_q + kExp, 0);
+        Job j = a.rows > a.cols ? job_of(a.xt[turn], a.n, a.q[q], a.m, a.m, exp_q + kExp, 0)
+                                : job_of(a.q[q], a.m, a.xt[turn], a.n, a.m, exp_q + kExp, 0);
         j.dst = a.dst;
         j.rate = a.rate;
         last.add(j);

@@ -85,7 +85,6 @@ struct Rows {
 //
 // Op: `Side` (what comes with a step's codes: scales), load(t), kSideLoads (memory instructions of a load),
 // touch(side), terms(half) and multiply<half, term, i, j>(acc, a, b, side), a and b the two pieces of a fragment.
-// kCross: in half 1 lane (r, h) takes the pieces of b that (r, 1 - h) would.
 template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> struct Tile {
   static constexpr int kWaves = kWavesM * kWavesN, kThreads = kWaves * kWave;
   static constexpr int kWm = kM / kWavesM, kWn = kN / kWavesN;  // a wave's part of the tile
@@ -137,7 +136,7 @@ template <int kM, int kN, int kWavesM, int kWavesN, int kBufs, typename Op> stru
     };
     auto read_half = [&](Frags& f, int buf, int half) {
       asm volatile("" : "+v"(oa), "+v"(ob));  // addresses are made anew, not kept in registers
-      const uint32_t a0 = (oa ^ (half * 32)) + buf * (kRows * kStepBytes), b0 = (ob ^ (half * (Op::kCross ? 96 : 32))) + buf * (kRows * kStepBytes);
+      const uint32_t a0 = (oa ^ (half * 32)) + buf * (kRows * kStepBytes), b0 = (ob ^ (half * 32)) + buf * (kRows * kStepBytes);
 #pragma unroll
       for (int j = 0; j < kFn; ++j) {
         f.b[j][0] = *reinterpret_cast<const i32x4*>(lds + b0 + j * (32 * kStepBytes));

@@ -13,15 +13,15 @@
  * (of U's transpose where rows > cols), which moves every singular value s to
  * a s + b s^3 + c s^5 and so, after five, to between 0.68 and 1.14 where it was not tiny.
  *
- * Precision.  For binary32 destinations every value between the products is held as the sum of
- * two binary16 numbers (22 bits) under a fixed power of two, and a product of two such values is
- * three matrix instructions with binary32 sums: what reaches them is about as exact as products
- * in binary32 (1.1e-6 to 3.6e-6 of the result on gradients of 64 x 64 to 2048 x 2048, where those are 1.0e-6
- * to 3.4e-6 off).  For bfloat16 destinations the parts that lie 2^-11 under a product's first are
- * multiplied in e4m3, which leaves 15 bits, and the last iterations (at most two, of more than
- * three) hold single binary16 numbers, 11 bits: the singular values are near 1 there, so their
- * rounding (8e-4 to 3e-3 of the result, the more the further U's singular values spread) stays
- * beside bfloat16's own.  Matrices of up to 32 rows or columns are iterated in binary64.
+ * Precision.  Every value between the products is held as the sum of two binary16 numbers (22
+ * bits) under a fixed power of two, and a product of two such values is three matrix instructions
+ * with binary32 sums; the result is rounded once, to the destination's type.  Before that it is
+ * 0.5 to 2 times as far off as products of binary32 numbers leave it: 7e-7 to 3e-5 of the result for
+ * 64 x 64 to 4096 x 4096, least where one entry holds nearly all of the norm, most where the
+ * singular values spread (5e-7 to 4e-5 with those); a bfloat16 result is as far from the exact
+ * one as that one rounded, 1.66e-3, to three digits.  The values' power of two is that of the largest
+ * possible one, so that what lies 2^-15 under it or further down is held to 2^-37 of it instead.
+ * Matrices of up to 32 rows or columns are iterated in binary64.
  *
  * Conventions are those of qopt.h (status codes, dtypes, *_dev pointers in device memory
  * of the current HIP device, caller-owned buffers, host-side argument checks before
