@@ -295,7 +295,7 @@ class Muon(torch.optim.Optimizer):
             settings = self._group_settings(group)
             if live:
                 _check_settings(**settings)
-            new = [p for p in live if not self.state[p]]
+            new = [p for p in live if not self.state.get(p)]  # without an entry for those that have none
             fresh += new
             work.append((group, live, new, settings))
         if fresh and torch.cuda.is_current_stream_capturing():
@@ -345,6 +345,8 @@ class Muon(torch.optim.Optimizer):
         by_id = self._params_by_saved_id(groups)
         state = defaultdict(dict)
         for pid, st in state_dict["state"].items():
+            if not st:  # a parameter that has not been stepped
+                continue
             p = by_id[pid]
             n = p.numel()
             want = (("m_codes", torch.uint8, n), ("m_absmax", torch.float32, nblocks(n))) if "m_codes" in st else \
@@ -374,6 +376,8 @@ class Muon(torch.optim.Optimizer):
         group_of = {p: g for g in self.param_groups for p in g["params"]}
         state = defaultdict(dict)
         for pid, st in muon_state_dict["state"].items():
+            if not st:
+                continue
             p = by_id[pid]
             m = st["momentum_buffer"]
             if m.shape != p.shape:
@@ -394,7 +398,7 @@ class Muon(torch.optim.Optimizer):
         params = [p for g in self.param_groups for p in g["params"]]
         state = {pid: {"momentum_buffer": qopt_dequantize_blockwise(st["m_codes"], st["m_absmax"], SIGNED)
                        .view(params[pid].shape) if "m_codes" in st else st["momentum_buffer"].clone()}
-                 for pid, st in sd["state"].items()}
+                 for pid, st in sd["state"].items() if st}
         defaults = torch.optim.Muon([torch.zeros(1, 1)]).defaults  # this torch's keys
         groups = [{**defaults, "lr": g["lr"], "momentum": g["momentum"], "weight_decay": g["weight_decay"],
                    "nesterov": g["nesterov"], "eps": g["eps"], "ns_steps": g["ns_steps"],
