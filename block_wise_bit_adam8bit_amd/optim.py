@@ -325,7 +325,7 @@ class AdamW(torch.optim.Optimizer):
                             weight_decay=group["weight_decay"])
             if live:
                 _check_settings(**settings)
-            new = [p for p in live if not self.state[p]]
+            new = [p for p in live if not self.state.get(p)]  # without an entry for those that have none
             fresh += new
             work.append((group, live, new, settings))
         # A step that begins states makes every list, which is where overlaps are found, before it runs
@@ -379,6 +379,8 @@ class AdamW(torch.optim.Optimizer):
         by_id = self._params_by_saved_id(groups)
         state = defaultdict(dict)
         for pid, st in state_dict["state"].items():
+            if not st:  # a parameter that has not been stepped
+                continue
             p = by_id[pid]
             n = p.numel()
             want = (("m_codes", torch.uint8, n), ("v_codes", torch.uint8, n),
