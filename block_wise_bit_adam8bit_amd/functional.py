@@ -41,7 +41,8 @@ def codebook_bytes(kind):
 
 def codebook(kind, device=None):
     """Device copy of the codebook of ``kind`` on ``device`` (built and uploaded once
-    per process and device; 16-byte aligned)."""
+    per process and device; 16-byte aligned).  The upload cannot be captured into a graph:
+    inside of a capture a codebook that is not there yet is refused."""
     if isinstance(device, torch.device) and device.type == "cuda":
         t = _cb_cache.get((kind, device.index))
         if t is not None:
@@ -56,6 +57,9 @@ def codebook(kind, device=None):
     with _cb_lock:
         t = _cb_cache.get(key)
         if t is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the first copy of a codebook to a GPU cannot be captured: make the "
+                                   "step's plan, or call codebook(kind, device), before the capture")
             t = codebook_bytes(kind).to(device)
             assert t.data_ptr() % 16 == 0
             _cb_cache[key] = t

@@ -139,7 +139,7 @@ def qopt_muon8bit_plan(tensors):
     tuples: matrices of any shapes, fp32 or bf16 params and grads; none may overlap another."""
     plan = _muon_plan(tensors, 8)
     if plan.device is not None:
-        codebook(SIGNED, plan.device)  # on the device from here on: its first copy cannot be captured
+        codebook(SIGNED, plan.device)  # a step may be captured from here on
     return plan.keep()
 
 
@@ -217,6 +217,8 @@ def _flat_state(device, shapes, coded):
     views = [m[o:o + s.numel()].view(s) for s, o in zip(shapes, off)]
     if not coded:
         return [(v,) for v in views]
+    if device.type == "cuda":
+        codebook(SIGNED, device)  # a step may be captured from here on
     am = torch.zeros(max(b, 1), dtype=torch.float32, device=device)
     return [(v.view(-1), am[k:k + nblocks(v.numel())]) for v, k in zip(views, blk)]
 

@@ -45,3 +45,42 @@ def test_a_refused_step_leaves_no_entries(q, monkeypatch):
     other.load_state_dict(opt.state_dict())
     opt.step()
     assert all(opt.state[p] for p in ps)
+
+
+def test_the_codebook_comes_with_coded_state(q, monkeypatch):
+    """A process that loads its state may capture its first step: the codebook, whose first copy cannot be captured,
+    is on the device by then.  So it is after the state's conversion and after a first step."""
+    from block_wise_bit_adam8bit_amd import functional, muon
+    ps = params(1)
+    first = q.Muon(ps, min_8bit_size=1)
+    first.step()
+    saved = first.state_dict()
+    for p in ps:
+        p.grad = torch.ones_like(p) * 1e-3
+    before = [p.detach().clone() for p in ps]
+    cache = {}
+    monkeypatch.setattr(functional, "_cb_cache", cache)
+    opt = q.Muon(ps, min_8bit_size=1)
+    opt.load_state_dict(saved)
+    assert (muon.SIGNED, 0) in cache
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    assert all(torch.equal(p, b) for p, b in zip(ps, before))
+    twin = [torch.nn.Parameter(p.detach().clone()) for p in ps]
+    other = q.Muon(twin, min_8bit_size=1)
+    other.load_state_dict(saved)
+    for t, p in zip(twin, ps):
+        t.grad = p.grad.clone()
+    for _ in range(3):
+        graph.replay()
+        other.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, t) for p, t in zip(ps, twin))
+    cache.clear()
+    opt = q.Muon([torch.nn.Parameter(torch.ones(64, 64, device="cuda"))])
+    p, = opt.param_groups[0]["params"]
+    p.grad = torch.ones_like(p)
+    opt._init_states(opt.param_groups[0], [p])
+    assert (muon.SIGNED, 0) in cache

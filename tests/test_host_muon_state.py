@@ -31,3 +31,12 @@ def test_a_parameter_without_state_converts_to_none():
     saved["state"] = {0: {}, 1: {}}
     opt.load_fp32_muon_state(saved)
     assert not opt.state
+
+
+def test_a_codebook_is_not_copied_inside_of_a_capture(monkeypatch):
+    from block_wise_bit_adam8bit_amd import functional
+    monkeypatch.setattr(functional, "_cb_cache", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="captured"):
+        functional.codebook(functional.SIGNED, torch.device("cuda", 0))
+    assert not functional._cb_cache
