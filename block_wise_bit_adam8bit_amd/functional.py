@@ -325,7 +325,11 @@ def _adamw_plan(tensors, bits):
 def qopt_adamw8bit_plan(tensors):
     """Plan of an 8-bit AdamW step over a list of (param, grad, m_codes, v_codes, m_absmax,
     v_absmax) tuples, checked as for qopt_adam8bit_step; none may overlap another."""
-    return _adamw_plan(tensors, 8).keep()
+    plan = _adamw_plan(tensors, 8)
+    if plan.device is not None:
+        for kind in (SIGNED, UNSIGNED):
+            codebook(kind, plan.device)  # a step may be captured from here on
+    return plan.keep()
 
 
 def qopt_adamw32bit_plan(tensors):

@@ -35,3 +35,28 @@ def test_a_refused_step_leaves_no_entries(q):
     other.load_state_dict(opt.state_dict())
     opt.step()
     assert all(opt.state[p] for p in ps)
+
+
+def test_a_plan_brings_the_codebooks(q, monkeypatch):
+    """A step of a plan may be captured as the first work of a process: the codebooks, whose first copy cannot be
+    captured, are on the device by then."""
+    from block_wise_bit_adam8bit_amd import functional
+    cache = {}
+    monkeypatch.setattr(functional, "_cb_cache", cache)
+    n = 5000
+    state = lambda: (torch.full((n,), 0.5, device="cuda"), torch.full((n,), 0.1, device="cuda"),  # noqa: E731
+                     *(torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                     *(torch.zeros(3, device="cuda") for _ in range(2)))
+    a, b = state(), state()
+    plan = q.qopt_adamw8bit_plan([a])
+    assert {(q.SIGNED, 0), (q.UNSIGNED, 0)} <= set(cache)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1, step=1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.qopt_adamw8bit_step(plan, **hp)
+    for _ in range(3):
+        graph.replay()
+        q.qopt_adamw8bit_step([b], **hp)
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
