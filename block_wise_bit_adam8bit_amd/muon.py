@@ -359,6 +359,8 @@ class Muon(torch.optim.Optimizer):
                 if t is None or t.dtype != dt or t.numel() != size:
                     raise ValueError(f"state '{k}' of a parameter with {n} elements must be "
                                      f"{dt} with {size} elements")
+                if k == "momentum_buffer" and t.shape != p.shape:
+                    raise ValueError("momentum's shape differs from its parameter's")
                 new[k] = t.to(device=p.device)
             state[p] = new
         self._take_state(state, groups, None)

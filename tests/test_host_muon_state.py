@@ -40,3 +40,18 @@ def test_a_codebook_is_not_copied_inside_of_a_capture(monkeypatch):
     with pytest.raises(RuntimeError, match="captured"):
         functional.codebook(functional.SIGNED, torch.device("cuda", 0))
     assert not functional._cb_cache
+
+
+def test_momentum_of_another_shape_is_refused():
+    opt = optimizer((3, 5))
+    p, = opt.param_groups[0]["params"]
+    saved = opt.state_dict()
+    for shape in ((5, 3), (15,), (1, 15)):  # as many elements as the parameter has
+        saved["state"] = {0: dict(momentum_buffer=torch.ones(shape))}
+        with pytest.raises(ValueError, match="shape"):
+            opt.load_state_dict(saved)
+        assert not opt.state
+    m = torch.arange(15.0).view(5, 3).t()  # its shape, in another order of memory
+    saved["state"] = {0: dict(momentum_buffer=m)}
+    opt.load_state_dict(saved)
+    assert torch.equal(opt.state[p]["momentum_buffer"], m) and opt.state[p]["momentum_buffer"].is_contiguous()
