@@ -164,7 +164,8 @@ def _linear(x, dx, m, k, ldx, w, form, out, do, ldo):
 
 def _not_traced():
     if _is_tracing():
-        raise RuntimeError("a library call cannot be traced; fp8_linear can")
+        raise RuntimeError("a library call cannot be traced; the forward passes of fp8_linear, fp4_linear and "
+                           "layer_norm can")
 
 
 def qopt_fp8_quantize(x, *, tiles=False, normal=True, transposed=False):
