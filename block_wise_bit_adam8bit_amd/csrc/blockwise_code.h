@@ -81,8 +81,6 @@ __device__ __forceinline__ uint32_t encode_nonneg(const Encoder& e, const BlockS
   return encode_mag(e, x * s.r);
 }
 
-// ---------------------------------------------------------- codec kernels
-
 }  // namespace blockwise
 
 #endif  // QOPT_BLOCKWISE_CODE_H

@@ -166,6 +166,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+// ---------------------------------------------------------- codec kernels
+
 // Index of the last piece whose first block is <= blk, by a fixed six-step search
 // (kMaxTensors <= 64) written without a loop: a loop here, inside the kernels' block
 // loops, measurably slows them even when it rarely runs.
