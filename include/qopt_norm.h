@@ -10,8 +10,10 @@
  *   mean_i  = mean of x[i, :],  rstd_i = 1 / sqrt(mean of (x[i, :] - mean_i)^2 + eps)
  *
  * Statistics and sums are binary32, the variance is the mean of squared distances (no
- * difference of squares), and every result is rounded once, to its type.  The order of each
- * sum depends on the sizes alone: equal calls give equal bits.
+ * difference of squares), and every result is rounded once, to its type.  So a row r times its
+ * spread away from zero is off by the rounding of its mean, some r 2^-23 of its spread, and a row
+ * whose squared distances sum to 2^128 or more has rstd 0 and comes out as b.  The order of
+ * each sum depends on the sizes alone: equal calls give equal bits.
  *
  * Conventions are those of qopt.h (status codes, dtypes, *_dev pointers in device memory of
  * the current HIP device, host-side argument checks before anything is enqueued,
