@@ -234,7 +234,8 @@ class Fp4LinearFunction(torch.autograd.Function):
 
 def fp4_linear(x, w):
     """x w^T over 4-bit codes, with straight-through gradients: x [..., k] and w [n, k] in
-    float32 or bfloat16.  The result and x's gradient have x's type, w's gradient has w's.  The
+    float32 or bfloat16.  The result and x's gradient have x's type, w's gradient has w's; the
+    gradients are ``fp8_linear``'s, with what its 8-bit products lose in bfloat16 ones (qopt_fp8.h).  The
     weight is quantized anew in every call; a server quantizes it once and calls
     ``qopt_fp4_linear``, which gives the same result.  A trace (torch.jit.trace) holds it as one
     operation; forward-mode derivatives are refused (NotImplementedError).  For passes that are

@@ -103,7 +103,9 @@ typedef struct qopt_muon_hparams {
  * A matrix whose u has an infinity or a NaN gets NaN parameters; the others are as without it.
  * No tensor may overlap another.  Matrices without elements are left out.
  * workspace_dev: at least qopt_muon_workspace(tensors, ...) bytes, 256-byte aligned; scratch
- * whose contents need no preparation, for one call at a time.
+ * whose contents need no preparation, for one call at a time.  It holds what the matrices that
+ * share their launches need, not all of them: 12 bytes per element and 20 per value of their m x m
+ * (m the shorter side), and partial sums (1.0 GB for 4096 x 11008).
  * Errors: QOPT_EINVAL (null pointers with elements, sizes, hyper-parameters: lr, weight_decay and
  * eps finite, lr and weight_decay >= 0, eps > 0, momentum in [0, 1), steps in 1 ..
  * QOPT_MUON_MAX_STEPS, nesterov 0 or 1; a workspace that is too small), QOPT_EUNSUPPORTED
