@@ -92,7 +92,7 @@ def _backward(x, dx, rows, dim, ldx, weight, dw, mean, rstd, dout, lddo, need_x,
 def qopt_layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, save_stats=True, out=None):
     """The rows of x [..., dim] (float32 or bfloat16) normalised, times ``weight`` plus ``bias``
     ([dim], both float32 or both bfloat16).  Returns (out, mean, rstd), out in x's shape and type, the
-    others float32, one value per row (None unless ``save_stats``).  ``out`` may be passed in;
+    others float32, one value per row (None unless ``save_stats``; NaN for rows without values).  ``out`` may be passed in;
     it shares no byte with an operand, but may be other columns of the buffer that x lies in."""
     _not_traced()
     dx = _check_dtype(x.dtype, "x")
@@ -104,7 +104,8 @@ def qopt_layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, save_stats=T
     out, ldo = _output(out, tuple(x.shape), x.dtype, dev, *operands)
     mean = rstd = None
     if save_stats:
-        mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=dev)
+        mean, rstd = torch.empty(2, rows, dtype=torch.float32, device=dev) if dim else \
+            torch.full((2, rows), math.nan, dtype=torch.float32, device=dev)
     _forward(x, dx, rows, dim, ldx, weight, bias, dw, eps, out, ldo, _ptr(mean), _ptr(rstd))
     return out, mean, rstd
 

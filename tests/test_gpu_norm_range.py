@@ -43,3 +43,20 @@ def test_rows_whose_squares_overflow(q, dim):
     assert rstd[1].item() == 0 and torch.equal(y[1], b)
     keep = [0, 2, 3]
     assert torch.equal(y[keep], q.qopt_layer_norm_forward(x[keep], w, b)[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_without_values(q, dtype):
+    """Their mean is that of nothing, as torch's is; nothing that lay in memory before is returned."""
+    for shape in ((5, 0), (2, 3, 0), (0, 0), (0, 7)):
+        rows = torch.Size(shape[:-1]).numel()
+        keep = torch.full((2, rows), 7.0, device="cuda")
+        del keep  # the memory that comes next
+        x = torch.empty(shape, dtype=dtype, device="cuda", requires_grad=True)
+        w, b = (torch.ones(shape[-1], device="cuda", requires_grad=True) for _ in range(2))
+        y, mean, rstd = q.qopt_layer_norm_forward(x.detach(), w.detach(), b.detach())
+        assert y.shape == shape and mean.shape == rstd.shape == (rows,)
+        assert mean.isnan().all() and rstd.isnan().all()
+        z = q.layer_norm(x, w, b)
+        dx, dw, db = torch.autograd.grad(z, (x, w, b), torch.ones_like(z))
+        assert dx.shape == shape and not dw.any() and not db.any() and dw.shape == db.shape == shape[-1:]
