@@ -233,7 +233,8 @@ class Muon(torch.optim.Optimizer):
     contiguous float32 or bfloat16 GPU tensors; all matrices of a group, device and type take one
     fused step.  ``step(grad_scale=t)`` multiplies every gradient with the float32 GPU value
     ``t`` inside the step.  A step that begins states is not captured into a graph; a captured one
-    keeps its settings and its parameters' and gradients' memory.
+    keeps its settings and the memory of its parameters, gradients and state: loading a state dict gives
+    the state other memory, behind which a step is captured anew.
 
     A step takes a workspace from torch's allocator and gives it back at its end: 12 bytes per element of
     the matrices that share their launches (at most 16 of more than 128 rows and columns, or until their

@@ -54,7 +54,7 @@ extern "C" {
  * batch, rows or cols 0: nothing is written.
  * Errors: QOPT_EINVAL (null pointers with elements, sizes negative or too large, eps not finite,
  * negative or zero, steps outside 1 .. QOPT_MUON_MAX_STEPS, a workspace that is too small),
- * QOPT_EUNSUPPORTED (dtypes), QOPT_EALIGN, QOPT_ELAUNCH.
+ * QOPT_EUNSUPPORTED (dtypes), QOPT_EALIGN, QOPT_ELAUNCH, QOPT_EINTERNAL (no host memory for the list of matrices).
  */
 int qopt_orthogonalize(const void* x_dev, int dtype, int64_t batch, int64_t rows, int64_t cols,
                        int steps, float eps, void* out_dev, int out_dtype, void* workspace_dev,
@@ -109,7 +109,7 @@ typedef struct qopt_muon_hparams {
  * Errors: QOPT_EINVAL (null pointers with elements, sizes, hyper-parameters: lr, weight_decay and
  * eps finite, lr and weight_decay >= 0, eps > 0, momentum in [0, 1), steps in 1 ..
  * QOPT_MUON_MAX_STEPS, nesterov 0 or 1; a workspace that is too small), QOPT_EUNSUPPORTED
- * (dtypes, adjust), QOPT_EALIGN, QOPT_ELAUNCH.  The hyper-parameters are checked also for a step of no tensors.
+ * (dtypes, adjust), QOPT_EALIGN, QOPT_ELAUNCH, QOPT_EINTERNAL.  The hyper-parameters are checked also for a step of no tensors.
  */
 int qopt_muon8bit_step(const qopt_muon_tensor* tensors, int32_t ntensors, int param_dtype,
                        int grad_dtype, const qopt_codebook* cb_m_dev, const qopt_muon_hparams* hp,
