@@ -16,8 +16,8 @@
 // Numbers.  A value is kept times a power of two that holds the largest possible one (|X| <= 1.203, A <= 1.45,
 // P <= 3.4445, Q <= 3.4445^3) under 65504, as hi + lo, two binary16 numbers: 22 bits, or 23, down to 2^-24, under which lo
 // ends: 2^-36 of X's largest possible value.  A product is hi hi + hi lo + lo hi with binary32 sums, which leaves out 2^-22
-// of it.  That holds for either destination: fewer bits would be faster (hi alone a third of the time) and next to a bfloat16
-// result's own rounding as large as it, 8e-4 to 2.4e-2 of the result.
+// of it.  That holds for either destination: with fewer bits a bfloat16 result would be faster (hi alone takes a third of the
+// time) and off by as much as its own rounding or more, 8e-4 to 2.4e-2 of itself where that is 1.66e-3.
 
 #include <hip/hip_runtime.h>
 
