@@ -711,17 +711,19 @@ __global__ void __launch_bounds__(256, 1) chain_kernel(ChainArgs args) {
 // ------------------------------------------------------------------ matrices of few rows or columns
 
 // Up to kTiny on the shorter side (an adapter's rank) the products with U are short sums and what would bound the
-// way above is its launches.  Here it takes three, in binary64, where five iterations on A need no fresh start:
-// A = U U^T, whose trace is the squared norm; the polynomial Q of A / |U|^2; and Q U / |U|.
+// way above is its launches.  Here it takes three, in binary64, where up to kTinySteps iterations on A need no fresh
+// start: A = U U^T, whose trace is the squared norm; the polynomial Q of A / |U|^2; and Q U / |U|.  More iterations are
+// taken in groups, with X in binary64 between them.  (2^-53 of A grows by 11.9 per iteration: under 2^-24 after six,
+// 1e-3 after twelve, and behind that the iteration leaves its bounds: 32 on a matrix of one direction ended in NaN.)
 // 16 x 4096 takes 34 us, 32 x 4096 57, 5 x 300 21 (the way above: 99 x 300 120, 33 x 4096 182), and the results are within 2.5e-8.  The
 // polynomial's products in one workgroup are most of it at 32: twice as many rows would make that chain eight times as long, and
 // its four matrices, 34 KB of LDS now, four times as large.
-constexpr int kTiny = 32;
+constexpr int kTiny = 32, kTinySteps = 6;
 constexpr int kGramColumns = 64, kResultColumns = 256;  // of the longer side, per workgroup and turn
 constexpr int kTinyParts = 128;                         // partial A per matrix
 
 struct TinyJob {
-  const void* u;
+  const void* u;  // U, or X between groups
   double *parts, *q;
   void* dst;
   int64_t n, along, across;  // element (i, c) of U's short rows lies at i * across + c * along
@@ -733,25 +735,32 @@ struct TinyArgs {
   TinyJob jobs[kMaxJobs];
   double eps;
   int steps;
+  int scaled;  // X, whose norm is not divided by
   float decay;
 };
 static_assert(sizeof(TinyArgs) <= 4096, "kernel arguments");
 
+// What LDS holds of an element: binary32, or X's binary64.
+__device__ __forceinline__ double held(double x) { return x; }
+__device__ __forceinline__ float held(float x) { return x; }
+__device__ __forceinline__ float held(uint16_t x) { return to_f32(x); }
+template <typename ST> using Held = decltype(held(ST{}));
+
 // Columns c0 to c0 + kColumns - 1 of U's short rows in LDS, 0 behind the end.
-template <typename ST, int kColumns> __device__ __forceinline__ void load_columns(const TinyJob& job, int64_t c0, float (*x)[kColumns + 1]) {
+template <typename ST, int kColumns> __device__ __forceinline__ void load_columns(const TinyJob& job, int64_t c0, Held<ST> (*x)[kColumns + 1]) {
   const ST* u = static_cast<const ST*>(job.u);
   const int all = job.m * kColumns;
 #pragma unroll 4
   for (int i = threadIdx.x; i < all; i += 256) {
     // the index that runs along memory first
     const int row = job.along == 1 ? i / kColumns : i % job.m, c = job.along == 1 ? i % kColumns : i / job.m;
-    x[row][c] = c0 + c < job.n ? to_f32(u[row * job.across + (c0 + c) * job.along]) : 0.0f;
+    x[row][c] = c0 + c < job.n ? held(u[row * job.across + (c0 + c) * job.along]) : Held<ST>{0};
   }
 }
 
 // A thread holds A[i][j] for i = 2 ti, 2 ti + 1 and j likewise.
 template <typename ST> __global__ void __launch_bounds__(256) tiny_gram_kernel(TinyArgs a) {
-  __shared__ float x[kTiny][kGramColumns + 1];
+  __shared__ Held<ST> x[kTiny][kGramColumns + 1];
   const TinyJob& job = a.jobs[blockIdx.y];
   if (blockIdx.x >= job.groups) return;
   const int ti = threadIdx.x / 16, tj = threadIdx.x % 16;
@@ -779,7 +788,7 @@ template <typename ST> __global__ void __launch_bounds__(256) tiny_gram_kernel(T
       if (2 * ti + i < job.m && 2 * tj + j < job.m) to[(2 * ti + i) * job.m + 2 * tj + j] = s[i][j];
 }
 
-// Q = the product of a I + b A + c A^2 over the iterations, A = P A P after each, over |U|.
+// Q = the product of a I + b A + c A^2 over the group's iterations, A = P A P after each, over |U| in the first group.
 __global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
   typedef double Mat[kTiny][kTiny + 1];
   __shared__ Mat a, p, q, h;
@@ -816,7 +825,7 @@ __global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
   double trace = 0.0;
   for (int i = 0; i < m; ++i) trace += a[i][i];
   __syncthreads();
-  const double norm = sqrt(trace), size = norm < args.eps ? args.eps : norm;
+  const double norm = sqrt(trace), size = args.scaled ? 1.0 : norm < args.eps ? args.eps : norm;
   own([&](int i, int j, int) { a[i][j] = a[i][j] / size / size; });
   __syncthreads();
   for (int it = 0; it < args.steps; ++it) {
@@ -843,9 +852,10 @@ __global__ void __launch_bounds__(256) tiny_polynomial_kernel(TinyArgs args) {
   });
 }
 
-// dst = Q U, or dst * decay - Q U * rate: a thread per column of U's short rows, eight results of it at a time.
+// dst = Q U, or dst * decay - Q U * rate: a thread per column of U's short rows, eight results of it at a time.  (X
+// becomes Q X in place: a workgroup's columns are in its LDS before it writes them.)
 template <typename ST, typename OT, bool kStep> __global__ void __launch_bounds__(256) tiny_result_kernel(TinyArgs a) {
-  __shared__ float x[kTiny][kResultColumns + 1];
+  __shared__ Held<ST> x[kTiny][kResultColumns + 1];
   __shared__ __align__(16) double q[kTiny][kTiny];  // q[k][i]: Q is symmetric
   const TinyJob& job = a.jobs[blockIdx.y];
   if (blockIdx.x >= job.result_groups) return;
@@ -869,8 +879,12 @@ template <typename ST, typename OT, bool kStep> __global__ void __launch_bounds_
       for (int i = 0; i < 8; ++i)
         if (i0 + i < job.m) {
           OT* to = static_cast<OT*>(job.dst) + (i0 + i) * job.across + c * job.along;
-          const float o = static_cast<float>(s[i]);
-          store1(to, kStep ? to_f32(*to) * a.decay - o * job.rate : o);
+          if constexpr (sizeof(OT) == 8) {
+            *to = s[i];
+          } else {
+            const float o = static_cast<float>(s[i]);
+            store1(to, kStep ? to_f32(*to) * a.decay - o * job.rate : o);
+          }
         }
     }
     __syncthreads();
@@ -897,7 +911,7 @@ struct Matrix {
   double* parts;
   uint32_t groups;
   uint8_t *x, *xt[2], *g, *p, *h, *q[2];
-  double *tiny_parts, *tiny_q;
+  double *tiny_parts, *tiny_q, *tiny_x;
 };
 
 int64_t up(int64_t bytes) { return ceil_div(bytes, 256) * 256; }
@@ -914,6 +928,7 @@ uint8_t* lay_out(Matrix& a, uint8_t* at) {
     a.u = reinterpret_cast<float*>(take(a.rows * a.cols * 4));
     a.tiny_parts = reinterpret_cast<double*>(take(kTinyParts * a.m * a.m * 8));
     a.tiny_q = reinterpret_cast<double*>(take(a.m * a.m * 8));
+    a.tiny_x = reinterpret_cast<double*>(take(a.rows * a.cols * 8));
     return at;
   }
   a.x = take(a.m * row_bytes(a.n));
@@ -1151,11 +1166,25 @@ template <typename ST, typename OT> void launch_tiny_result(const TinyArgs& a, b
   else hipLaunchKernelGGL((tiny_result_kernel<ST, OT, false>), grid, dim3(256), 0, s, a);
 }
 
+// One group, from matrices of type ST: to X, or the last one to the destinations.
+template <typename ST> void launch_tiny(TinyArgs a, const Matrix* mats, int count, bool last, const Run& r, dim3 gram, dim3 result) {
+  hipStream_t s = r.stream;
+  hipLaunchKernelGGL(tiny_gram_kernel<ST>, gram, dim3(256), 0, s, a);
+  hipLaunchKernelGGL(tiny_polynomial_kernel, dim3(static_cast<unsigned>(count)), dim3(256), 0, s, a);
+  if (!last) {
+    for (int i = 0; i < count; ++i) a.jobs[i].dst = mats[i].tiny_x;
+    hipLaunchKernelGGL((tiny_result_kernel<ST, double, false>), result, dim3(256), 0, s, a);
+  } else if (r.dst_dtype == QOPT_F32) {
+    launch_tiny_result<ST, float>(a, r.update, result, s);
+  } else {
+    launch_tiny_result<ST, uint16_t>(a, r.update, result, s);
+  }
+}
+
 int run_tiny(Matrix* mats, int count, const Run& r) {
   if (r.source != kPlain && run_source(mats, count, r) != QOPT_OK) return QOPT_ELAUNCH;
   TinyArgs a = {};
   a.eps = static_cast<double>(r.eps);
-  a.steps = r.steps;
   a.decay = r.decay;
   uint32_t most = 0, most_results = 0;
   for (int i = 0; i < count; ++i) {
@@ -1169,15 +1198,19 @@ int run_tiny(Matrix* mats, int count, const Run& r) {
                  static_cast<int32_t>(m.m), groups, results, m.rate};
   }
   const dim3 grid(most, static_cast<unsigned>(count)), wide(most_results, static_cast<unsigned>(count));
-  hipStream_t s = r.stream;
-  const bool half = r.source == kPlain && r.src_dtype == QOPT_BF16;
-  if (half) hipLaunchKernelGGL(tiny_gram_kernel<uint16_t>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(tiny_gram_kernel<float>, grid, dim3(256), 0, s, a);
-  hipLaunchKernelGGL(tiny_polynomial_kernel, dim3(static_cast<unsigned>(count)), dim3(256), 0, s, a);
-  if (half && r.dst_dtype == QOPT_F32) launch_tiny_result<uint16_t, float>(a, r.update, wide, s);
-  else if (half) launch_tiny_result<uint16_t, uint16_t>(a, r.update, wide, s);
-  else if (r.dst_dtype == QOPT_F32) launch_tiny_result<float, float>(a, r.update, wide, s);
-  else launch_tiny_result<float, uint16_t>(a, r.update, wide, s);
+  for (int done = 0; done < r.steps; done += kTinySteps) {
+    a.steps = std::min(kTinySteps, r.steps - done);
+    a.scaled = done > 0;
+    const bool last = done + kTinySteps >= r.steps;
+    if (done > 0) {
+      for (int i = 0; i < count; ++i) a.jobs[i].u = mats[i].tiny_x;
+      launch_tiny<double>(a, mats, count, last, r, grid, wide);
+    } else if (r.source == kPlain && r.src_dtype == QOPT_BF16) {
+      launch_tiny<uint16_t>(a, mats, count, last, r, grid, wide);
+    } else {
+      launch_tiny<float>(a, mats, count, last, r, grid, wide);
+    }
+  }
   return launch_status();
 }
 
