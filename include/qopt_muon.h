@@ -15,12 +15,17 @@
  *
  * Precision.  Every value between the products is held as the sum of two binary16 numbers (22
  * bits) under a fixed power of two, and a product of two such values is three matrix instructions
- * with binary32 sums; the result is rounded once, to the destination's type.  Before that it is
- * 0.5 to 2 times as far off as products of binary32 numbers leave it: 7e-7 to 3e-5 of the result for
- * 64 x 64 to 4096 x 4096, least where one entry holds nearly all of the norm, most where the
- * singular values spread (5e-7 to 4e-5 with those); a bfloat16 result is as far from the exact
- * one as that one rounded, 1.66e-3, to three digits.  The values' power of two is that of the largest
- * possible one, so that what lies 2^-15 under it or further down is held to 2^-37 of it instead.
+ * with binary32 sums; the result is rounded once, to the destination's type.  After five iterations
+ * it is, before that, 0.5 to 2 times as far off as products of binary32 numbers leave it: 7e-7 to
+ * 3e-5 of the result for 64 x 64 to 4096 x 4096, least where one entry holds nearly all of the norm, most
+ * where the singular values spread (5e-7 to 4e-5 with those), and more where a few directions are
+ * all that there is (2e-4 and 4e-4 for one of 2048; 9e-4 and 1e-4 where that one is rows of equal
+ * values).  A bfloat16 result of the former is as far from the exact one as that one rounded,
+ * 1.66e-3, to three digits.  The values' power of two is that of the largest possible one, so that
+ * what lies 2^-15 under it or further down is held to 2^-37 of it instead: after 12 iterations rows whose
+ * sizes spread by e^9 are 2e-4 off, 1e-5 with products of binary32 numbers.  What rounding adds in
+ * directions that U does not have grows 3.4445 times per iteration, as in any such iteration, until
+ * it counts, after some 12; no singular value leaves 1.21.
  * Matrices of up to 32 rows or columns are iterated in binary64.
  *
  * Conventions are those of qopt.h (status codes, dtypes, *_dev pointers in device memory

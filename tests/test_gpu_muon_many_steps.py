@@ -90,3 +90,17 @@ def test_a_step_of_many_iterations(q):
     q.qopt_muon32bit_step([(p, g, m)], lr=1.0, momentum=0.0, weight_decay=0.0, nesterov=False, steps=13)
     assert torch.equal(p, -q.qopt_orthogonalize(g, steps=13))
     assert torch.equal(m, g)
+
+
+@pytest.mark.parametrize("rows,cols", [(33, 40), (100, 300), (300, 99), (700, 900)])
+def test_larger_matrices_stay_bounded(q, rows, cols):
+    """The same on the way of larger matrices, whose groups begin with A anew; 2^-8 for the destination's own rounding."""
+    rng = np.random.default_rng(rows)
+    one = np.repeat(rng.normal(size=(1, cols)), rows, 0)
+    steep = rng.normal(size=(rows, 2)) @ rng.normal(size=(2, cols)) * 1e6 + rng.normal(size=(rows, cols))
+    spread = rng.normal(size=(rows, cols)) * np.exp(3 * rng.normal(size=(rows, 1)))
+    for x in (one, steep, spread):
+        for steps in (12, 20, 32):
+            for dtype in (F32, BF16):
+                got = host(q.qopt_orthogonalize(torch.from_numpy(x.astype(np.float32)).cuda(), steps=steps, out_dtype=dtype))
+                assert np.isfinite(got).all() and np.linalg.norm(got, 2) <= 1.21 + 2.0 ** -8
